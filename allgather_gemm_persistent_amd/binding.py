@@ -23,11 +23,13 @@ LIB_PATH = os.path.join(PKG, "libagg.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "agg.h")
 
 AGG_OK, AGG_E_ARG, AGG_E_UNSUPPORTED, AGG_E_HIP, AGG_E_TIMEOUT, AGG_E_STATE = range(6)
-AGG_BF16, AGG_FP8_E4M3 = 0, 1
+AGG_BF16, AGG_FP8_E4M3, AGG_FP32 = 0, 1, 2
 AGG_OVERLAP, AGG_SERIAL, AGG_GEMM_ONLY, AGG_COPY_ONLY = range(4)
 MODES = {"overlap": AGG_OVERLAP, "serial": AGG_SERIAL, "gemm_only": AGG_GEMM_ONLY,
          "copy_only": AGG_COPY_ONLY}
-DTYPES = {"bf16": AGG_BF16, "fp8": AGG_FP8_E4M3}
+DTYPES = {"bf16": AGG_BF16, "fp8": AGG_FP8_E4M3, "fp32": AGG_FP32}
+SCORES = {"softmax": 0, "sigmoid": 1}
+PLAN_PAIRS = 1024
 MAX_ROW_TILES = 1024
 
 _c_int, _c_i64, _c_u32, _c_u64, _c_f32 = (ctypes.c_int, ctypes.c_int64, ctypes.c_uint32,
@@ -85,6 +87,25 @@ _SIGNATURES = {
                            ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _i32p, _c_int, _c_int, _vp, _vp],
     "agg_a2a_row_tile_order": [_c_int, _c_int, _c_i64, _c_int, _i32p, _i32p, _c_int, _c_int, _i32p,
                                _c_int, ctypes.POINTER(_c_int)],
+    "rms_norm": [_vp, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_f32, _c_int,
+                 _vp, _c_i64, _vp, _c_f32, _vp],
+    "quant_rows": [_vp, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _c_f32, _vp],
+    "moe_route": [_vp, _c_i64, _c_int, _c_int, _c_int, _vp, _c_i64, _vp, _c_int, _c_int, _c_int, _c_int,
+                  _c_f32, _vp, _vp, _vp],
+    "moe_plan": [_vp, _c_i64, _c_int, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp],
+    "moe_gemm": [_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_int, _c_i64, _vp, _c_i64, _vp, _vp, _vp,
+                 _vp, _vp, _vp, _vp],
+    "moe_combine": [_vp, _c_i64, _c_int, _c_i64, _c_i64, _vp, _vp, _vp, _c_int, _vp, _vp],
+    "agg_check_norm_args": [_c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_f32,
+                            _c_int, _vp, _c_i64, _vp, _c_f32],
+    "agg_check_route_args": [_c_i64, _c_int, _c_int, _c_int, _vp, _c_i64, _c_int, _c_int, _c_int, _c_f32,
+                             _vp, _vp],
+    "agg_check_plan_args": [_c_i64, _c_int, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp],
+    "agg_check_moe_gemm_args": [_c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_int, _c_i64, _vp, _c_i64, _vp,
+                                _vp, _vp, _vp, _vp, _vp],
+    "agg_check_combine_args": [_c_i64, _c_int, _c_i64, _c_i64, _vp, _vp, _vp, _c_int, _vp],
+    "agg_moe_gemm_shape": [_c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_int, ctypes.POINTER(_c_int),
+                           ctypes.POINTER(_c_int), ctypes.POINTER(_c_int)],
     "agg_check_ag_args": [_c_int, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_f32, _c_f32,
                           ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _i32p, _c_int, _c_int, _vp, _vp],
     "agg_check_rs_args": [_c_int, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _vp, _vp, _vp, _vp,
@@ -534,3 +555,126 @@ def agg_kernel_regs(op: int, dtype, bm: int, bn: int):
     g, c = _c_int(), _c_int()
     _call("agg_kernel_regs", op, _dtype(dtype), bm, bn, ctypes.byref(g), ctypes.byref(c))
     return g.value, c.value
+
+
+# ------------------------------------------------------------------------------ mixture of experts
+
+_TENSOR_DTYPES = {torch.bfloat16: AGG_BF16, torch.float8_e4m3fn: AGG_FP8_E4M3, torch.float32: AGG_FP32}
+
+
+def _tensor_dtype(x, what):
+    """The library's dtype of a tensor."""
+    try:
+        return _TENSOR_DTYPES[x.dtype]
+    except (KeyError, AttributeError):
+        raise AggError(AGG_E_ARG, what, "must be a bfloat16, float8_e4m3fn or float32 tensor") from None
+
+
+def _rows(x, rows, cols, what, dtype=None):
+    """(pointer, elements from one row to the next) of a rows x cols tensor whose columns are
+    contiguous; (None, 0) for None."""
+    if x is None:
+        return None, 0
+    if x.dim() != 2 or x.shape[1] != cols or x.shape[0] < rows:
+        raise AggError(AGG_E_ARG, what, f"has shape {tuple(x.shape)}, the call takes {rows} x {cols}")
+    if dtype is not None and x.dtype != dtype:
+        raise AggError(AGG_E_ARG, what, f"is {x.dtype}, not {dtype}")
+    if cols > 1 and x.stride(1) != 1:
+        raise AggError(AGG_E_ARG, what, "must have contiguous columns")
+    if not x.is_cuda and x.numel():
+        raise AggError(AGG_E_ARG, what, f"must be a device tensor, got {x.device}")
+    # (a single row, or none, may carry any stride)
+    return x.data_ptr(), x.stride(0) if rows > 1 else max(cols, x.stride(0))
+
+
+def _flat(x, count, what, dtype):
+    """The pointer of a contiguous tensor of at least `count` elements; None for None."""
+    if x is None:
+        return None
+    if x.dtype != dtype:
+        raise AggError(AGG_E_ARG, what, f"is {x.dtype}, not {dtype}")
+    if not x.is_contiguous() or x.numel() < count:
+        raise AggError(AGG_E_ARG, what, f"must be contiguous and hold {count} elements, has {x.numel()}")
+    if not x.is_cuda and count:
+        raise AggError(AGG_E_ARG, what, f"must be a device tensor, got {x.device}")
+    return x.data_ptr()
+
+
+def rms_norm(ctx, rows: int, cols: int, x, weight, out, *, residual=None, residual_out=None, eps: float = 1e-6,
+             scales=None, scale: float = 1.0, stream=None) -> None:
+    """out = norm(x + residual) * weight as bf16, or as fp8 with a scale per row (written to
+    `scales`) or the given `scale`; residual_out = bf16(x + residual)."""
+    px, lx = _rows(x, rows, cols, "x")
+    pr, lr = _rows(residual, rows, cols, "residual", torch.bfloat16)
+    po, lo = _rows(residual_out, rows, cols, "residual_out", torch.bfloat16)
+    pd, ld = _rows(out, rows, cols, "out")
+    _call("rms_norm", ctx, rows, cols, _tensor_dtype(x, "x"), px, lx, pr, lr, po, lo,
+          _flat(weight, cols, "weight", torch.bfloat16), eps, _tensor_dtype(out, "out"), pd, ld,
+          _flat(scales, rows, "scales", torch.float32), scale, _stream(stream))
+
+
+def quant_rows(ctx, rows: int, cols: int, x, out, *, scales=None, scale: float = 1.0, stream=None) -> None:
+    """out = fp8 of x with a scale per row (written to `scales`) or the given `scale`."""
+    px, lx = _rows(x, rows, cols, "x")
+    pd, ld = _rows(out, rows, cols, "out", torch.float8_e4m3fn)
+    _call("quant_rows", ctx, rows, cols, _tensor_dtype(x, "x"), px, lx, pd, ld,
+          _flat(scales, rows, "scales", torch.float32), scale, _stream(stream))
+
+
+def moe_route(ctx, tokens: int, experts: int, top_k: int, logits, ids, weights, *, score="softmax", bias=None,
+              groups: int = 1, top_groups: int = 1, renorm: bool = True, scale: float = 1.0, stream=None) -> None:
+    """The experts (`ids`) and weights each token takes, from its logits."""
+    px, lx = _rows(logits, tokens, experts, "logits")
+    _call("moe_route", ctx, tokens, experts, top_k, _tensor_dtype(logits, "logits"), px, lx,
+          _flat(bias, experts, "bias", torch.float32), SCORES[score] if isinstance(score, str) else int(score),
+          groups, top_groups, int(renorm), scale, _flat(ids, tokens * top_k, "ids", torch.int32),
+          _flat(weights, tokens * top_k, "weights", torch.float32), _stream(stream))
+
+
+def moe_plan_words(tokens: int, top_k: int, n_local: int) -> int:
+    """Elements of moe_plan's `work`."""
+    return (tokens * top_k // PLAN_PAIRS + 1) * (n_local + 1)
+
+
+def moe_plan(ctx, tokens: int, top_k: int, ids, first: int, n_local: int, offsets, slot_token, token_slot, work, *,
+             stream=None) -> None:
+    """The (token, choice) pairs of experts [first, first + n_local) sorted by expert."""
+    pairs = tokens * top_k
+    i32 = torch.int32
+    _call("moe_plan", ctx, tokens, top_k, _flat(ids, pairs, "ids", i32), first, n_local,
+          _flat(offsets, n_local + 1, "offsets", i32), _flat(slot_token, pairs, "slot_token", i32),
+          _flat(token_slot, pairs, "token_slot", i32),
+          _flat(work, moe_plan_words(tokens, top_k, n_local), "work", i32), _stream(stream))
+
+
+def moe_gemm(ctx, slots: int, n_experts: int, n: int, k: int, dtype, a, b, offsets, out, *, gated: bool = False,
+             slot_token=None, a_scale=None, b_scale=None, stream=None) -> None:
+    """out[s] = A[slot_token[s] or s] @ B[e] for the slots of each expert e; gated: B holds the gate's
+    and the up projection's columns side by side and out = silu(gate) * up."""
+    dt = _dtype(dtype)
+    el = torch.float8_e4m3fn if dt == AGG_FP8_E4M3 else torch.bfloat16
+    a_rows = a.shape[0] if a.dim() == 2 else -1
+    cols = 2 * n if gated else n
+    pa, la = _rows(a, a_rows, k, "a", el)
+    _call("moe_gemm", ctx, slots, n_experts, n, k, dt, int(gated), a_rows, pa, la,
+          _flat(a_scale, a_rows, "a_scale", torch.float32), _flat(slot_token, slots, "slot_token", torch.int32),
+          _flat(b, n_experts * k * cols, "b", el), _flat(b_scale, n_experts * cols, "b_scale", torch.float32),
+          _flat(offsets, n_experts + 1, "offsets", torch.int32), _flat(out, slots * n, "out", torch.bfloat16),
+          _stream(stream))
+
+
+def moe_combine(ctx, tokens: int, top_k: int, n: int, slots: int, y, token_slot, weights, out, *, stream=None) -> None:
+    """out[t] = sum over a token's choices of weight * y[slot], as bf16 or fp32."""
+    pairs = tokens * top_k
+    dt = _tensor_dtype(out, "out")
+    _call("moe_combine", ctx, tokens, top_k, n, slots, _flat(y, slots * n, "y", torch.bfloat16),
+          _flat(token_slot, pairs, "token_slot", torch.int32), _flat(weights, pairs, "weights", torch.float32), dt,
+          _flat(out, tokens * n, "out", out.dtype), _stream(stream))
+
+
+def agg_moe_gemm_shape(dtype, slots: int, n_experts: int, n: int, k: int, gated: bool = False):
+    """How moe_gemm multiplies: ("stream", rows at a time) or ("tiles", (bm, bn))."""
+    rows, bm, bn = _c_int(), _c_int(), _c_int()
+    _call("agg_moe_gemm_shape", _dtype(dtype), slots, n_experts, n, k, int(gated), ctypes.byref(rows),
+          ctypes.byref(bm), ctypes.byref(bn))
+    return ("stream", rows.value) if rows.value else ("tiles", (bm.value, bn.value))

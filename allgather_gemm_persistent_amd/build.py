@@ -14,6 +14,7 @@ import re
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +22,10 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libagg.so")
 ARCH = "gfx950"
 
-SOURCES = ["plan.cpp", "host.hip", "kernels.hip"]
+SOURCES = ["plan.cpp", "moe.cpp", "host.hip", "moe_host.hip", "kernels.hip", "experts.hip", "rows.hip", "route.hip"]
+# sources with GEMM kernel instantiations, whose accumulators are checked; kernels.resources.txt and
+# experts.resources.txt in _build hold the compiler's remarks
+GEMM_SOURCES = ("kernels.hip", "experts.hip")
 
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
@@ -82,41 +86,45 @@ def accumulator_problems(resources: dict) -> list:
     return problems
 
 
+def _compile(src: str, out_dir: str, verbose: bool) -> str:
+    """Compile one source; returns the object's path."""
+    obj = os.path.join(out_dir, src + ".o")
+    cmd = [hipcc(), *HIP_FLAGS, "-I", os.path.join(ROOT, "include"), "-c",
+           os.path.join(CSRC, src), "-o", obj]
+    if src in GEMM_SOURCES:
+        cmd.append("-Rpass-analysis=kernel-resource-usage")
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, stderr=subprocess.PIPE, text=True)
+    remarks = [l for l in r.stderr.splitlines() if "kernel-resource-usage" in l]
+    # (the remarks' own source excerpts: "  749 | __global__ ..." and "      | ^")
+    rest = "\n".join(l for l in r.stderr.splitlines()
+                     if "kernel-resource-usage" not in l and not re.match(r"^\s*\d*\s*\|", l))
+    if rest.strip():
+        print(rest, file=sys.stderr, flush=True)
+    if r.returncode != 0:
+        raise subprocess.CalledProcessError(r.returncode, cmd)
+    if src in GEMM_SOURCES:
+        text = "\n".join(remarks) + "\n"
+        with open(os.path.join(out_dir, src.replace(".hip", ".resources.txt")), "w") as f:
+            f.write(text)
+        res = kernel_resources(text)
+        if not any(_GEMM_KERNEL.fullmatch(n) for n in res):
+            raise RuntimeError("no resource remarks for the GEMM kernels")
+        bad = accumulator_problems(res)
+        if bad:
+            raise RuntimeError("accumulators outside the AGPRs: " + "; ".join(bad))
+    return obj
+
+
 def build(verbose: bool = True) -> str:
-    """Compile every source and link libagg.so next to this file. Returns its path. The kernel
-    source is compiled with the compiler's resource remarks (kept in _build/kernels.resources.txt);
-    a GEMM kernel whose accumulators do not fit its AGPRs fails the build."""
+    """Compile every source and link libagg.so next to this file. Returns its path. The sources of
+    GEMM kernels are compiled with the compiler's resource remarks (kept in _build); a GEMM kernel
+    whose accumulators do not fit its AGPRs fails the build."""
     out_dir = os.path.join(ROOT, "_build")
     os.makedirs(out_dir, exist_ok=True)
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(out_dir, src + ".o")
-        cmd = [hipcc(), *HIP_FLAGS, "-I", os.path.join(ROOT, "include"), "-c",
-               os.path.join(CSRC, src), "-o", obj]
-        if src == "kernels.hip":
-            cmd.append("-Rpass-analysis=kernel-resource-usage")
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, stderr=subprocess.PIPE, text=True)
-        remarks = [l for l in r.stderr.splitlines() if "kernel-resource-usage" in l]
-        # (the remarks' own source excerpts: "  749 | __global__ ..." and "      | ^")
-        rest = "\n".join(l for l in r.stderr.splitlines()
-                         if "kernel-resource-usage" not in l and not re.match(r"^\s*\d*\s*\|", l))
-        if rest.strip():
-            print(rest, file=sys.stderr, flush=True)
-        if r.returncode != 0:
-            raise subprocess.CalledProcessError(r.returncode, cmd)
-        if src == "kernels.hip":
-            text = "\n".join(remarks) + "\n"
-            with open(os.path.join(out_dir, "kernels.resources.txt"), "w") as f:
-                f.write(text)
-            res = kernel_resources(text)
-            if not any(_GEMM_KERNEL.fullmatch(n) for n in res):
-                raise RuntimeError("no resource remarks for the GEMM kernels")
-            bad = accumulator_problems(res)
-            if bad:
-                raise RuntimeError("accumulators outside the AGPRs: " + "; ".join(bad))
-        objs.append(obj)
+    with ThreadPoolExecutor(max_workers=4) as pool:
+        objs = list(pool.map(lambda src: _compile(src, out_dir, verbose), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs,
            "-Wl,-rpath,/opt/rocm/lib"]

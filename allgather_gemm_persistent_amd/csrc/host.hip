@@ -719,6 +719,13 @@ extern "C" int agg_ctx_create(int device, agg_ctx** out) {
   return AGG_OK;
 }
 
+namespace agg {
+
+int ctx_units(const agg_ctx* ctx) { return ctx->cus; }
+int ctx_device(const agg_ctx* ctx) { return ctx->device; }
+
+}  // namespace agg
+
 extern "C" int agg_ctx_destroy(agg_ctx* ctx) {
   clear_error();
   if (!ctx) return AGG_OK;

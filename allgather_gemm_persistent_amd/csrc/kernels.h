@@ -28,7 +28,9 @@ constexpr int kScrLocal = kScrSplit + 1024;  // RS: local tiles stored, per row 
 constexpr int kScrWords = kScrLocal + AGG_MAX_ROW_TILES;
 constexpr int kMaxLists = 16;
 
-enum Epilogue { kEpiAllGather = 0, kEpiReduceScatter = 1, kEpiAllReduce = 2, kEpiFfn = 3 };
+constexpr int kXcds = 8;           // accelerator dies of an MI355X, each with its own L2
+
+enum Epilogue { kEpiAllGather = 0, kEpiReduceScatter = 1, kEpiAllReduce = 2, kEpiFfn = 3, kEpiExperts = 4 };
 
 // One set of copy jobs of the in-kernel producer: job i*pieces + q of the set moves piece q of the
 // i-th arriving chunk from its peer's block into the symmetric buffer; the job completing a chunk
@@ -45,6 +47,18 @@ struct CopySet {
   int cps;                              // chunks per peer block
   int order_off;                        // its arrival order: scratch[kScrOrder + order_off + i]
   int piece_off;                        // its piece counters: scratch[kScrPieces + piece_off + chunk]
+};
+
+// The experts' products (kEpiExperts): expert e multiplies slots [offsets[e], offsets[e+1]).
+struct ExpertArgs {
+  const int32_t* offsets;     // n_experts + 1
+  const int32_t* slot_token;  // slot -> row of A, or null: slot s is row s of A
+  const float* a_scale;       // fp8: per row of A
+  const float* b_scale;       // fp8: n_experts x N, per column of B
+  int64_t slots;              // rows of the output
+  int64_t a_rows, a_stride;   // rows of A and the bytes from one to the next
+  int n_experts;
+  int gated;                  // B = [gate | up], out = silu(A gate) * (A up)
 };
 
 struct GemmArgs {
@@ -116,6 +130,9 @@ struct GemmArgs {
   int64_t K1, N1;
   int chunk_rows1, cps1;
   int n_row_tiles1, n_col_tiles1;
+  // experts' products (kEpiExperts): `a` rows taken through x, `b` n_experts x K x N, `c` slots x
+  // N (gated: N/2) bfloat16
+  ExpertArgs x;
 };
 
 // Launch the persistent kernel instantiated for (bm, bn, dtype, epilogue) with `grid`

@@ -6,6 +6,8 @@
 #include <string>
 #include <vector>
 
+#include "../../include/agg.h"
+
 namespace agg {
 
 // Thread-local error text behind agg_last_error(); returns `code` for chaining.
@@ -74,5 +76,20 @@ std::vector<int32_t> ring_order(int world, int rank, int chunks_per_shard);
 
 // Checks that `order` holds each remote chunk id exactly once. Returns AGG_OK or AGG_E_ARG.
 int check_order(int world, int rank, int chunks_per_shard, const int32_t* order, int n_order);
+
+// The ctx's compute units and HIP device.
+int ctx_units(const agg_ctx* ctx);
+int ctx_device(const agg_ctx* ctx);
+
+// Relative MFMA efficiency of a tile shape (256 x 256: 1).
+double tile_eff(const TileShape& s);
+
+// How moe_gemm multiplies: row_blocks > 0: the streaming kernel, 16 * row_blocks rows at a time;
+// otherwise tiles of bm x bn.
+struct ExpertShape {
+  int row_blocks;
+  TileShape tile;
+};
+ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t cols, int64_t k, int units);
 
 }  // namespace agg

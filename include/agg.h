@@ -69,7 +69,8 @@ enum agg_status {
 
 enum agg_dtype {
   AGG_BF16 = 0,           /* bfloat16 operands */
-  AGG_FP8_E4M3 = 1        /* OCP float8 E4M3 ("fn": max 448, no inf) operands, per-tensor scales */
+  AGG_FP8_E4M3 = 1,       /* OCP float8 E4M3 ("fn": max 448, no inf) operands, per-tensor scales */
+  AGG_FP32 = 2            /* float32: rows of rms_norm, quant_rows, moe_route and moe_combine only */
 };
 
 enum agg_mode {
@@ -85,6 +86,12 @@ enum agg_mode {
 #define AGG_MAX_WORLD 8           /* emulated ranks */
 #define AGG_MAX_ROW_TILES 1024    /* row tiles of the output per call */
 #define AGG_MAX_CHUNKS 4096       /* world * chunks per shard (or per block) */
+
+#define AGG_MAX_EXPERTS 1024      /* experts of a routing, and experts multiplied by one call */
+#define AGG_MAX_GROUPS 64         /* expert groups of a routing */
+#define AGG_MAX_TOP_K 16          /* experts a token takes */
+#define AGG_MAX_NORM_COLS 32768   /* columns of rms_norm and quant_rows */
+#define AGG_PLAN_PAIRS 1024       /* (token, choice) pairs a block of moe_plan sorts */
 
 /* ---- context -------------------------------------------------------------------------- */
 
@@ -510,6 +517,116 @@ int ffn_chain(agg_ctx* ctx, int world, int rank, int64_t m_shard, int64_t k1, in
  */
 int agg_ctx_set_chain_fused(agg_ctx* ctx, int on);
 
+/* ---- A mixture-of-experts layer: norm, routing, experts' products, combine ----------------
+ *
+ * What a routed FFN needs beside the collectives: the rows that gemm_ar or gemm_rs leave are
+ * normalised (rms_norm), a router's logits (ag_gemm's product, or any) become choices and weights
+ * (moe_route), the choices that fall on this rank's experts become groups of rows (moe_plan),
+ * every group is multiplied by its expert's weight (moe_gemm), and the choices' results are summed
+ * back to tokens (moe_combine). They are forward operators, like the others here.
+ *
+ * Every call launches on `stream` alone (one kernel; moe_plan two beyond 1024 pairs), is
+ * capturable, allocates nothing and keeps nothing in the ctx, which names the device: calls on
+ * several streams do not meet. Strides `ld_*` are elements from one row to the next. Device arrays
+ * are 16-byte aligned unless stated. None of the results depends on timing: no floating-point
+ * atomics.
+ * Passage: section "DITRON adds three levels of tiling" (AllToAll among the collectives, whose
+ *  delivered tokens these operators route and multiply); the operators' formulas are the plain
+ *  definitions stated here, the pages give none.
+ */
+
+/* Residual addition and root-mean-square norm of `rows` rows of `cols`:
+ *   s = x + residual (fp32); residual_out = bf16(s);
+ *   y = s * rsqrt(sum(s^2)/cols + eps) * weight, out = bf16(y) or e4m3 of y over a scale.
+ *   x, x_dtype       rows x cols, AGG_BF16 or AGG_FP32 (what gemm_ar and gemm_rs write)
+ *   residual         bf16 rows, or NULL (s = x); residual_out: bf16 rows, or NULL (not stored; it
+ *                    must be NULL without a residual). y is computed from the unrounded s
+ *   weight           bf16[cols]
+ *   out, out_dtype   AGG_BF16, or AGG_FP8_E4M3: with `scales` (fp32[rows], 4-byte aligned) row r is
+ *                    e4m3(y / scales[r]) with scales[r] = max|y| / 448 written by the call (1 for a
+ *                    row of zeros or one that holds a NaN); with scales NULL, e4m3(y / scale) for
+ *                    the given scale (> 0), values beyond +-448 saturating: the operand of an fp8
+ *                    ag_gemm with scale_a = scale. A NaN stays a NaN
+ * cols and the strides are multiples of 8, row starts of x and the residuals of 16 bytes; cols at
+ * most AGG_MAX_NORM_COLS. residual_out may be residual or a bf16 x, out may be x, at equal strides
+ * and types (each row is read before it is written).
+ */
+int rms_norm(agg_ctx* ctx, int64_t rows, int64_t cols, int x_dtype, const void* x, int64_t ld_x,
+             const void* residual, int64_t ld_residual, void* residual_out, int64_t ld_residual_out,
+             const void* weight, float eps, int out_dtype, void* out, int64_t ld_out, float* scales,
+             float scale, agg_stream stream);
+
+/* The 8-bit output of rms_norm without the norm: out = e4m3(x / scale), scales as there. What an
+ * fp8 moe_gemm needs of the bf16 rows that another one wrote.
+ */
+int quant_rows(agg_ctx* ctx, int64_t rows, int64_t cols, int x_dtype, const void* x, int64_t ld_x,
+               void* out, int64_t ld_out, float* scales, float scale, agg_stream stream);
+
+/* Scores of a router. */
+enum { AGG_SCORE_SOFTMAX = 0, AGG_SCORE_SIGMOID = 1 };
+
+/* The experts each token takes and their weights, from the router's logits (tokens x experts,
+ * AGG_BF16 or AGG_FP32; element-aligned).
+ *   An expert is a candidate unless its logit is -inf or NaN (a disabled expert, a padded token).
+ *   p  = softmax over the candidates, or 1/(1 + exp(-x)); the key that ranks them is p + bias
+ *   bias: fp32[experts], or NULL; it enters the key alone. (Without it softmax ranks by the logit,
+ *   the same order.)
+ *   groups > 1: the experts are `groups` runs of experts/groups; a group's score is its largest key
+ *   (softmax) or the sum of its two largest (sigmoid); only the top_groups best groups' experts
+ *   stay candidates.
+ *   ids[t, j], weights[t, j], j < top_k: the candidates by descending key, ties (experts and
+ *   groups) to the lowest index; weight = p * scale, with renorm p over the sum of the chosen p.
+ *   Where fewer than top_k candidates are left: id -1 and weight 0.
+ */
+int moe_route(agg_ctx* ctx, int64_t tokens, int experts, int top_k, int logits_dtype,
+              const void* logits, int64_t ld, const float* bias, int score, int groups,
+              int top_groups, int renorm, float scale, int32_t* ids, float* weights,
+              agg_stream stream);
+
+/* The plan of a routing for the rank that holds experts [first, first + n_local): the (token,
+ * choice) pairs whose expert is held, sorted by expert, pairs of one expert in their order (token,
+ * then choice). A pair's place is its slot.
+ *   ids              int32[tokens * top_k]; any id outside the held range is another rank's or none
+ *   offsets          int32[n_local + 1]: expert e's slots are [offsets[e], offsets[e+1])
+ *   slot_token       int32[tokens * top_k]: the token of each slot, -1 past the last slot
+ *   token_slot       int32[tokens * top_k]: the slot of each pair, -1 if it has none
+ *   work             int32[(tokens * top_k / AGG_PLAN_PAIRS + 1) * (n_local + 1)] scratch
+ */
+int moe_plan(agg_ctx* ctx, int64_t tokens, int top_k, const int32_t* ids, int first, int n_local,
+             int32_t* offsets, int32_t* slot_token, int32_t* token_slot, int32_t* work,
+             agg_stream stream);
+
+/* The experts' products: out[s] = A[row of s] @ B[e] for every slot s in [offsets[e],
+ * offsets[e+1]), e < n_experts; with `gated`, out[s] = silu(A B_gate) * (A B_up), silu(v) =
+ * v / (1 + exp(-v)). One launch for all experts.
+ *   slots            rows of `out`; offsets (device int32[n_experts + 1], ascending, kept inside
+ *                    [0, slots]) says on the device how many each expert has. Rows past the last
+ *                    offset are left alone
+ *   n, k             columns of out, contraction length; dtype: AGG_BF16 or AGG_FP8_E4M3
+ *   a, a_rows, ld_a  a_rows x k; slot s reads row slot_token[s] (a row outside [0, a_rows) counts
+ *                    as zeros), or, with slot_token NULL, row s (a_rows >= slots)
+ *   b                n_experts x k x n, N contiguous as everywhere here; gated: n_experts x k x 2n,
+ *                    a row holding the n gate columns and then the n up columns
+ *   a_scale          fp8: fp32[a_rows]; b_scale: fp32[n_experts, columns of b]: each row and each
+ *                    column of the product times its scale. Both ignored for bf16
+ *   out              slots x n bf16, rounded once from the fp32 product
+ * Limits: k * elem, n * elem and n * 2 bytes multiples of 16, one expert's weight below 2 GiB, and
+ * with slot_token A below 2 GiB.
+ */
+int moe_gemm(agg_ctx* ctx, int64_t slots, int n_experts, int64_t n, int64_t k, int dtype, int gated,
+             int64_t a_rows, const void* a, int64_t ld_a, const float* a_scale,
+             const int32_t* slot_token, const void* b, const float* b_scale, const int32_t* offsets,
+             void* out, agg_stream stream);
+
+/* The experts' results back to tokens: out[t] = sum over j < top_k, ascending, of
+ * weights[t, j] * y[token_slot[t, j]] in fp32; a pair without a slot in [0, slots) adds nothing
+ * (a token without any gets zeros).
+ *   y                slots x n bf16; out: tokens x n, AGG_BF16 or AGG_FP32 (a rank's partial sum)
+ */
+int moe_combine(agg_ctx* ctx, int64_t tokens, int top_k, int64_t n, int64_t slots, const void* y,
+                const int32_t* token_slot, const float* weights, int out_dtype, void* out,
+                agg_stream stream);
+
 /* ---- host-only planning (no device needed; used by the calls above) --------------------- */
 
 /* The tile shape the library uses for a call: *bm x *bn output tiles.
@@ -589,6 +706,33 @@ int agg_check_ar_args(int world, int rank, int64_t m, int64_t n, int64_t k, int 
                       const float* const* peer_src, const void* recv, const void* flags,
                       const void* out, const int32_t* order, int n_order, int mode,
                       agg_stream stream, agg_stream copy_stream);
+
+/* The argument checks of rms_norm / quant_rows, moe_route, moe_plan, moe_gemm and moe_combine, run
+ * by them first.
+ */
+int agg_check_norm_args(int64_t rows, int64_t cols, int x_dtype, const void* x, int64_t ld_x,
+                        const void* residual, int64_t ld_residual, const void* residual_out,
+                        int64_t ld_residual_out, const void* weight, float eps, int out_dtype,
+                        const void* out, int64_t ld_out, const float* scales, float scale);
+int agg_check_route_args(int64_t tokens, int experts, int top_k, int logits_dtype,
+                         const void* logits, int64_t ld, int score, int groups, int top_groups,
+                         float scale, const int32_t* ids, const float* weights);
+int agg_check_plan_args(int64_t tokens, int top_k, const int32_t* ids, int first, int n_local,
+                        const int32_t* offsets, const int32_t* slot_token,
+                        const int32_t* token_slot, const int32_t* work);
+int agg_check_moe_gemm_args(int64_t slots, int n_experts, int64_t n, int64_t k, int dtype,
+                            int gated, int64_t a_rows, const void* a, int64_t ld_a,
+                            const float* a_scale, const int32_t* slot_token, const void* b,
+                            const float* b_scale, const int32_t* offsets, const void* out);
+int agg_check_combine_args(int64_t tokens, int top_k, int64_t n, int64_t slots, const void* y,
+                           const int32_t* token_slot, const float* weights, int out_dtype,
+                           const void* out);
+
+/* How moe_gemm multiplies a call on a whole MI355X: *stream_rows rows at a time with the weights
+ * streamed through registers (then *bm = *bn = 0), or, with *stream_rows 0, tiles of *bm x *bn.
+ */
+int agg_moe_gemm_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated,
+                       int* stream_rows, int* bm, int* bn);
 
 /* ---- diagnostics ---------------------------------------------------------------------- */
 
