@@ -1,0 +1,172 @@
+"""The mixture-of-experts operators' host side, without a GPU: the argument checks' codes, the choice
+of the experts' kernel, and the binding's own checks."""
+
+import ctypes
+
+import pytest
+import torch
+
+from allgather_gemm_persistent_amd import binding as B
+
+FAKE = 1 << 20          # an aligned non-NULL address (never dereferenced by the checks)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return B.load()
+
+
+def _norm(lib, **kw):
+    d = dict(rows=16, cols=64, xd=B.AGG_BF16, x=FAKE, lx=64, r=FAKE, lr=64, ro=FAKE, lro=64, w=FAKE, eps=1e-6,
+             od=B.AGG_BF16, out=FAKE, lo=64, scales=None, scale=1.0)
+    d.update(kw)
+    return lib.agg_check_norm_args(*d.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(rows=0, x=None, out=None), dict(cols=0, lx=0), dict(r=None, ro=None), dict(ro=None),
+    dict(xd=B.AGG_FP32), dict(od=B.AGG_FP8_E4M3), dict(od=B.AGG_FP8_E4M3, scales=FAKE, scale=0.0), dict(eps=0.0),
+    dict(lx=72, lr=80, lro=88, lo=96), dict(od=B.AGG_FP8_E4M3, lo=72), dict(cols=32768, lx=32768, lr=32768, lro=32768, lo=32768)])
+def test_norm_args_ok(lib, kw):
+    assert _norm(lib, **kw) == B.AGG_OK
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), B.AGG_E_ARG), (dict(cols=-8), B.AGG_E_ARG), (dict(cols=60), B.AGG_E_ARG),
+    (dict(xd=B.AGG_FP8_E4M3), B.AGG_E_ARG), (dict(od=B.AGG_FP32), B.AGG_E_ARG), (dict(eps=-1.0), B.AGG_E_ARG),
+    (dict(eps=float("nan")), B.AGG_E_ARG), (dict(od=B.AGG_FP8_E4M3, scale=0.0), B.AGG_E_ARG),
+    (dict(od=B.AGG_FP8_E4M3, scale=float("inf")), B.AGG_E_ARG), (dict(r=None), B.AGG_E_ARG), (dict(x=None), B.AGG_E_ARG),
+    (dict(out=None), B.AGG_E_ARG), (dict(x=FAKE + 2), B.AGG_E_ARG), (dict(w=FAKE + 8), B.AGG_E_ARG),
+    (dict(r=FAKE + 4), B.AGG_E_ARG), (dict(ro=FAKE + 4), B.AGG_E_ARG), (dict(lx=63), B.AGG_E_ARG),
+    (dict(lx=68), B.AGG_E_ARG), (dict(lr=56), B.AGG_E_ARG), (dict(lro=65), B.AGG_E_ARG), (dict(lo=60), B.AGG_E_ARG),
+    (dict(cols=32776, lx=32776), B.AGG_E_UNSUPPORTED), (dict(rows=(1 << 30) + 1), B.AGG_E_UNSUPPORTED)])
+def test_norm_args_rejected(lib, kw, code):
+    assert _norm(lib, **kw) == code
+    assert B.last_error()
+
+
+def _route(lib, **kw):
+    d = dict(tokens=4, experts=64, k=2, ld=B.AGG_FP32, logits=FAKE, stride=64, score=0, groups=1, top_groups=1,
+             scale=1.0, ids=FAKE, weights=FAKE)
+    d.update(kw)
+    return lib.agg_check_route_args(*d.values())
+
+
+def test_route_args_ok(lib):
+    for kw in (dict(), dict(tokens=0, logits=None), dict(experts=1, k=1), dict(experts=1024, k=16, stride=1024),
+               dict(groups=64, top_groups=2), dict(groups=8, top_groups=2, k=16), dict(score=1, ld=B.AGG_BF16), dict(scale=-2.5)):
+        assert _route(lib, **kw) == B.AGG_OK, kw
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=-1), B.AGG_E_ARG), (dict(experts=0), B.AGG_E_ARG), (dict(experts=1025, stride=1025), B.AGG_E_ARG),
+    (dict(k=0), B.AGG_E_ARG), (dict(k=17), B.AGG_E_ARG), (dict(experts=4, k=5), B.AGG_E_ARG),
+    (dict(groups=8, top_groups=1, k=9), B.AGG_E_ARG), (dict(groups=0), B.AGG_E_ARG), (dict(groups=3), B.AGG_E_ARG),
+    (dict(experts=1024, stride=1024, groups=128), B.AGG_E_ARG), (dict(groups=4, top_groups=5), B.AGG_E_ARG),
+    (dict(top_groups=0), B.AGG_E_ARG), (dict(score=2), B.AGG_E_ARG), (dict(ld=B.AGG_FP8_E4M3), B.AGG_E_ARG),
+    (dict(scale=float("nan")), B.AGG_E_ARG), (dict(stride=63), B.AGG_E_ARG), (dict(logits=None), B.AGG_E_ARG),
+    (dict(ids=None), B.AGG_E_ARG), (dict(weights=None), B.AGG_E_ARG), (dict(tokens=(1 << 30) + 1), B.AGG_E_UNSUPPORTED)])
+def test_route_args_rejected(lib, kw, code):
+    assert _route(lib, **kw) == code
+    assert B.last_error()
+
+
+def _plan(lib, **kw):
+    d = dict(tokens=10, k=2, ids=FAKE, first=0, n=8, offsets=FAKE, st=FAKE, ts=FAKE, work=FAKE)
+    d.update(kw)
+    return lib.agg_check_plan_args(*d.values())
+
+
+def test_plan_args(lib):
+    for kw in (dict(), dict(tokens=0, ids=None, st=None, ts=None, work=None), dict(first=100), dict(n=1024, k=16)):
+        assert _plan(lib, **kw) == B.AGG_OK, kw
+    for kw in (dict(tokens=-1), dict(k=0), dict(k=17), dict(first=-1), dict(n=0), dict(n=1025), dict(offsets=None),
+               dict(ids=None), dict(st=None), dict(ts=None), dict(work=None)):
+        assert _plan(lib, **kw) == B.AGG_E_ARG, kw
+    assert _plan(lib, tokens=1 << 30) == B.AGG_E_UNSUPPORTED
+
+
+def _gemm(lib, **kw):
+    d = dict(slots=32, e=8, n=64, k=128, dt=B.AGG_BF16, gated=0, rows=32, a=FAKE, la=128, sa=None, st=FAKE, b=FAKE,
+             sb=None, off=FAKE, out=FAKE)
+    d.update(kw)
+    return lib.agg_check_moe_gemm_args(*d.values())
+
+
+def test_gemm_args_ok(lib):
+    for kw in (dict(), dict(slots=0, a=None, b=None), dict(n=0), dict(gated=1), dict(st=None), dict(rows=1),
+               dict(la=136), dict(dt=B.AGG_FP8_E4M3, sa=FAKE, sb=FAKE), dict(e=1024),
+               dict(st=None, rows=1 << 20, slots=1 << 20, k=8192, la=8192)):
+        assert _gemm(lib, **kw) == B.AGG_OK, kw
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(slots=-1), B.AGG_E_ARG), (dict(n=-8), B.AGG_E_ARG), (dict(k=-8), B.AGG_E_ARG), (dict(rows=-1), B.AGG_E_ARG),
+    (dict(e=0), B.AGG_E_ARG), (dict(e=1025), B.AGG_E_ARG), (dict(dt=B.AGG_FP32), B.AGG_E_ARG), (dict(k=124), B.AGG_E_ARG),
+    (dict(n=60), B.AGG_E_ARG), (dict(k=0, la=0), B.AGG_E_ARG),
+    (dict(dt=B.AGG_FP8_E4M3, sa=FAKE, sb=FAKE, k=136, la=144), B.AGG_E_ARG),
+    (dict(dt=B.AGG_FP8_E4M3, sa=FAKE, sb=FAKE, n=72), B.AGG_E_ARG), (dict(dt=B.AGG_FP8_E4M3, sb=FAKE), B.AGG_E_ARG),
+    (dict(dt=B.AGG_FP8_E4M3, sa=FAKE), B.AGG_E_ARG), (dict(la=120), B.AGG_E_ARG), (dict(la=130), B.AGG_E_ARG),
+    (dict(rows=0), B.AGG_E_ARG), (dict(st=None, rows=31), B.AGG_E_ARG), (dict(a=None), B.AGG_E_ARG),
+    (dict(b=None), B.AGG_E_ARG), (dict(off=None), B.AGG_E_ARG), (dict(out=None), B.AGG_E_ARG),
+    (dict(a=FAKE + 8), B.AGG_E_ARG), (dict(b=FAKE + 2), B.AGG_E_ARG), (dict(out=FAKE + 2), B.AGG_E_ARG),
+    (dict(rows=1 << 20, k=8192, la=8192), B.AGG_E_UNSUPPORTED),
+    (dict(n=1 << 16, k=1 << 14, la=1 << 14), B.AGG_E_UNSUPPORTED),
+    (dict(n=1 << 15, k=1 << 14, la=1 << 14, gated=1), B.AGG_E_UNSUPPORTED)])
+def test_gemm_args_rejected(lib, kw, code):
+    assert _gemm(lib, **kw) == code
+    assert B.last_error()
+
+
+def test_combine_args(lib):
+    def call(**kw):
+        d = dict(tokens=4, k=2, n=64, slots=8, y=FAKE, ts=FAKE, w=FAKE, od=B.AGG_BF16, out=FAKE)
+        d.update(kw)
+        return lib.agg_check_combine_args(*d.values())
+    for kw in (dict(), dict(tokens=0, ts=None), dict(slots=0, y=None), dict(od=B.AGG_FP32), dict(k=16)):
+        assert call(**kw) == B.AGG_OK, kw
+    for kw in (dict(tokens=-1), dict(n=-8), dict(slots=-1), dict(k=0), dict(k=17), dict(n=60), dict(od=B.AGG_FP8_E4M3),
+               dict(y=None), dict(y=FAKE + 4), dict(ts=None), dict(w=None), dict(out=None), dict(out=FAKE + 8)):
+        assert call(**kw) == B.AGG_E_ARG, kw
+    assert call(tokens=(1 << 30) + 1) == B.AGG_E_UNSUPPORTED
+
+
+def test_a_call_without_a_ctx_or_weight_is_refused(lib):
+    assert lib.moe_plan(None, 10, 2, FAKE, 0, 8, FAKE, FAKE, FAKE, FAKE, None) == B.AGG_E_ARG
+    assert "ctx" in B.last_error()
+    assert lib.rms_norm(None, 1, 8, B.AGG_BF16, FAKE, 8, None, 0, None, 0, None, 1e-6, B.AGG_BF16, FAKE, 8, None, 1.0,
+                        None) == B.AGG_E_ARG
+    assert "weight" in B.last_error()
+
+
+def test_kernel_choice(lib):
+    """Few rows an expert stream; many take tiles no larger than the rows call for."""
+    assert B.agg_moe_gemm_shape("bf16", 1, 8, 3584, 8192) == ("stream", 16)
+    assert B.agg_moe_gemm_shape("bf16", 32, 8, 3584, 8192, gated=True)[0] == "stream"
+    kind, shape = B.agg_moe_gemm_shape("bf16", 10240, 8, 3584, 8192, gated=True)
+    assert kind == "tiles" and shape[0] == 256
+    kind, shape = B.agg_moe_gemm_shape("fp8", 16384, 8, 3584, 8192, gated=True)
+    assert kind == "tiles" and shape[0] == 256
+    # sizes without work still name a kernel
+    assert B.agg_moe_gemm_shape("fp8", 0, 1, 16, 16)[0] == "stream"
+    with pytest.raises(B.AggError):
+        B._call("agg_moe_gemm_shape", 0, 1, 1, 8, 8, 0, None, None, None)
+    assert ctypes.c_int is B._c_int
+
+
+def test_binding_refuses_what_the_call_would_read_wrongly(lib):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w = torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(B.AggError, match="device tensor"):
+        B.rms_norm(None, 4, 64, x, w, x)
+    with pytest.raises(B.AggError, match="shape"):
+        B.rms_norm(None, 5, 64, x, w, x)
+    with pytest.raises(B.AggError, match="contiguous columns"):
+        B.rms_norm(None, 64, 4, x.t(), w, x)
+    with pytest.raises(B.AggError, match="float16"):
+        B.quant_rows(None, 0, 64, x[:0].half(), x[:0].to(torch.float8_e4m3fn))
+    with pytest.raises(B.AggError, match="int32"):
+        B.moe_plan(None, 4, 2, torch.zeros(8, dtype=torch.int64), 0, 8, None, None, None, None)
+    with pytest.raises(B.AggError, match="contiguous and hold"):
+        B.moe_plan(None, 4, 2, torch.zeros(7, dtype=torch.int32), 0, 8, None, None, None, None)
+    assert B.moe_plan_words(512, 2, 7) == 16
