@@ -673,8 +673,8 @@ def moe_combine(ctx, tokens: int, top_k: int, n: int, slots: int, y, token_slot,
 
 
 def agg_moe_gemm_shape(dtype, slots: int, n_experts: int, n: int, k: int, gated: bool = False):
-    """How moe_gemm multiplies: ("stream", rows at a time) or ("tiles", (bm, bn))."""
-    rows, bm, bn = _c_int(), _c_int(), _c_int()
-    _call("agg_moe_gemm_shape", _dtype(dtype), slots, n_experts, n, k, int(gated), ctypes.byref(rows),
+    """How moe_gemm multiplies: ("stream", parts of K) or ("tiles", (bm, bn))."""
+    parts, bm, bn = _c_int(), _c_int(), _c_int()
+    _call("agg_moe_gemm_shape", _dtype(dtype), slots, n_experts, n, k, int(gated), ctypes.byref(parts),
           ctypes.byref(bm), ctypes.byref(bn))
-    return ("stream", rows.value) if rows.value else ("tiles", (bm.value, bn.value))
+    return ("stream", parts.value) if parts.value else ("tiles", (bm.value, bn.value))

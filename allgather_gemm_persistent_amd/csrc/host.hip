@@ -66,6 +66,7 @@ constexpr int kDefaultReservedCus = 32;
 // AGG_PULL_AUTO pulls gathers of at most this many remote bytes (latency-bound transfers)
 constexpr int64_t kPullMaxBytes = int64_t(4) << 20;
 constexpr int kTimingRing = 256;          // launches whose kernel duration is kept
+constexpr size_t kMoeWsStride = size_t(kMoeCounters) * 4 + size_t(kMoeWsBytes);
 
 enum FlagSlot { kFlagsAg = 0, kFlagsRsRecv = 1, kFlagsRsSend = 2, kFlagsArRecv = 3, kFlagsArSend = 4, kFlagSlots = 5 };
 
@@ -138,6 +139,10 @@ struct agg_ctx {
                                              //   counters are in the device's static scratch)
   hipEvent_t ev_upload = nullptr;
   bool upload_pending = false;
+  // moe_gemm's workspaces, each the counters and then the partial sums, and the streams they belong to
+  uint8_t* moe_ws = nullptr;
+  agg_stream moe_stream[kMoeWorkspaces] = {};
+  int moe_streams = 0;
 };
 
 namespace {
@@ -709,6 +714,9 @@ extern "C" int agg_ctx_create(int device, agg_ctx** out) {
   if (rc == AGG_OK) step(make_own_queue_stream(ctx, &ctx->ks), "hipExtStreamCreateWithCUMask");
   step(hipHostMalloc(reinterpret_cast<void**>(&ctx->up_host), kTabHostWords * sizeof(uint32_t)),
        "hipHostMalloc(tables)");
+  step(hipMalloc(reinterpret_cast<void**>(&ctx->moe_ws), kMoeWorkspaces * kMoeWsStride), "hipMalloc(moe workspaces)");
+  for (int j = 0; j < kMoeWorkspaces && rc == AGG_OK; ++j)
+    step(hipMemset(ctx->moe_ws + j * kMoeWsStride, 0, size_t(kMoeCounters) * 4), "hipMemset(moe counters)");
   if (rc == AGG_OK) rc = static_scratch_setup(device);
   step(hipSetDevice(prev), "hipSetDevice");
   if (rc != AGG_OK) {
@@ -723,6 +731,17 @@ namespace agg {
 
 int ctx_units(const agg_ctx* ctx) { return ctx->cus; }
 int ctx_device(const agg_ctx* ctx) { return ctx->device; }
+bool ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, float** ws, uint32_t** counts) {
+  int i = 0;
+  while (i < ctx->moe_streams && ctx->moe_stream[i] != stream) ++i;
+  if (i == kMoeWorkspaces) return false;
+  if (i == ctx->moe_streams) ctx->moe_stream[ctx->moe_streams++] = stream;
+  uint8_t* const p = ctx->moe_ws + i * kMoeWsStride;
+  *counts = reinterpret_cast<uint32_t*>(p);
+  *ws = reinterpret_cast<float*>(p + size_t(kMoeCounters) * 4);
+  return true;
+}
+TileShape ctx_forced_tile(const agg_ctx* ctx) { return TileShape{ctx->force_bm, ctx->force_bn}; }
 
 }  // namespace agg
 
@@ -743,6 +762,7 @@ extern "C" int agg_ctx_destroy(agg_ctx* ctx) {
     if (e) step(hipEventDestroy(e), "hipEventDestroy");
   if (ctx->up_host) step(hipHostFree(ctx->up_host), "hipHostFree");
   if (ctx->ws) step(hipFree(ctx->ws), "hipFree(ws)");
+  if (ctx->moe_ws) step(hipFree(ctx->moe_ws), "hipFree(moe workspaces)");
   for (int j = 0; j < kTimingRing; ++j) {
     if (ctx->ev_t0[j]) step(hipEventDestroy(ctx->ev_t0[j]), "hipEventDestroy");
     if (ctx->ev_t1[j]) step(hipEventDestroy(ctx->ev_t1[j]), "hipEventDestroy");

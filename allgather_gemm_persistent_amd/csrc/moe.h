@@ -13,10 +13,13 @@ struct StreamArgs {
   uint16_t* c;          // slots x N (gated: N / 2) bfloat16
   int64_t N, K;
   ExpertArgs x;
+  int strips, ksplit;   // strips of the output's columns; parts of K
+  float* ws;            // ksplit > 1: ksplit x slots x N floats
+  int64_t ws_bytes;
+  uint32_t* counts;     // ksplit > 1: n_experts x strips counters, zero before and after
 };
 
-// Rows are taken 16 * row_blocks at a time (bf16: 1, 2 or 4; fp8: 1 or 2).
-hipError_t launch_expert_stream(const StreamArgs& args, int row_blocks, int dtype, hipStream_t stream);
+hipError_t launch_expert_stream(const StreamArgs& args, int dtype, hipStream_t stream);
 // The tiled kernel: args as kEpiExperts reads them, tiles of bm x bn.
 hipError_t launch_expert_tiles(const GemmArgs& args, int bm, int bn, int dtype, int grid, hipStream_t stream);
 

@@ -1,6 +1,6 @@
 // The C entry points of the mixture-of-experts operators: checks, then one or two launches on the
-// caller's stream. They keep nothing in the ctx (it names the device and its compute units), so
-// calls on several streams do not meet.
+// caller's stream. What they use of the ctx, beside its device, is a workspace of the call's stream
+// (moe_gemm with a split K), so calls on several streams do not meet.
 #include "moe.h"
 #include "plan.h"
 
@@ -88,11 +88,14 @@ extern "C" int moe_gemm(agg_ctx* ctx, int64_t slots, int n_experts, int64_t n, i
   const int64_t cols = gated ? 2 * n : n;
   const ExpertArgs x{offsets, slot_token, a_scale, b_scale, slots, a_rows, ld_a * eb, n_experts, gated != 0};
   const int units = ctx_units(ctx);
-  const ExpertShape shape = choose_expert_shape(dtype, slots, n_experts, cols, k, units);
-  if (shape.row_blocks) {
-    const StreamArgs s{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(b), static_cast<uint16_t*>(out),
-                       cols, k, x};
-    HIP_TRY(launch_expert_stream(s, shape.row_blocks, dtype, S(stream)));
+  const TileShape forced = ctx_forced_tile(ctx);
+  const ExpertShape shape = forced.bm ? ExpertShape{false, 0, 0, forced}
+                                      : choose_expert_shape(dtype, slots, n_experts, n, k, gated, units);
+  if (shape.stream) {
+    StreamArgs s{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(b), static_cast<uint16_t*>(out),
+                 cols, k, x, shape.strips, shape.ksplit, nullptr, kMoeWsBytes, nullptr};
+    if (s.ksplit > 1 && !ctx_moe_workspace(ctx, stream, &s.ws, &s.counts)) s.ksplit = 1;
+    HIP_TRY(launch_expert_stream(s, dtype, S(stream)));
     return AGG_OK;
   }
   GemmArgs g{};

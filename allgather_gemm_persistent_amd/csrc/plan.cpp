@@ -82,7 +82,7 @@ KSplit choose_ksplit(int op, int dtype, int64_t tiles, int64_t k, int units) {
 // Relative MFMA efficiency of each shape (operand bytes per flop fall as the tile grows; the
 // 128 x 128 weight from bare launches of the 5120-row AllToAll workload, where its 4.4 waves
 // ran 14% slower than two waves of 256 x 256 tiles).
-double tile_eff(const TileShape& s) {
+static double tile_eff(const TileShape& s) {
   if (s.bm == 256 && s.bn == 256) return 1.0;
   if (s.bm == 256) return 0.98;
   if (s.bm == 128 && s.bn == 128) return 0.6;

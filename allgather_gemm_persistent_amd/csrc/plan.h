@@ -80,16 +80,25 @@ int check_order(int world, int rank, int chunks_per_shard, const int32_t* order,
 // The ctx's compute units and HIP device.
 int ctx_units(const agg_ctx* ctx);
 int ctx_device(const agg_ctx* ctx);
+// The tile shape agg_ctx_set_tile forces; {0, 0}: none.
+TileShape ctx_forced_tile(const agg_ctx* ctx);
 
-// Relative MFMA efficiency of a tile shape (256 x 256: 1).
-double tile_eff(const TileShape& s);
+// The workspace of moe_gemm's split K on one stream: partial sums, and a counter for every strip of
+// every expert. A ctx has kMoeWorkspaces of them and gives one to each stream that asks (the first
+// kMoeWorkspaces streams; false for a later one), so calls on different streams do not meet.
+constexpr int64_t kMoeWsBytes = int64_t(8) << 20;
+constexpr int kMoeCounters = 4096;
+constexpr int kMoeWorkspaces = 4;
+bool ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, float** ws, uint32_t** counts);
 
-// How moe_gemm multiplies: row_blocks > 0: the streaming kernel, 16 * row_blocks rows at a time;
-// otherwise tiles of bm x bn.
+// How moe_gemm multiplies: stream: strips of the output's columns with K in ksplit parts; otherwise
+// tiles of `tile`.
 struct ExpertShape {
-  int row_blocks;
+  bool stream;
+  int strips, ksplit;
   TileShape tile;
 };
-ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t cols, int64_t k, int units);
+ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated,
+                                int units);
 
 }  // namespace agg

@@ -526,10 +526,13 @@ int agg_ctx_set_chain_fused(agg_ctx* ctx, int on);
  * back to tokens (moe_combine). They are forward operators, like the others here.
  *
  * Every call launches on `stream` alone (one kernel; moe_plan two beyond 1024 pairs), is
- * capturable, allocates nothing and keeps nothing in the ctx, which names the device: calls on
- * several streams do not meet. Strides `ld_*` are elements from one row to the next. Device arrays
- * are 16-byte aligned unless stated. None of the results depends on timing: no floating-point
- * atomics.
+ * capturable and allocates nothing. Of the ctx they use its device and, in moe_gemm with few rows
+ * and few experts, one of four workspaces of partial sums, each given to one of the first four
+ * streams that need one (a later stream's calls go without, slower): calls on several streams do not
+ * meet, but a graph that holds calls captured on a stream must not be replayed while other calls
+ * captured or made on that stream run. Strides `ld_*` are elements from one row to the next. Device
+ * arrays are 16-byte aligned unless stated. None of the results depends on timing: no
+ * floating-point atomics.
  * Passage: section "DITRON adds three levels of tiling" (AllToAll among the collectives, whose
  *  delivered tokens these operators route and multiply); the operators' formulas are the plain
  *  definitions stated here, the pages give none.
@@ -610,6 +613,8 @@ int moe_plan(agg_ctx* ctx, int64_t tokens, int top_k, const int32_t* ids, int fi
  *   a_scale          fp8: fp32[a_rows]; b_scale: fp32[n_experts, columns of b]: each row and each
  *                    column of the product times its scale. Both ignored for bf16
  *   out              slots x n bf16, rounded once from the fp32 product
+ * Few rows an expert stream the weights through registers, more take tiles (agg_moe_gemm_shape); a
+ * shape forced by agg_ctx_set_tile applies here too.
  * Limits: k * elem, n * elem and n * 2 bytes multiples of 16, one expert's weight below 2 GiB, and
  * with slot_token A below 2 GiB.
  */
@@ -728,11 +733,11 @@ int agg_check_combine_args(int64_t tokens, int top_k, int64_t n, int64_t slots, 
                            const int32_t* token_slot, const float* weights, int out_dtype,
                            const void* out);
 
-/* How moe_gemm multiplies a call on a whole MI355X: *stream_rows rows at a time with the weights
- * streamed through registers (then *bm = *bn = 0), or, with *stream_rows 0, tiles of *bm x *bn.
+/* How moe_gemm multiplies a call on a whole MI355X: *ksplit > 0: the weights streamed through
+ * registers, K in that many parts (then *bm = *bn = 0); *ksplit 0: tiles of *bm x *bn.
  */
 int agg_moe_gemm_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated,
-                       int* stream_rows, int* bm, int* bn);
+                       int* ksplit, int* bm, int* bn);
 
 /* ---- diagnostics ---------------------------------------------------------------------- */
 

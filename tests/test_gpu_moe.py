@@ -574,3 +574,23 @@ def test_layer_on_a_side_stream_and_in_a_replayed_graph(ctx, T):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager), seed
+
+
+def test_split_k_on_more_streams_than_workspaces(ctx):
+    """Calls of few rows and experts, K split over workgroups, at once on six streams (two of them go
+    without a workspace) and over and over: every result is its own."""
+    xs = [_Experts([1, 2], 256, 4096, "bf16", i % 2 == 0, True, seed=i) for i in range(6)]
+    assert B.agg_moe_gemm_shape("bf16", 3, 2, 256, 4096, True)[1] > 1
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = []
+    for x in xs:
+        x.run(ctx)                                   # lays the data out on the device
+        outs.append(torch.zeros(3, 256, dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, s, out in zip(xs, streams, outs):
+            a, b, off, tok, sa, sb = x.held
+            B.moe_gemm(ctx, 3, 2, 256, 4096, "bf16", a, b, off, out, gated=x.gated, slot_token=tok, stream=s)
+    torch.cuda.synchronize()
+    for x, out in zip(xs, outs):
+        x.check(out)

@@ -1,8 +1,6 @@
 """The mixture-of-experts operators' host side, without a GPU: the argument checks' codes, the choice
 of the experts' kernel, and the binding's own checks."""
 
-import ctypes
-
 import pytest
 import torch
 
@@ -140,18 +138,26 @@ def test_a_call_without_a_ctx_or_weight_is_refused(lib):
 
 
 def test_kernel_choice(lib):
-    """Few rows an expert stream; many take tiles no larger than the rows call for."""
-    assert B.agg_moe_gemm_shape("bf16", 1, 8, 3584, 8192) == ("stream", 16)
-    assert B.agg_moe_gemm_shape("bf16", 32, 8, 3584, 8192, gated=True)[0] == "stream"
-    kind, shape = B.agg_moe_gemm_shape("bf16", 10240, 8, 3584, 8192, gated=True)
-    assert kind == "tiles" and shape[0] == 256
-    kind, shape = B.agg_moe_gemm_shape("fp8", 16384, 8, 3584, 8192, gated=True)
-    assert kind == "tiles" and shape[0] == 256
+    """Few rows an expert over a long K stream the weights, K split while the strips of the busy
+    experts leave compute units idle; many rows take tiles as high as the rows call for."""
+    kind, parts = B.agg_moe_gemm_shape("bf16", 1, 8, 3584, 8192)
+    assert kind == "stream" and 28 * parts <= 256 < 28 * (parts + 1)
+    assert B.agg_moe_gemm_shape("bf16", 32, 8, 3584, 8192, gated=True) == ("stream", 1)
+    assert B.agg_moe_gemm_shape("fp8", 32, 8, 3584, 8192, gated=True) == ("stream", 2)
+    assert B.agg_moe_gemm_shape("bf16", 8 * 16, 8, 3584, 8192)[0] == "stream"
+    assert B.agg_moe_gemm_shape("bf16", 8 * 17, 8, 3584, 8192)[0] == "tiles"
+    # K too short to share among the waves
+    assert B.agg_moe_gemm_shape("bf16", 8, 8, 3584, 1016)[0] == "tiles"
+    # partial sums that would not fit the workspace, more strips than counters: fewer parts
+    assert B.agg_moe_gemm_shape("bf16", 16, 1, 8192, 1 << 15) == ("stream", 4)
+    assert B.agg_moe_gemm_shape("bf16", 1, 1024, 1024, 8192) == ("stream", 1)
+    for dtype, slots in (("bf16", 10240), ("fp8", 16384)):
+        kind, shape = B.agg_moe_gemm_shape(dtype, slots, 8, 3584, 8192, gated=True)
+        assert kind == "tiles" and shape[0] == 256
     # sizes without work still name a kernel
-    assert B.agg_moe_gemm_shape("fp8", 0, 1, 16, 16)[0] == "stream"
+    assert B.agg_moe_gemm_shape("fp8", 0, 1, 16, 16)[0] == "tiles"
     with pytest.raises(B.AggError):
         B._call("agg_moe_gemm_shape", 0, 1, 1, 8, 8, 0, None, None, None)
-    assert ctypes.c_int is B._c_int
 
 
 def test_binding_refuses_what_the_call_would_read_wrongly(lib):
