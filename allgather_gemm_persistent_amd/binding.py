@@ -150,10 +150,9 @@ def load(path: str | None = None):
 
 
 def _call(name: str, *args) -> None:
-    lib = load()
-    rc = getattr(lib, name)(*args)
+    rc = getattr(_lib or load(), name)(*args)
     if rc != AGG_OK:
-        raise AggError(rc, name, lib.agg_last_error().decode())
+        raise AggError(rc, name, load().agg_last_error().decode())
 
 
 # ------------------------------------------------------------------------------ marshalling
@@ -572,26 +571,29 @@ def _tensor_dtype(x, what):
 
 def _rows(x, rows, cols, what, dtype=None):
     """(pointer, elements from one row to the next) of a rows x cols tensor whose columns are
-    contiguous; (None, 0) for None."""
+    contiguous; (None, 0) for None. (Decode calls take a few microseconds: every tensor attribute is
+    read once.)"""
     if x is None:
         return None, 0
-    if x.dim() != 2 or x.shape[1] != cols or x.shape[0] < rows:
-        raise AggError(AGG_E_ARG, what, f"has shape {tuple(x.shape)}, the call takes {rows} x {cols}")
-    if dtype is not None and x.dtype != dtype:
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 2 or shape[1] != cols or shape[0] < rows:
+        raise AggError(AGG_E_ARG, what, f"has shape {tuple(shape)}, the call takes {rows} x {cols}")
+    if dtype is not None and x.dtype is not dtype:
         raise AggError(AGG_E_ARG, what, f"is {x.dtype}, not {dtype}")
-    if cols > 1 and x.stride(1) != 1:
+    ld, step = strides
+    if step != 1 and cols > 1:
         raise AggError(AGG_E_ARG, what, "must have contiguous columns")
-    if not x.is_cuda and x.numel():
+    if not x.is_cuda and shape[0] and cols:
         raise AggError(AGG_E_ARG, what, f"must be a device tensor, got {x.device}")
     # (a single row, or none, may carry any stride)
-    return x.data_ptr(), x.stride(0) if rows > 1 else max(cols, x.stride(0))
+    return x.data_ptr(), ld if rows > 1 or ld > cols else cols
 
 
 def _flat(x, count, what, dtype):
     """The pointer of a contiguous tensor of at least `count` elements; None for None."""
     if x is None:
         return None
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise AggError(AGG_E_ARG, what, f"is {x.dtype}, not {dtype}")
     if not x.is_contiguous() or x.numel() < count:
         raise AggError(AGG_E_ARG, what, f"must be contiguous and hold {count} elements, has {x.numel()}")

@@ -39,27 +39,106 @@ __device__ inline float token_reduce(float v, F op) {
   return v;
 }
 
+// Orders a wave's LDS accesses: what its lanes wrote before is what they read after (the lanes of a
+// token share a wave, whose LDS operations run in order; this keeps the compiler to that order).
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 __device__ inline float bf16_float(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
+
+// 1 / d for 1 <= d <= 2^126, rounded like the division: a reciprocal, one Newton step, and the
+// residual's correction (Markstein); equal to the division for every such float (all were tried). The
+// general division takes twice as many instructions for ranges that do not occur here.
+__device__ inline float reciprocal(float d) {
+  float r = __builtin_amdgcn_rcpf(d);
+  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+constexpr float kReciprocalMost = 8.5e37f;   // below 2^126
+
+// A group's score from its two largest keys.
+__device__ inline float group_key(int sigmoid, float b0, float b1) { return sigmoid && b1 > kNone ? b0 + b1 : b0; }
+
+// The groups before group g: larger scores, or equal ones at a lower index.
+__device__ inline int group_rank(const float* score, int groups, int g) {
+  const float mine = score[g];
+  int before = 0;
+  for (int o = 0; o < groups; ++o) {
+    const float x = score[o];
+    before += x > mine || (x == mine && o < g) ? 1 : 0;
+  }
+  return before;
+}
+
+// Drop the keys of the groups that do not stay, where group g is the G rows of experts g * G .. of a
+// lane: its two largest keys meet over the lanes in registers. `score`: the token's room in LDS.
+template <int STEPS, int V, int G>
+__device__ inline void keep_groups(float (&key)[V], int sigmoid, int top_groups, float* score, int lane) {
+  constexpr int L = 1 << STEPS, N = V / G;
+  if constexpr (N >= 1) {
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+      float b0 = key[g * G], b1 = kNone;
+#pragma unroll
+      for (int i = 1; i < G; ++i) {
+        b1 = fmaxf(b1, fminf(b0, key[g * G + i]));
+        b0 = fmaxf(b0, key[g * G + i]);
+      }
+      each_step<0, STEPS>([&](auto i) {
+        const float o0 = __builtin_bit_cast(float, other_lane<decltype(i)::value>(__builtin_bit_cast(int, b0)));
+        const float o1 = __builtin_bit_cast(float, other_lane<decltype(i)::value>(__builtin_bit_cast(int, b1)));
+        b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
+        b0 = fmaxf(b0, o0);
+      });
+      if (lane == g % L) score[g] = group_key(sigmoid, b0, b1);
+    }
+    wave_sync();
+    uint32_t kept = 0;
+#pragma unroll
+    for (int g0 = 0; g0 < N; g0 += L)
+      if (g0 + lane < N && group_rank(score, N, g0 + lane) < top_groups) kept |= 1u << (g0 + lane);
+    each_step<0, STEPS>([&](auto i) { kept |= (uint32_t)other_lane<decltype(i)::value>((int)kept); });
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (!(kept & (1u << (v / G)))) key[v] = kNone;
+  }
+}
 
 }  // namespace
 
-// 2^STEPS lanes a token, each holding the keys of V experts in registers (expert v * L + lane).
-// The k picks are k maxima over (key, lowest index); a picked key becomes kNone. Chosen experts'
-// scores are computed again from their logits at the end, by the lane that writes them, so no
-// second array is held. With groups the keys also go to LDS, where a lane scans a whole group for
-// its score.
-template <int STEPS, int V>
+// 2^STEPS lanes a token, each holding the keys of V experts in registers (expert v * L + lane). With
+// groups the keys also go to LDS, where a lane scans a whole group for its score.
+//
+// The choice: with no more picks than half the lanes, the top_k-th largest of the lanes' own maxima is
+// a bound that top_k keys reach, so only keys that reach it can be picked; they are few (about 10 for
+// 8 of 256), go to a list in LDS, and each takes its place by counting the keys before it, (larger, or
+// equal at a lower index). Otherwise, or where ties fill the list, the picks are top_k maxima over
+// (key, lowest index) one after another, a picked key becoming kNone. Chosen experts' scores are
+// computed again from their logits, by the lane that writes them.
+//
+// Bound by instructions at many tokens (the sigmoid first): 32768 tokens of 256 experts in fp32 are
+// 33.6 MB, 5 us of reading.
+template <int STEPS, int V, bool BF16>
 __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
   constexpr int L = 1 << STEPS, TOKENS = 256 / L, E = L * V;
   constexpr int OUT = AGG_MAX_TOP_K > L ? AGG_MAX_TOP_K / L : 1;   // choices a lane writes
   __shared__ float keys[TOKENS][E + 1];
   __shared__ float group_score[TOKENS][AGG_MAX_GROUPS];
+  constexpr int LIST = 2 * L;               // candidates a token's list holds
+  struct __attribute__((aligned(8))) Candidate {
+    float key;
+    int at;
+  };
+  __shared__ Candidate list[TOKENS][LIST];
+  __shared__ int picked[TOKENS][AGG_MAX_TOP_K];
   const int lane = threadIdx.x & (L - 1), slot = threadIdx.x / L;
   const int64_t t = (int64_t)blockIdx.x * TOKENS + slot;
   const bool live = t < a.tokens;
   const float* const xf = static_cast<const float*>(a.logits) + t * a.ld;
   const uint16_t* const xb = static_cast<const uint16_t*>(a.logits) + t * a.ld;
-  auto logit = [&](int e) { return a.logits_bf16 ? bf16_float(xb[e]) : xf[e]; };
+  auto logit = [&](int e) { return BF16 ? bf16_float(xb[e]) : xf[e]; };
 
   float key[V];
   float top = kNone;
@@ -85,83 +164,174 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
     }
   }
   auto score = [&](float x) { return a.sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - top) / sum; };
-  if (a.sigmoid || a.bias) {
+  if (a.sigmoid) {
+    float d[V], most = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (!(key[v] > kNone)) continue;
-      key[v] = score(key[v]);
-      if (a.bias) key[v] += a.bias[v * L + lane];
+      d[v] = 1.0f + expf(-key[v]);          // (kNone: infinity)
+      most = fmaxf(most, key[v] > kNone ? d[v] : 0.0f);
+    }
+    const bool plain = __any(!(most <= kReciprocalMost));
+    if (plain) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = 1.0f / d[v];
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = reciprocal(d[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = key[v] > kNone ? d[v] : kNone;
+  } else if (a.bias) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = key[v] > kNone ? score(key[v]) : kNone;
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = v * L + lane;
+      if (e < a.experts) key[v] += a.bias[e];
       if (key[v] != key[v]) key[v] = kNone;
     }
   }
 
   if (a.groups > 1) {
     const int size = a.experts / a.groups;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = v * L + lane;
-      if (e < a.experts) keys[slot][e] = key[v];
-    }
-    __syncthreads();
-    for (int g = lane; g < a.groups; g += L) {
-      float b0 = kNone, b1 = kNone;
-      for (int i = 0; i < size; ++i) {
-        const float x = keys[slot][g * size + i];
-        b1 = fmaxf(b1, fminf(b0, x));
-        b0 = fmaxf(b0, x);
-      }
-      group_score[slot][g] = a.sigmoid && b1 > kNone ? b0 + b1 : b0;
-    }
-    __syncthreads();
+    // groups of one, two or four whole rows of experts across the lanes: scored in registers;
+    // others: through LDS
+    const bool whole = a.experts == E && size % L == 0 && a.groups <= 32;
     uint32_t kept[2] = {0, 0};              // a bit for each group that stays
-    for (int g = lane; g < a.groups; g += L) {
-      const float mine = group_score[slot][g];
-      int before = 0;
-      for (int o = 0; o < a.groups; ++o) {
-        const float x = group_score[slot][o];
-        before += (x > mine || (x == mine && o < g)) ? 1 : 0;
-      }
-      if (before < a.top_groups) kept[g >> 5] |= 1u << (g & 31);
-    }
-    each_step<0, STEPS>([&](auto i) {
-      kept[0] |= (uint32_t)other_lane<decltype(i)::value>((int)kept[0]);
-      kept[1] |= (uint32_t)other_lane<decltype(i)::value>((int)kept[1]);
-    });
-    // e / size by a product: exact while e * size < 2^20
-    const uint32_t inv = ((1u << 20) + (uint32_t)size - 1) / (uint32_t)size;
+    if (whole && size == L) keep_groups<STEPS, V, 1>(key, a.sigmoid, a.top_groups, group_score[slot], lane);
+    else if (whole && size == 2 * L) keep_groups<STEPS, V, 2>(key, a.sigmoid, a.top_groups, group_score[slot], lane);
+    else if (whole && size == 4 * L) keep_groups<STEPS, V, 4>(key, a.sigmoid, a.top_groups, group_score[slot], lane);
+    else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t g = ((uint32_t)(v * L + lane) * inv) >> 20;
-      if (!((kept[(g >> 5) & 1] >> (g & 31)) & 1u)) key[v] = kNone;
+      for (int v = 0; v < V; ++v) {
+        const int e = v * L + lane;
+        if (e < a.experts) keys[slot][e] = key[v];
+      }
+      wave_sync();
+      // `parts` lanes a group, each over its share of the members, starting at different members (the
+      // groups' members lie a power of two apart in LDS: from the same one the lanes would meet in
+      // its banks)
+      int slots = 1;
+      while (slots < a.groups && slots < L) slots *= 2;
+      const int parts = L / slots, part = lane / slots;
+      for (int g = lane & (slots - 1); g < a.groups; g += slots) {
+        float b0 = kNone, b1 = kNone;
+        int m = (g + part) % size;
+        for (int i = part; i < size; i += parts) {
+          const float x = keys[slot][g * size + m];
+          b1 = fmaxf(b1, fminf(b0, x));
+          b0 = fmaxf(b0, x);
+          m += parts;
+          if (m >= size) m -= size;
+        }
+        for (int d = slots; d < L; d *= 2) {
+          const float o0 = __shfl_xor(b0, d), o1 = __shfl_xor(b1, d);
+          b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
+          b0 = fmaxf(b0, o0);
+        }
+        if (part == 0) group_score[slot][g] = group_key(a.sigmoid, b0, b1);
+      }
+      wave_sync();
+      for (int g = lane; g < a.groups; g += L)
+        if (group_rank(group_score[slot], a.groups, g) < a.top_groups) kept[g >> 5] |= 1u << (g & 31);
+      each_step<0, STEPS>([&](auto i) {
+        kept[0] |= (uint32_t)other_lane<decltype(i)::value>((int)kept[0]);
+        kept[1] |= (uint32_t)other_lane<decltype(i)::value>((int)kept[1]);
+      });
+      // e / size by a product: exact while e * size < 2^20
+      const uint32_t inv = ((1u << 20) + (uint32_t)size - 1) / (uint32_t)size;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint32_t g = ((uint32_t)(v * L + lane) * inv) >> 20;
+        if (!((kept[(g >> 5) & 1] >> (g & 31)) & 1u)) key[v] = kNone;
+      }
     }
   }
 
   int mine[OUT];
-#pragma unroll
-  for (int o = 0; o < OUT; ++o) mine[o] = -1;
-  for (int j = 0; j < a.top_k; ++j) {
+  // (three picks one after another cost no more than the list)
+  bool listed = 2 * a.top_k <= L && a.top_k > 3;
+  if (listed) {
+    // the bound: the top_k-th largest of the lanes' maxima (equal ones count for every lane)
     float best = key[0];
-    int at = lane;
 #pragma unroll
-    for (int v = 1; v < V; ++v) {
-      const bool more = key[v] > best;      // (equal keys: the lower index stays)
-      best = more ? key[v] : best;
-      at = more ? v * L + lane : at;
+    for (int v = 1; v < V; ++v) best = fmaxf(best, key[v]);
+    wave_sync();                            // (the groups' scores were read from here)
+    group_score[slot][lane] = best;
+    wave_sync();
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < L; ++i) before += group_score[slot][i] > best ? 1 : 0;
+    // lanes with fewer than top_k larger maxima hold the top_k largest; the least of them
+    // (no less than the lowest float, which kNone does not reach)
+    const float bound = fmaxf(token_reduce<STEPS>(before < a.top_k ? best : __builtin_inff(),
+                                                  [](float x, float y) { return fminf(x, y); }),
+                              -3.402823466e38f);
+    int count = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) count += key[v] >= bound ? 1 : 0;
+    int held = count;                       // becomes the lanes' inclusive prefix
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) {
+      const int o = __shfl_up(held, d, L);
+      if (lane >= d) held += o;
     }
-    each_step<0, STEPS>([&](auto i) {
-      const float ob = __builtin_bit_cast(float, other_lane<decltype(i)::value>(__builtin_bit_cast(int, best)));
-      const int oa = other_lane<decltype(i)::value>(at);
-      const bool take = ob > best || (ob == best && oa < at);
-      best = take ? ob : best;
-      at = take ? oa : at;
-    });
-    const int chosen = best > kNone ? at : -1;
+    const int all = __shfl(held, L - 1, L);
+    listed = !__any(all > LIST);
+    if (listed) {
+      int at = held - count;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * L + lane == at) key[v] = kNone;
+      for (int v = 0; v < V; ++v)
+        if (key[v] >= bound) {
+          list[slot][at] = Candidate{key[v], v * L + lane};
+          ++at;
+        }
+      for (int j = lane; j < a.top_k; j += L) picked[slot][j] = -1;
+      wave_sync();
+      for (int c = lane; c < all; c += L) {
+        const Candidate own = list[slot][c];
+        int place = 0;
+#pragma unroll 4
+        for (int i = 0; i < all; ++i) {
+          const Candidate o = list[slot][i];
+          place += o.key > own.key || (o.key == own.key && o.at < own.at) ? 1 : 0;
+        }
+        if (place < a.top_k) picked[slot][place] = own.at;
+      }
+      wave_sync();
 #pragma unroll
-    for (int o = 0; o < OUT; ++o)
-      if (j == o * L + lane) mine[o] = chosen;
+      for (int o = 0; o < OUT; ++o) mine[o] = o * L + lane < a.top_k ? picked[slot][o * L + lane] : -1;
+    }
+  }
+  if (!listed) {
+#pragma unroll
+    for (int o = 0; o < OUT; ++o) mine[o] = -1;
+    for (int j = 0; j < a.top_k; ++j) {
+      float best = key[0];
+      int at = lane;
+#pragma unroll
+      for (int v = 1; v < V; ++v) {
+        const bool more = key[v] > best;    // (equal keys: the lower index stays)
+        best = more ? key[v] : best;
+        at = more ? v * L + lane : at;
+      }
+      each_step<0, STEPS>([&](auto i) {
+        const float ob = __builtin_bit_cast(float, other_lane<decltype(i)::value>(__builtin_bit_cast(int, best)));
+        const int oa = other_lane<decltype(i)::value>(at);
+        const bool take = ob > best || (ob == best && oa < at);
+        best = take ? ob : best;
+        at = take ? oa : at;
+      });
+      const int chosen = best > kNone ? at : -1;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v * L + lane == at) key[v] = kNone;
+#pragma unroll
+      for (int o = 0; o < OUT; ++o)
+        if (j == o * L + lane) mine[o] = chosen;
+    }
   }
   float w[OUT], total = 0.0f;
 #pragma unroll
@@ -186,8 +356,9 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
 template <int STEPS, int V>
 static hipError_t launch_route_lv(const RouteArgs& a, hipStream_t stream) {
   constexpr int64_t tokens = 256 >> STEPS;
-  hipLaunchKernelGGL((route_kernel<STEPS, V>), dim3((unsigned)((a.tokens + tokens - 1) / tokens)), dim3(256), 0,
-                     stream, a);
+  const dim3 grid((unsigned)((a.tokens + tokens - 1) / tokens)), block(256);
+  if (a.logits_bf16) hipLaunchKernelGGL((route_kernel<STEPS, V, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((route_kernel<STEPS, V, false>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
@@ -217,41 +388,46 @@ __device__ inline int bucket_of(const PlanArgs& a, int64_t p) {
 
 }  // namespace
 
-__global__ void __launch_bounds__(256) plan_count_kernel(const PlanArgs a) {
+constexpr int kPlanThreads = 1024;
+
+// Block b of R * kPlanPairs pairs.
+template <int R>
+__global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs a) {
   __shared__ int count[AGG_MAX_EXPERTS + 1];
   const int buckets = a.n_local + 1;
-  for (int e = threadIdx.x; e < buckets; e += 256) count[e] = 0;
+  for (int e = threadIdx.x; e < buckets; e += kPlanThreads) count[e] = 0;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPlanPairs / 256; ++i) {
-    const int64_t p = (int64_t)blockIdx.x * kPlanPairs + i * 256 + threadIdx.x;
+  for (int r = 0; r < R; ++r) {
+    const int64_t p = ((int64_t)blockIdx.x * R + r) * kPlanPairs + threadIdx.x;
     if (p < a.pairs) atomicAdd(&count[bucket_of(a, p)], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < buckets; e += 256) a.work[(int64_t)blockIdx.x * buckets + e] = count[e];
+  for (int e = threadIdx.x; e < buckets; e += kPlanThreads) a.work[(int64_t)blockIdx.x * buckets + e] = count[e];
 }
 
-__global__ void __launch_bounds__(256) plan_place_kernel(const PlanArgs a) {
-  constexpr int W = 4, R = kPlanPairs / 256;         // waves; rounds of 64 pairs a wave
+template <int R>
+__global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs a) {
+  constexpr int W = kPlanThreads / 64;               // waves
   __shared__ int count[W][AGG_MAX_EXPERTS + 1];      // pairs of this block, by wave and bucket
   __shared__ int total[AGG_MAX_EXPERTS + 1];         // pairs of all blocks, by bucket
   __shared__ int place[AGG_MAX_EXPERTS + 1];         // where the block's pairs of a bucket begin
   __shared__ int wave_sum[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int buckets = a.n_local + 1, blocks = (int)gridDim.x, block = (int)blockIdx.x;
-  for (int e = tid; e < buckets; e += 256) {
+  for (int e = tid; e < buckets; e += kPlanThreads) {
     for (int w = 0; w < W; ++w) count[w][e] = 0;
     total[e] = place[e] = 0;
   }
-  __syncthreads();
-
-  // each wave takes 64 pairs after 64 of its quarter of the block, in order: the lanes of one
-  // bucket find each other by comparing the bucket's bits over ballots
+  // each wave takes 64 pairs after 64 of its part of the block, in order
+  auto pair = [&](int r) { return ((int64_t)block * W + wave) * (R * 64) + r * 64 + lane; };
   int bucket[R], rank[R];
 #pragma unroll
+  for (int r = 0; r < R; ++r) bucket[r] = pair(r) < a.pairs ? bucket_of(a, pair(r)) : -1;
+  __syncthreads();
+  // the lanes of one bucket find each other by comparing the bucket's bits over ballots
+#pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int64_t p = (int64_t)block * kPlanPairs + wave * (kPlanPairs / W) + r * 64 + lane;
-    bucket[r] = p < a.pairs ? bucket_of(a, p) : -1;
     uint64_t same = __ballot(bucket[r] >= 0);
     for (int b = 0; (1 << b) <= a.n_local; ++b) {
       const bool bit = (bucket[r] >> b) & 1;
@@ -262,34 +438,45 @@ __global__ void __launch_bounds__(256) plan_place_kernel(const PlanArgs a) {
     rank[r] = 0;
     if (bucket[r] >= 0) {
       rank[r] = count[wave][bucket[r]] + before;
+      wave_sync();
       if (before == 0) count[wave][bucket[r]] += __popcll(same);
     }
-    __syncthreads();
+    wave_sync();
   }
 
   // totals of every bucket and what the blocks before this one hold of it
   if (blocks > 1) {
+    // kBatch loads on their way together; a thread steps through (block, bucket) by kPlanThreads
+    constexpr int kBatch = 8;
     int e = tid % buckets, b = tid / buckets;
-    const int step_e = 256 % buckets, step_b = 256 / buckets;
-    for (int i = tid; i < blocks * buckets; i += 256) {
-      const int c = a.work[i];
-      if (c) {
-        atomicAdd(&total[e], c);
-        if (b < block) atomicAdd(&place[e], c);
+    const int step_e = kPlanThreads % buckets, step_b = kPlanThreads / buckets, words = blocks * buckets;
+    for (int i0 = tid; i0 < words; i0 += kPlanThreads * kBatch) {
+      int c[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) c[u] = i0 + u * kPlanThreads < words ? a.work[i0 + u * kPlanThreads] : 0;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (c[u]) {
+          atomicAdd(&total[e], c[u]);
+          if (b < block) atomicAdd(&place[e], c[u]);
+        }
+        e += step_e;
+        b += step_b;
+        if (e >= buckets) { e -= buckets; ++b; }
       }
-      e += step_e;
-      b += step_b;
-      if (e >= buckets) { e -= buckets; ++b; }
     }
+    __syncthreads();
   } else {
-    for (int e = tid; e < buckets; e += 256) {
+    __syncthreads();
+    for (int e = tid; e < buckets; e += kPlanThreads) {
       int c = 0;
       for (int w = 0; w < W; ++w) c += count[w][e];
       total[e] = c;
     }
+    __syncthreads();
   }
-  __syncthreads();
-  constexpr int kRun = (AGG_MAX_EXPERTS + 1 + 255) / 256;
+  // a thread's run of buckets, and all runs before it
+  constexpr int kRun = (AGG_MAX_EXPERTS + 1 + kPlanThreads - 1) / kPlanThreads;
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
@@ -319,7 +506,7 @@ __global__ void __launch_bounds__(256) plan_place_kernel(const PlanArgs a) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (bucket[r] < 0) continue;
-    const int64_t p = (int64_t)block * kPlanPairs + wave * (kPlanPairs / W) + r * 64 + lane;
+    const int64_t p = pair(r);
     int s = place[bucket[r]] + rank[r];
     for (int w = 0; w < wave; ++w) s += count[w][bucket[r]];
     const bool held = bucket[r] < a.n_local;
@@ -328,14 +515,23 @@ __global__ void __launch_bounds__(256) plan_place_kernel(const PlanArgs a) {
   }
 }
 
-hipError_t launch_plan(const PlanArgs& a, hipStream_t stream) {
-  const int64_t blocks = a.pairs > 0 ? (a.pairs + kPlanPairs - 1) / kPlanPairs : 1;
+template <int R>
+static hipError_t launch_plan_r(const PlanArgs& a, hipStream_t stream) {
+  const int64_t blocks = a.pairs > 0 ? (a.pairs + R * kPlanPairs - 1) / (R * kPlanPairs) : 1;
   if (blocks > 1) {
-    hipLaunchKernelGGL(plan_count_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(plan_count_kernel<R>, dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  hipLaunchKernelGGL(plan_place_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(plan_place_kernel<R>, dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, a);
   return hipGetLastError();
+}
+
+// Every block reads every block's counts, so large plans take larger blocks.
+hipError_t launch_plan(const PlanArgs& a, hipStream_t stream) {
+  static_assert(kPlanThreads == kPlanPairs, "a pair a thread and round");
+  if (a.pairs <= 128 * kPlanPairs) return launch_plan_r<1>(a, stream);
+  if (a.pairs <= 256 * kPlanPairs) return launch_plan_r<2>(a, stream);
+  return launch_plan_r<4>(a, stream);
 }
 
 }  // namespace agg
