@@ -160,6 +160,21 @@ def test_quant_rows(ctx, rows, cols):
     assert q.float().abs().max().item() == 448
 
 
+def test_quant_rows_of_the_smallest_and_largest_numbers(ctx):
+    """Row scales whose reciprocal overflows, and rows near fp32's largest number."""
+    x = torch.randn(4, 512, generator=_gen(1))
+    x = x / x.abs().amax(1, keepdim=True)
+    x[0] *= 1e-40
+    x[1] *= 3e-36
+    x[2] *= 3e38
+    q, scales = torch.empty(4, 512, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(4, device="cuda")
+    B.quant_rows(ctx, 4, 512, x.cuda(), q, scales=scales, stream=torch.cuda.current_stream())
+    want = x.double().abs().amax(1) / 448
+    # (a subnormal scale is rounded to a multiple of 2^-149)
+    _within(scales, want, want * EPS32 + 2.0 ** -149, "scales")
+    _check_fp8(q.cpu(), scales.cpu(), x.double(), 1)
+
+
 # ------------------------------------------------------------------------------ routing
 
 def _route_ref(x, bias, score, groups, top_groups, k, renorm, scale):
