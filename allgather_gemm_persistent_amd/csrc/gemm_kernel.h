@@ -773,9 +773,11 @@ __device__ inline void static_for(F&& f) {
 // ---- experts' products: the tiles of all experts in one grid
 //
 // Expert e's rows are slots [offsets[e], offsets[e+1]), cut into row tiles of BM, so the number of
-// tiles is known on the device alone. Every workgroup builds the same prefix sum of row tiles over
-// the experts in LDS, and the tiles, in one sequence, are dealt without counters: they cost the
-// same, and nothing has to be cleared between launches.
+// tiles is known on the device alone. Every workgroup builds the same prefix sums of row tiles over the
+// experts in LDS, and the tiles are dealt without counters, so nothing has to be cleared between
+// launches. An expert's last row tile, where 256-row tiles would leave more than half of it empty, is a
+// low tile: half the MFMA rows, about half the time. Low tiles come last, first to the workgroups
+// that are a whole tile short (ExpertDeal).
 
 // The end of expert e - 1 and the start of expert e, kept inside [0, slots] and in order whatever
 // the array holds, so that no store leaves `out`.
@@ -784,37 +786,58 @@ __device__ inline int64_t expert_bound(const ExpertArgs& x, int e) {
   return v < 0 ? 0 : (v > x.slots ? x.slots : v);
 }
 
-// first[e] = row tiles of the experts before e, for e = 0 .. n_experts (all threads; ends in a
-// barrier). Each thread takes a run of consecutive experts.
-template <int BM>
-__device__ inline void expert_row_tiles(const ExpertArgs& x, int tid, int* first, int* wave_sum) {
+// first[e] and low[e] = whole and low row tiles of the experts before e, for e = 0 .. n_experts (all
+// threads; ends in a barrier). Each thread takes a run of consecutive experts.
+template <int BM, bool LOW>
+__device__ inline void expert_row_tiles(const ExpertArgs& x, int tid, int* first, int* low, int* wave_sum) {
   constexpr int kRun = (AGG_MAX_EXPERTS + kThreads - 1) / kThreads;
-  int n[kRun], mine = 0;
+  constexpr int W = kThreads / kWaveLanes;
+  int n[kRun], h[kRun], mine = 0, mine_low = 0;
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
     const int e = tid * kRun + i;
     int64_t rows = 0;
     if (e < x.n_experts) rows = expert_bound(x, e + 1) - expert_bound(x, e);
-    n[i] = rows > 0 ? (int)((rows + BM - 1) / BM) : 0;
+    if (rows < 0) rows = 0;
+    const int rest = (int)(rows % BM);
+    h[i] = LOW && rest > 0 && rest <= BM / 2;
+    n[i] = (int)(rows / BM) + (rest > 0 && !h[i]);
     mine += n[i];
+    mine_low += h[i];
   }
-  int incl = mine;
+  int incl = mine, incl_low = mine_low;
 #pragma unroll
   for (int d = 1; d < kWaveLanes; d *= 2) {
-    const int o = __shfl_up(incl, d);
-    if ((tid & 63) >= d) incl += o;
+    const int o = __shfl_up(incl, d), ol = __shfl_up(incl_low, d);
+    if ((tid & 63) >= d) {
+      incl += o;
+      incl_low += ol;
+    }
   }
-  if ((tid & 63) == 63) wave_sum[tid >> 6] = incl;
+  if ((tid & 63) == 63) {
+    wave_sum[tid >> 6] = incl;
+    wave_sum[W + (tid >> 6)] = incl_low;
+  }
   __syncthreads();
-  int at = incl - mine;
-  for (int w = 0; w < (tid >> 6); ++w) at += wave_sum[w];
+  int at = incl - mine, at_low = incl_low - mine_low;
+  for (int w = 0; w < (tid >> 6); ++w) {
+    at += wave_sum[w];
+    at_low += wave_sum[W + w];
+  }
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
     const int e = tid * kRun + i;
-    if (e <= x.n_experts) first[e] = at;
+    if (e <= x.n_experts) {
+      first[e] = at;
+      low[e] = at_low;
+    }
     at += n[i];
+    at_low += h[i];
   }
-  if (tid == kThreads - 1 && kThreads * kRun == x.n_experts) first[x.n_experts] = at;
+  if (tid == kThreads - 1 && kThreads * kRun == x.n_experts) {
+    first[x.n_experts] = at;
+    low[x.n_experts] = at_low;
+  }
   __syncthreads();
 }
 
@@ -822,18 +845,23 @@ struct ExpertTile {
   int expert, row_tile, col_tile;
 };
 
-// Tile `pos` of the sequence: experts ascending; within an expert, groups of kGroupCols column
-// tiles, rows after rows within a group. The workgroups of one XCD take neighbouring positions
-// (expert_pos), so about 32 tiles in flight share a block of A rows and B columns in its L2.
-constexpr int kGroupCols = 8;
-__device__ inline ExpertTile expert_tile(const int* first, int n_experts, int n_col_tiles, int pos) {
-  const int rt = pos / n_col_tiles;
+// The expert whose row tiles, by the prefix sums `first`, hold row tile rt.
+__device__ inline int expert_of(const int* first, int n_experts, int rt) {
   int lo = 0, hi = n_experts;                     // first[lo] <= rt < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= rt) lo = mid;
     else hi = mid;
   }
+  return lo;
+}
+
+// Whole tile `pos` of the sequence: experts ascending; within an expert, groups of kGroupCols column
+// tiles, rows after rows within a group. The workgroups of one XCD take neighbouring positions
+// (ExpertDeal), so about 32 tiles in flight share a block of A rows and B columns in its L2.
+constexpr int kGroupCols = 8;
+__device__ inline ExpertTile expert_tile(const int* first, int n_experts, int n_col_tiles, int pos) {
+  const int lo = expert_of(first, n_experts, pos / n_col_tiles);
   const int rows = first[lo + 1] - first[lo];
   const int q = pos - first[lo] * n_col_tiles;
   const int g = q / (rows * kGroupCols);
@@ -847,6 +875,45 @@ __device__ inline ExpertTile expert_tile(const int* first, int n_experts, int n_
   return t;
 }
 
+// Low tile `pos`: experts ascending, their last row tile's columns in order.
+__device__ inline ExpertTile expert_low_tile(const int* first, const int* low, int n_experts, int n_col_tiles,
+                                             int pos) {
+  const int e = expert_of(low, n_experts, pos / n_col_tiles);
+  return ExpertTile{e, first[e + 1] - first[e], pos % n_col_tiles};
+}
+
+// What a workgroup takes. The workgroups are dealt to the XCDs round robin; XCD x takes the x-th eighth
+// of the whole tiles and of the low ones. Its w workgroups take whole tiles in turn. Where that leaves
+// d of them a whole tile short, these take the first 2 * d low tiles, in two turns; all w take the rest
+// in turn.
+struct ExpertDeal {
+  int next, end, step;                // whole tiles: next, next + step, ... below end
+  int low_next, low_end, low_turn;    // the next low tile, and how many this workgroup has had
+  int low_begin, short_by, rank;      // the XCD's first low tile; d; this workgroup's number on the XCD
+  __device__ inline ExpertDeal(int total, int total_low) {
+    const int grid = (int)gridDim.x, b = (int)blockIdx.x;
+    const int X = grid < kXcds ? grid : kXcds;
+    const int x = b % X;
+    rank = b / X;
+    step = (grid - x + X - 1) / X;
+    const int begin = (int)((int64_t)total * x / X);
+    end = (int)((int64_t)total * (x + 1) / X);
+    next = begin + rank;
+    low_begin = (int)((int64_t)total_low * x / X);
+    low_end = (int)((int64_t)total_low * (x + 1) / X);
+    const int over = (end - begin) % step;
+    short_by = over ? step - over : 0;
+    low_turn = over && rank >= over ? 0 : 2;
+    low_next = low_turn ? low_begin + 2 * short_by + rank : low_begin + rank - over;
+  }
+  __device__ inline void take_low() {
+    ++low_turn;
+    if (low_turn == 1) low_next += short_by;
+    else if (low_turn == 2) low_next = low_begin + 2 * short_by + rank;
+    else low_next += step;
+  }
+};
+
 // Column v of the interleaved halves [gate | up] of an N-column weight: chunks of CW columns, even
 // ones from the gate, odd ones from the up half at N / 2, so that every chunk of gate columns has
 // its up columns beside it in the same MFMA block.
@@ -857,17 +924,6 @@ __device__ inline int64_t gated_column(int64_t v, int64_t N) {
 }
 
 __device__ inline float silu(float v) { return v / (1.0f + __expf(-v)); }
-
-// The positions this workgroup takes: start, start + step, ... below end. The workgroups are dealt
-// to the XCDs round robin; XCD x takes the x-th eighth of the sequence.
-__device__ inline void expert_range(int total, int& start, int& step, int& end) {
-  const int grid = (int)gridDim.x, b = (int)blockIdx.x;
-  const int X = grid < kXcds ? grid : kXcds;
-  const int x = b % X;
-  start = (int)((int64_t)total * x / X) + b / X;
-  end = (int)((int64_t)total * (x + 1) / X);
-  step = (grid - x + X - 1) / X;
-}
 
 // Epilogue of an experts' tile: acc quad (i, j) of this lane holds row qrow(i), columns qcol(j) ..
 // +3 of the tile at rows [lo, hi), columns from n0. fp8: times the row's and the columns' scales.
@@ -988,7 +1044,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
     int ok;
     int job;
     int acq;
-    int first[EPI == kEpiExperts ? AGG_MAX_EXPERTS + 1 : 1];   // experts: prefix of row tiles
+    // experts: prefixes of whole and low row tiles
+    int first[EPI == kEpiExperts ? AGG_MAX_EXPERTS + 1 : 1], low[EPI == kEpiExperts ? AGG_MAX_EXPERTS + 1 : 1];
+    int sums[EPI == kEpiExperts ? 8 : 1];
   };
   static_assert(kStageBytes <= kLdsDmaLimit, "direct-to-LDS destinations must stay below 128 KiB");
   static_assert(__builtin_offsetof(Smem, stages) == 0, "the operand stages start the LDS block");
@@ -1015,20 +1073,29 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
   // workgroups whose first tile is taken statically (pull: all but the copiers at the end)
   const int nstat = (EPI == kEpiAllGather && (a.pull || a.copiers_last)) ? (int)gridDim.x - a.copy_wgs
                                                                         : (int)gridDim.x;
-  int x_next = 0, x_step = 0, x_end = 0;   // experts: this workgroup's tile positions
-  if constexpr (EPI == kEpiExperts) {
-    expert_row_tiles<BM>(a.x, tid, sm.first, sm.tile);
-    expert_range(sm.first[a.x.n_experts] * a.n_col_tiles, x_next, x_step, x_end);
-  }
+  // experts: low tiles exist for the 256-row shapes
+  constexpr bool kLowTiles = EPI == kEpiExperts && BM == 256;
+  [[maybe_unused]] auto deal = [&] {
+    if constexpr (EPI == kEpiExperts) {
+      expert_row_tiles<BM, kLowTiles>(a.x, tid, sm.first, sm.low, sm.sums);
+      return ExpertDeal(sm.first[a.x.n_experts] * a.n_col_tiles, sm.low[a.x.n_experts] * a.n_col_tiles);
+    } else {
+      return 0;
+    }
+  }();
   auto claim_tile = [&](bool first) {
     if constexpr (EPI == kEpiExperts) {
+      const bool low = deal.next >= deal.end;
       if (tid == 0) {
         ExpertTile t{0, -1, 0};
-        if (x_next < x_end) t = expert_tile(sm.first, a.x.n_experts, a.n_col_tiles, x_next);
+        if (!low) t = expert_tile(sm.first, a.x.n_experts, a.n_col_tiles, deal.next);
+        else if (deal.low_next < deal.low_end)
+          t = expert_low_tile(sm.first, sm.low, a.x.n_experts, a.n_col_tiles, deal.low_next);
         s_tile[0] = t.row_tile;
         s_tile[1] = t.col_tile; s_tile[2] = t.expert;
       }
-      x_next += x_step;
+      if (!low) deal.next += deal.step;
+      else deal.take_low();
       __syncthreads();
       return;
     }
@@ -1146,6 +1213,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
         return;  // abandoned (timeout): the tile's output is left as it was
       }
       if (__builtin_amdgcn_readfirstlane(s_acq)) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "");
+
+      // a low tile: rows 0 .. BM/2 - 1, half of a wave's MFMA rows each
+      const bool low = kLowTiles && hi - lo <= BM / 2;
+      const int wave_rows = low ? WTM / 2 : WTM;
 
       // ---- K loop: 64-byte K slices in LDS stages or pair regions, filled by direct-to-LDS loads
       // (out-of-range rows and the K tail read zeros through the buffer descriptor's range check)
@@ -1558,15 +1629,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
           return u32x4{r0[0], r0[1], r1[0], r1[1]};
         };
         auto lda = [&](int sg, int i) {
-          return *reinterpret_cast<const u32x4*>(stages + frag_off(sg, wm * WTM + i * 16 + (lane & 15), lane >> 4));
+          return *reinterpret_cast<const u32x4*>(stages + frag_off(sg, wm * wave_rows + i * 16 + (lane & 15), lane >> 4));
         };
-        run_slices(acc, u32x4{}, lda, ldb,
-                   [](f32x4& c, const u32x4& b, const u32x4& x) { mfma_bf16(c, b, x); },
-                   [](f32x4& c, const u32x4& b, const u32x4& x, const u32x4& d, uint32_t m0v, uint32_t vo) {
-                     mfma_bf16_dma(c, b, x, d, m0v, vo);
-                   },
-                   std::integral_constant<int, FM>{}, std::integral_constant<int, FN>{},
-                   std::integral_constant<bool, false>{});
+        auto run = [&](auto rows) {
+          run_slices(acc, u32x4{}, lda, ldb,
+                     [](f32x4& c, const u32x4& b, const u32x4& x) { mfma_bf16(c, b, x); },
+                     [](f32x4& c, const u32x4& b, const u32x4& x, const u32x4& d, uint32_t m0v, uint32_t vo) {
+                       mfma_bf16_dma(c, b, x, d, m0v, vo);
+                     },
+                     rows, std::integral_constant<int, FN>{}, std::integral_constant<bool, false>{});
+        };
+        if constexpr (kLowTiles) {
+          if (low) run(std::integral_constant<int, FM / 2>{});
+          else run(std::integral_constant<int, FM>{});
+        } else {
+          run(std::integral_constant<int, FM>{});
+        }
       } else {
         // ---- fp8 (e4m3): 32x32x64 MFMA blocks with unit block scales, one 32-byte fragment per
         // lane; the per-tensor scales are applied in the epilogue
@@ -1577,7 +1655,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
           for (int j = 0; j < F8N; ++j) acc8[i][j] = f32x16{};
         // a 32-row fp8 A fragment: row r + (lane & 31), K bytes 32*(lane/32) .. +31 of the slice
         auto lda = [&](int sg, int i) {
-          const int row = wm * WTM + i * 32 + (lane & 31), g = (lane >> 5) * 2;
+          const int row = wm * wave_rows + i * 32 + (lane & 31), g = (lane >> 5) * 2;
           const u32x4 lo4 = *reinterpret_cast<const u32x4*>(stages + frag_off(sg, row, g));
           const u32x4 hi4 = *reinterpret_cast<const u32x4*>(stages + frag_off(sg, row, g + 1));
           return i32x8{(int)lo4[0], (int)lo4[1], (int)lo4[2], (int)lo4[3],
@@ -1597,13 +1675,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
         };
         // a wave with a single 32x32 block reuses its accumulator in the next slice's first
         // MFMA: give the previous one time to write it back
-        run_slices(acc8, i32x8{}, lda, ldb,
-                   [](f32x16& c, const i32x8& b, const i32x8& x) { mfma_fp8(c, b, x); },
-                   [](f32x16& c, const i32x8& b, const i32x8& x, const u32x4& d, uint32_t m0v, uint32_t vo) {
-                     mfma_fp8_dma(c, b, x, d, m0v, vo);
-                   },
-                   std::integral_constant<int, F8M>{}, std::integral_constant<int, F8N>{},
-                   std::integral_constant<bool, (F8M * F8N < 3)>{});
+        auto run = [&](auto rows) {
+          run_slices(acc8, i32x8{}, lda, ldb,
+                     [](f32x16& c, const i32x8& b, const i32x8& x) { mfma_fp8(c, b, x); },
+                     [](f32x16& c, const i32x8& b, const i32x8& x, const u32x4& d, uint32_t m0v, uint32_t vo) {
+                       mfma_fp8_dma(c, b, x, d, m0v, vo);
+                     },
+                     rows, std::integral_constant<int, F8N>{},
+                     std::integral_constant<bool, (decltype(rows)::value * F8N < 3)>{});
+        };
+        if constexpr (kLowTiles) {
+          if (low) run(std::integral_constant<int, F8M / 2>{});
+          else run(std::integral_constant<int, F8M>{});
+        } else {
+          run(std::integral_constant<int, F8M>{});
+        }
         // the epilogue's view: quad q of block (i, j) is acc[i][4j + q]
   #pragma unroll
         for (int i = 0; i < F8M; ++i)
@@ -1618,7 +1704,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
       // ---- epilogue
       // quad (i, j) of this lane: row qrow(i), columns qcol(j) .. qcol(j)+3 of the tile
       auto qrow = [&](int i) {
-        return FP8 ? wm * WTM + i * 32 + (lane & 31) : wm * WTM + i * 16 + (lane & 15);
+        if (kLowTiles && low && i >= FM / 2) return BM;      // (no row: a low tile has half of them)
+        return FP8 ? wm * wave_rows + i * 32 + (lane & 31) : wm * wave_rows + i * 16 + (lane & 15);
       };
       auto qcol = [&](int j) {
         return FP8 ? wn * WTN + (j >> 2) * 32 + (j & 3) * 8 + (lane >> 5) * 4

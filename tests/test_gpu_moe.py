@@ -418,6 +418,23 @@ def test_moe_gemm_every_tile(ctx, tile, dtype, gated):
         B.agg_ctx_set_tile(ctx, 0, 0)
 
 
+@pytest.mark.parametrize("tile", [(256, 224), (256, 256), (128, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_moe_gemm_more_tiles_than_workgroups(ctx, tile, dtype):
+    """Several whole and low tiles a workgroup: each row tile is computed, whatever the experts' last
+    rows are (none, one, half a tile, one more than half)."""
+    B.agg_ctx_set_tile(ctx, *tile)
+    try:
+        rng = np.random.default_rng(3)
+        counts = [int(c) for c in rng.integers(0, 700, 40)] + [0, 1, 128, 129, 256, 257, 384, 385]
+        x = _Experts(counts, 2064, 32, dtype, False, True, spare=2)
+        x.check(x.run(ctx))
+        x = _Experts([1, 128, 3, 0, 77], 4112, 48, dtype, True, False)   # low tiles alone
+        x.check(x.run(ctx))
+    finally:
+        B.agg_ctx_set_tile(ctx, 0, 0)
+
+
 @pytest.mark.parametrize("per,experts", [(1, 2), (12, 3), (30, 3), (60, 2)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 @pytest.mark.parametrize("gated", [False, True])
