@@ -776,7 +776,7 @@ __device__ inline void static_for(F&& f) {
 // tiles is known on the device alone. Every workgroup builds the same prefix sums of row tiles over the
 // experts in LDS, and the tiles are dealt without counters, so nothing has to be cleared between
 // launches. An expert's last row tile, where 256-row tiles would leave more than half of it empty, is a
-// low tile: half the MFMA rows, about half the time. Low tiles come last, first to the workgroups
+// low tile: it has half the MFMA rows, or a quarter where that is enough. Low tiles come last, first to the workgroups
 // that are a whole tile short (ExpertDeal).
 
 // The end of expert e - 1 and the start of expert e, kept inside [0, slots] and in order whatever
@@ -1214,9 +1214,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
       }
       if (__builtin_amdgcn_readfirstlane(s_acq)) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "");
 
-      // a low tile: rows 0 .. BM/2 - 1, half of a wave's MFMA rows each
-      const bool low = kLowTiles && hi - lo <= BM / 2;
-      const int wave_rows = low ? WTM / 2 : WTM;
+      // a low tile: rows 0 .. BM/2 - 1 (low = 1) or 0 .. BM/4 - 1 (low = 2), half or a quarter of a
+      // wave's MFMA rows each
+      constexpr bool kQuarter = kLowTiles && WTM % (4 * BLK) == 0;
+      const int low = !kLowTiles || hi - lo > BM / 2 ? 0 : kQuarter && hi - lo <= BM / 4 ? 2 : 1;
+      const int wave_rows = WTM >> low;
 
       // ---- K loop: 64-byte K slices in LDS stages or pair regions, filled by direct-to-LDS loads
       // (out-of-range rows and the K tail read zeros through the buffer descriptor's range check)
@@ -1640,7 +1642,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
                      rows, std::integral_constant<int, FN>{}, std::integral_constant<bool, false>{});
         };
         if constexpr (kLowTiles) {
-          if (low) run(std::integral_constant<int, FM / 2>{});
+          if (low == 2) run(std::integral_constant<int, FM / 4>{});
+          else if (low) run(std::integral_constant<int, FM / 2>{});
           else run(std::integral_constant<int, FM>{});
         } else {
           run(std::integral_constant<int, FM>{});
@@ -1685,7 +1688,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
                      std::integral_constant<bool, (decltype(rows)::value * F8N < 3)>{});
         };
         if constexpr (kLowTiles) {
-          if (low) run(std::integral_constant<int, F8M / 2>{});
+          if (kQuarter && low == 2) run(std::integral_constant<int, kQuarter ? F8M / 4 : 1>{});
+          else if (low) run(std::integral_constant<int, F8M / 2>{});
           else run(std::integral_constant<int, F8M>{});
         } else {
           run(std::integral_constant<int, F8M>{});
@@ -1704,7 +1708,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
       // ---- epilogue
       // quad (i, j) of this lane: row qrow(i), columns qcol(j) .. qcol(j)+3 of the tile
       auto qrow = [&](int i) {
-        if (kLowTiles && low && i >= FM / 2) return BM;      // (no row: a low tile has half of them)
+        if (kLowTiles && i >= (FM >> low)) return BM;        // (no row: a low tile has fewer of them)
         return FP8 ? wm * wave_rows + i * 32 + (lane & 31) : wm * wave_rows + i * 16 + (lane & 15);
       };
       auto qcol = [&](int j) {

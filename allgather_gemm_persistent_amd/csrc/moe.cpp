@@ -7,53 +7,100 @@
 
 namespace agg {
 
-// The streaming kernel's and the tiles' limits and times below are fits to measured calls of 8
-// experts of 8192 x 7168 and 3584 x 8192, 30 of 1000 x 1032 and 32 of 2048 x 1536, with 1 to 384 rows
-// an expert, bf16 and fp8.
+namespace {
+
+// Microseconds of a tile over all of K: a start and a rate per two bytes of K.
+struct TileTime {
+  double start, rate;
+  double at(double k2) const { return start + rate * k2; }
+};
+
+double ceil_div(double a, double b) { return std::ceil(a / b); }
+
+}  // namespace
+
+// The kernel whose time is expected to be the least. The times are fits to measured calls (8 experts of
+// 8192 x 7168 and 3584 x 8192, 8 of 1024 x 4096, 30 of 1000 x 1032, 32 of 2048 x 1536, 60 of 256 x
+// 2816; 1 to 400 rows an expert, bf16 and fp8) and choose the fastest of the kernels, or one within 10%
+// of it, on 9 of 10 of them. What they stand for, at 8 experts of 8192 x 7168 bf16, us:
+//   rows an expert      4    16    48    96   192   384
+//   streaming         152   159   329   620  1128  2139
+//   256 x 256 tiles   175   174   175   184   211   404
+//   128 x 128         202   207   217   226   377   615
+//   64 x 64           297   309   325   520   710  1277
+// and at 30 of 1000 x 1032, 16 rows: streaming 26, 64 x 64 19, 256 x 256 22.
 ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated, int units) {
   ExpertShape r{false, 0, 1, {64, 64}};
   const bool fp8 = dtype == AGG_FP8_E4M3;
   const int64_t cols = gated ? 2 * n : n;
-  // rows an expert holds if the slots are spread evenly over the experts that can hold any
+  // rows an expert holds if the slots are spread evenly over the experts that can hold any; they scatter
+  // around that
   const int64_t busy = std::max<int64_t>(1, std::min<int64_t>(n_experts, slots));
-  const double rows = double(slots) / double(busy);
-  // Streaming takes 32 rows at a time: up to 16 on average nearly every expert needs one reading of
-  // its weight (bf16 8192 x 7168, 16 rows: 159 us against 207 in tiles of 128 x 128; 24 rows: 261
-  // against 210). A short K leaves each of its 8 waves too few blocks (K = 1000: 25 us against 20).
-  if (rows <= 16 && k * (fp8 ? 1 : 2) >= 2048) {
-    r.stream = true;
-    const int64_t width = fp8 ? 256 : 128;
-    r.strips = int((n + width - 1) / width);
-    // fewer workgroups than 3/4 of the compute units: K in parts of 16 blocks of 32 or more, as many
-    // as fill the units
-    const int64_t groups = busy * r.strips;
-    if (groups * 4 < int64_t(units) * 3 && int64_t(n_experts) * r.strips <= kMoeCounters) {
-      int64_t parts = std::min<int64_t>({units / groups, (k + 511) / 512, 16});
-      parts = std::min(parts, kMoeWsBytes / std::max<int64_t>(1, slots * cols * 4));
-      r.ksplit = int(std::max<int64_t>(parts, 1));
-    }
-    return r;
+  const double rows = double(slots) / double(busy), spread = std::sqrt(rows);
+  const double k2 = double(k) * (fp8 ? 0.5 : 1.0);             // K in units of two bytes
+  const double bytes = double(busy) * double(k) * double(cols) * (fp8 ? 1.0 : 2.0);
+  const double u = units;
+
+  // Streaming: the weights at 6.2 TB/s, or a compute unit's 160 pieces of rows a microsecond; read again
+  // for every 32 rows of the fullest expert. Strips fewer than 3/4 of the units: K in parts of 16 blocks
+  // of 32 or more, as many as fill the units.
+  const int64_t width = fp8 ? 256 : 128;
+  const int64_t strips = (n + width - 1) / width, groups = busy * strips;
+  int64_t parts = 1;
+  if (groups * 4 < int64_t(units) * 3 && int64_t(n_experts) * strips <= kMoeCounters) {
+    parts = std::min<int64_t>({units / groups, (k + 511) / 512, 16});
+    parts = std::max<int64_t>(1, std::min(parts, kMoeWsBytes / std::max<int64_t>(1, slots * cols * 4)));
   }
-  // Tiles: waves of the grid times a wave's microseconds, a start and a rate per 2 bytes of K. An
-  // expert's rows scatter around their mean, so its row tiles are counted at the mean and a deviation
-  // to either side.
-  struct Time { TileShape s; double start, bf16, bf16_gated, fp8, fp8_gated; };
-  static const Time times[] = {
-      {{256, 256}, 14, 0.0245, 0.0245, 0.0185, 0.0195}, {{256, 224}, 14, 0.0215, 0.0250, 0.0190, 0.0225},
-      {{128, 128}, 3, 0.0115, 0.0118, 0.0118, 0.0150},  {{128, 64}, 2, 0.0062, 0.0092, 0.0074, 0.0120},
-      {{64, 64}, 2, 0.0061, 0.0088, 0.0066, 0.0115}};
-  const double spread = 1.2 * std::sqrt(rows);
+  const double passes = ceil_div(rows + 2 * spread, 32);
+  const double stream = passes * std::max(bytes / 6.2e6 + 3, ceil_div(double(groups * parts), u) *
+                                                                 (5.7 + double(k) * (gated ? 2 : 1) / (160.0 * double(parts))));
+
+  // Tiles: waves of the grid times a tile's microseconds, or the weights at 5.4 TB/s. The 256-row shapes
+  // have whole tiles and, for an expert's last 64 or 128 rows, low ones.
+  struct Shape { TileShape s; TileTime whole, half, quarter; };
+  const double g = gated ? 1.25 : 1.0;                         // narrow tiles: gate and up pieces apart
+  const Shape shapes[] = {
+      {{256, 256}, fp8 ? TileTime{22, 0.0247} : TileTime{14, 0.0235}, fp8 ? TileTime{14, 0.016} : TileTime{10, 0.016},
+       fp8 ? TileTime{12.5, 0.0107} : TileTime{9, 0.0128}},
+      {{256, 224}, fp8 ? TileTime{22, 0.0247 * g} : TileTime{13, 0.0206 * (gated ? 1.15 : 1.0)},
+       fp8 ? TileTime{20, 0.024} : TileTime{10, 0.015 * g}, fp8 ? TileTime{20, 0.024} : TileTime{9, 0.0125 * g}},
+      {{128, 128}, {5, fp8 ? 0.0135 : 0.0118}, {}, {}},
+      {{128, 64}, {3, fp8 ? 0.0072 * g : 0.0068 * g}, {}, {}},
+      {{64, 64}, {2.5, fp8 ? 0.0066 * g : 0.0068 * g}, {}, {}}};
   double best = 1e300;
-  for (const Time& t : times) {
-    double per = 0;
-    for (double d : {-spread, 0.0, spread}) per += std::max(1.0, std::ceil((rows + d) / t.s.bm)) / 3;
-    const double tiles = double(busy) * per * double((cols + t.s.bn - 1) / t.s.bn);
-    const double rate = fp8 ? (gated ? t.fp8_gated : t.fp8) : (gated ? t.bf16_gated : t.bf16);
-    const double cost = std::ceil(tiles / units) * (t.start + rate * double(k) * (fp8 ? 0.5 : 1.0));
+  for (const Shape& t : shapes) {
+    const double across = double((cols + t.s.bn - 1) / t.s.bn) * double(busy) / 3.0;
+    double whole = 0, half = 0, quarter = 0;                   // tiles, over rows - spread, rows, rows + spread
+    for (double d : {-spread, 0.0, spread}) {
+      const double held = std::max(1.0, std::ceil(rows + d)), full = std::floor(held / t.s.bm), rest = held - full * t.s.bm;
+      whole += full * across;
+      if (rest == 0) continue;
+      if (t.s.bm < 256 || rest > 128) whole += across;
+      else if (rest > 64) half += across;
+      else quarter += across;
+    }
+    const double tw = t.whole.at(k2), th = t.half.at(k2), tq = t.quarter.at(k2);
+    // (a long launch is bound by power: a partly filled last wave costs its share, not a whole one)
+    const double waves = whole > 2 * u ? whole / u + 0.15 : ceil_div(whole, u), low = half + quarter;
+    double cost = waves * tw;
+    if (low > 0) {
+      // the workgroups that are a whole tile short take up to two low ones, all take the others
+      const double tl = (half * th + quarter * tq) / low, spare = waves * u - whole;
+      const double turns = spare > 0 ? std::min(2.0, ceil_div(low, spare)) : 0.0;
+      const double others = std::max(0.0, ceil_div(low - turns * spare, u));
+      cost = std::max(cost, std::max(waves - 1, 0.0) * tw + turns * tl) + others * tl;
+      cost = std::max({cost, half > 0 ? th : 0.0, quarter > 0 ? tq : 0.0});
+    }
+    cost = std::max(cost, bytes / 5.4e6 + 3);
     if (cost < best) {
       best = cost;
       r.tile = t.s;
     }
+  }
+  if (stream < best) {
+    r.stream = true;
+    r.strips = int(strips);
+    r.ksplit = int(parts);
   }
   return r;
 }
