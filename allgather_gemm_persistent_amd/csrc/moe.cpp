@@ -22,7 +22,8 @@ double ceil_div(double a, double b) { return std::ceil(a / b); }
 // The kernel whose time is expected to be the least. The times are fits to measured calls (8 experts of
 // 8192 x 7168 and 3584 x 8192, 8 of 1024 x 4096, 30 of 1000 x 1032, 32 of 2048 x 1536, 60 of 256 x
 // 2816; 1 to 400 rows an expert, bf16 and fp8) and choose the fastest of the kernels, or one within 10%
-// of it, on 9 of 10 of them. What they stand for, at 8 experts of 8192 x 7168 bf16, us:
+// of it, on 9 of 10 of them (and on 40 random calls within 11% on average, the single runs' noise among
+// it). What they stand for, at 8 experts of 8192 x 7168 bf16, us:
 //   rows an expert      4    16    48    96   192   384
 //   streaming         152   159   329   620  1128  2139
 //   256 x 256 tiles   175   174   175   184   211   404
@@ -51,7 +52,7 @@ ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t
     parts = std::min<int64_t>({units / groups, (k + 511) / 512, 16});
     parts = std::max<int64_t>(1, std::min(parts, kMoeWsBytes / std::max<int64_t>(1, slots * cols * 4)));
   }
-  const double passes = ceil_div(rows + 2 * spread, 32);
+  const double passes = ceil_div(2 * rows + 2 * spread, 32);   // (the fullest of unevenly liked experts)
   const double stream = passes * std::max(bytes / 6.2e6 + 3, ceil_div(double(groups * parts), u) *
                                                                  (5.7 + double(k) * (gated ? 2 : 1) / (160.0 * double(parts))));
 

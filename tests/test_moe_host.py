@@ -144,8 +144,8 @@ def test_kernel_choice(lib):
     assert kind == "stream" and 28 * parts <= 256 < 28 * (parts + 1)
     assert B.agg_moe_gemm_shape("bf16", 32, 8, 3584, 8192, gated=True) == ("stream", 1)
     assert B.agg_moe_gemm_shape("fp8", 32, 8, 3584, 8192, gated=True) == ("stream", 2)
-    assert B.agg_moe_gemm_shape("bf16", 8 * 16, 8, 3584, 8192)[0] == "stream"
-    assert B.agg_moe_gemm_shape("bf16", 8 * 32, 8, 3584, 8192)[0] == "tiles"
+    assert B.agg_moe_gemm_shape("bf16", 8 * 11, 8, 3584, 8192)[0] == "stream"
+    assert B.agg_moe_gemm_shape("bf16", 8 * 16, 8, 3584, 8192)[0] == "tiles"
     # a second wave of strips with few blocks of K each
     assert B.agg_moe_gemm_shape("bf16", 30 * 16, 30, 1032, 1000) == ("tiles", (64, 64))
     # partial sums that would not fit the workspace, more strips than counters: fewer parts
