@@ -626,3 +626,66 @@ def test_split_k_on_more_streams_than_workspaces(ctx):
     torch.cuda.synchronize()
     for x, out in zip(xs, outs):
         x.check(out)
+
+
+@pytest.mark.parametrize("T", [1, 9, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("held", [8, 4])
+def test_moe_layer(gpu, T, dtype, held):
+    """The layer from the residual stream to the rank's partial sum. The steps between the operators
+    round to bf16 or e4m3, so each is compared from the rows that entered it."""
+    from allgather_gemm_persistent_amd.moe_layer import random_layer
+    H, F, E, k = 256, 128, 8, 2
+    layer = random_layer(T + 3, H, F, E, k, dtype, n_local=held, first=E - held, seed=T, score="sigmoid",
+                         bias=torch.linspace(-0.1, 0.1, E))
+    try:
+        g = _gen(T)
+        x, r = torch.randn(T, H, generator=g), torch.randn(T, H, generator=g).bfloat16()
+        residual = r.cuda()
+        out = layer.run(x.cuda(), residual).cpu()
+        s, y = _norm_ref(x, r, layer.norm.cpu(), 1e-6)
+        _within(residual, s, s.abs() * (HALF_BF16 + EPS32), "residual")
+        xn = layer.x[:T].cpu()
+        _within(xn, y, y.abs() * (HALF_BF16 + H * EPS32 + FINE) + 1e-30, "norm")
+        logits = layer.logits[:T].cpu()
+        ref = xn.double() @ layer.router.double().cpu()
+        size = xn.double().abs() @ layer.router.double().cpu().abs()
+        _within(logits, ref, ref.abs() * HALF_BF16 + size * H * EPS32 + 1e-30, "logits")
+        ids, w = layer.ids[:T].cpu(), layer.weights[:T].cpu().double()
+        want_ids, want_w = _route_ref(logits.double().numpy(), np.linspace(-0.1, 0.1, E, dtype=np.float32).astype(np.float64),
+                                      "sigmoid", 1, 1, k, True, 1.0)
+        assert (ids.numpy() == want_ids).all()
+        assert (np.abs(w.numpy() - want_w) <= want_w * (E * EPS32 + FINE)).all()
+        # the products from what the layer itself quantised or rounded before them
+        ref, size = torch.zeros(T, H, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
+        slot = layer.token_slot[:T].cpu() if T == layer.tokens else layer.token_slot.view(-1)[:T * k].view(T, k).cpu()
+        for t in range(T):
+            for j in range(k):
+                e = int(ids[t, j]) - (E - held)
+                if e < 0:
+                    assert slot[t, j] == -1
+                    continue
+                m = int(slot[t, j])
+                if dtype == "fp8":
+                    a = layer.x8[t].cpu().double() * float(layer.x_scale[t])
+                    up = layer.w_up[e].cpu().double() * layer.up_scale[e].cpu().double()
+                    down = layer.w_down[e].cpu().double() * layer.down_scale[e].cpu().double()
+                    mid = layer.mid8[m].cpu().double() * float(layer.mid_scale[m])
+                else:
+                    a, up, down = xn[t].double(), layer.w_up[e].cpu().double(), layer.w_down[e].cpu().double()
+                    mid = layer.mid[m].cpu().double()
+                z, zs = a @ up, a.abs() @ up.abs()
+                act = z[:F] * torch.sigmoid(z[:F])
+                cut = FP8_SUM if dtype == "fp8" else 0
+                err = zs * (H * EPS32 + FINE + cut)
+                bound = 1.1 * err[:F] * (z[F:].abs() + err[F:]) + act.abs() * err[F:] + (act * z[F:]).abs() * (FINE + HALF_BF16)
+                _within(layer.mid[m].cpu(), act * z[F:], 1.01 * bound + 1e-30, "between the products")
+                y = mid @ down
+                ref[t] += w[t, j] * y
+                size[t] += w[t, j] * (y.abs() * HALF_BF16 + (mid.abs() @ down.abs()) * (F * EPS32 + FINE + cut))
+        _within(out, ref, 1.01 * size + ref.abs() * 4 * EPS32 + 1e-30, "the layer")
+        assert layer.run(x[:0].cuda()).shape == (0, H)
+        with pytest.raises(B.AggError):
+            layer.run(torch.zeros(T + 4, H, device="cuda"))
+    finally:
+        layer.close()
