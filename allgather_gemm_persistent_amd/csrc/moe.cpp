@@ -82,8 +82,10 @@ ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t
     }
     const double tw = t.whole.at(k2), th = t.half.at(k2), tq = t.quarter.at(k2);
     // (a long launch is bound by power: a partly filled last wave costs its share, not a whole one)
-    const double waves = whole > 2 * u ? whole / u + 0.15 : ceil_div(whole, u), low = half + quarter;
+    const double waves = whole > 2 * u && t.s.bm > 64 ? whole / u + 0.15 : ceil_div(whole, u), low = half + quarter;
     double cost = waves * tw;
+    // (64 x 64 tiles run two to a compute unit: later ones save most of their start)
+    if (t.s.bm == 64) cost -= (waves - 1) * std::min(2.5, 0.45 * tw);
     if (low > 0) {
       // the workgroups that are a whole tile short take up to two low ones, all take the others
       const double tl = (half * th + quarter * tq) / low, spare = waves * u - whole;

@@ -111,9 +111,14 @@ extern "C" int moe_gemm(agg_ctx* ctx, int64_t slots, int n_experts, int64_t n, i
   g.n_lists = g.list_cols = 1;
   g.scale = 1.0f;
   g.x = x;
-  // no more workgroups than there can be tiles: every expert rounds its last row tile up
-  const int64_t most = (slots / shape.tile.bm + n_experts) * int64_t(g.n_col_tiles);
-  const int grid = int(most < units ? most : units);
+  // no more workgroups than there can be tiles (every expert rounds its last row tile up), the same on
+  // every XCD: the tiles are dealt to the XCDs in eighths
+  int64_t most = (slots / shape.tile.bm + n_experts) * int64_t(g.n_col_tiles);
+  most = (most + kXcds - 1) / kXcds * kXcds;
+  // (64 x 64 tiles: two workgroups fit on a compute unit, so one's start and end hide behind the other's
+  // main loop)
+  const int64_t room = int64_t(units) * (shape.tile.bm == 64 ? 2 : 1);
+  const int grid = int(most < room ? most : room);
   HIP_TRY(launch_expert_tiles(g, shape.tile.bm, shape.tile.bn, dtype, grid, S(stream)));
   return AGG_OK;
 }
