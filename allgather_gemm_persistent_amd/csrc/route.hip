@@ -376,7 +376,7 @@ hipError_t launch_route(const RouteArgs& a, int cus, hipStream_t stream) {
 // Pair p = token * top_k + choice goes into the bucket of its expert, or, where the expert is not
 // one of this rank's n_local (or is -1), into a last bucket that gets no slot. Blocks of kPlanPairs
 // pairs: the first kernel counts each block's buckets, the second adds up what comes before its
-// block and gives every pair its place. One block needs the second kernel alone. Counts are sums
+// block and gives every pair its place; up to kPlanAlone pairs the second does without the first. Counts are sums
 // of ones, so no order of additions changes them, and the places follow the pairs' order.
 
 namespace {
@@ -389,6 +389,7 @@ __device__ inline int bucket_of(const PlanArgs& a, int64_t p) {
 }  // namespace
 
 constexpr int kPlanThreads = 1024;
+constexpr int64_t kPlanAlone = 12 * kPlanPairs;
 
 // Block b of R * kPlanPairs pairs.
 template <int R>
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs
   for (int e = threadIdx.x; e < buckets; e += kPlanThreads) a.work[(int64_t)blockIdx.x * buckets + e] = count[e];
 }
 
-template <int R>
+template <int R, bool ALONE>
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs a) {
   constexpr int W = kPlanThreads / 64;               // waves
   __shared__ int count[W][AGG_MAX_EXPERTS + 1];      // pairs of this block, by wave and bucket
@@ -445,7 +446,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
   }
 
   // totals of every bucket and what the blocks before this one hold of it
-  if (blocks > 1) {
+  if (ALONE && blocks > 1) {
+    // from the pairs themselves, kBatch loads on their way together
+    constexpr int kBatch = 8;
+    const int pairs = (int)a.pairs, mine = block * R * kPlanPairs;
+    for (int p0 = tid; p0 < pairs; p0 += kPlanThreads * kBatch) {
+      int b[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) b[u] = p0 + u * kPlanThreads < pairs ? bucket_of(a, p0 + u * kPlanThreads) : -1;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (b[u] < 0) continue;
+        atomicAdd(p0 + u * kPlanThreads < mine ? &place[b[u]] : &total[b[u]], 1);
+      }
+    }
+    __syncthreads();
+    for (int e = tid; e < buckets; e += kPlanThreads) total[e] += place[e];
+    __syncthreads();
+  } else if (blocks > 1) {
     // kBatch loads on their way together; a thread steps through (block, bucket) by kPlanThreads
     constexpr int kBatch = 8;
     int e = tid % buckets, b = tid / buckets;
@@ -515,23 +533,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
   }
 }
 
-template <int R>
+template <int R, bool ALONE>
 static hipError_t launch_plan_r(const PlanArgs& a, hipStream_t stream) {
   const int64_t blocks = a.pairs > 0 ? (a.pairs + R * kPlanPairs - 1) / (R * kPlanPairs) : 1;
-  if (blocks > 1) {
+  if (!ALONE) {
     hipLaunchKernelGGL(plan_count_kernel<R>, dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  hipLaunchKernelGGL(plan_place_kernel<R>, dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, a);
+  hipLaunchKernelGGL((plan_place_kernel<R, ALONE>), dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 // Every block reads every block's counts, so large plans take larger blocks.
 hipError_t launch_plan(const PlanArgs& a, hipStream_t stream) {
   static_assert(kPlanThreads == kPlanPairs, "a pair a thread and round");
-  if (a.pairs <= 128 * kPlanPairs) return launch_plan_r<1>(a, stream);
-  if (a.pairs <= 256 * kPlanPairs) return launch_plan_r<2>(a, stream);
-  return launch_plan_r<4>(a, stream);
+  // few pairs: every block counts them all itself, cheaper than the launch that would count them once
+  if (a.pairs <= kPlanAlone) return launch_plan_r<1, true>(a, stream);
+  if (a.pairs <= 128 * kPlanPairs) return launch_plan_r<1, false>(a, stream);
+  if (a.pairs <= 256 * kPlanPairs) return launch_plan_r<2, false>(a, stream);
+  return launch_plan_r<4, false>(a, stream);
 }
 
 }  // namespace agg
