@@ -139,6 +139,10 @@ struct agg_ctx {
                                              //   counters are in the device's static scratch)
   hipEvent_t ev_upload = nullptr;
   bool upload_pending = false;
+  // the stream of the last call that used the ctx's scratch, and the event a call on another one waits for
+  hipStream_t last_stream = nullptr;
+  bool any_call = false;
+  hipEvent_t ev_order = nullptr;
   // moe_gemm's workspaces, each the counters and then the partial sums, and the streams they belong to
   uint8_t* moe_ws = nullptr;
   agg_stream moe_stream[kMoeWorkspaces] = {};
@@ -260,6 +264,30 @@ int grid_for(agg_ctx* ctx, int64_t tiles, bool overlapped) {
   int64_t units = ctx->cus - (overlapped ? ctx->reserved_cus : 0);
   int64_t g = std::min<int64_t>(std::max<int64_t>(units, 1), tiles);
   return int(std::max<int64_t>(g, 1));
+}
+
+// A ctx serialises its calls, which share its scratch: a call on another stream than the last one's
+// starts after it. Under a stream capture the order is the caller's (an event recorded outside a
+// capture cannot be waited for inside it).
+int order_calls(agg_ctx* ctx, hipStream_t s) {
+  const hipStream_t last = ctx->last_stream;
+  if (ctx->any_call && last != s) {
+    auto capturing = [](hipStream_t x) {
+      hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+      return x && hipStreamIsCapturing(x, &st) == hipSuccess && st != hipStreamCaptureStatusNone;
+    };
+    if (!capturing(s) && !capturing(last)) {
+      if (hipEventRecord(ctx->ev_order, last) == hipSuccess) {
+        HIP_TRY(hipStreamWaitEvent(s, ctx->ev_order, 0));
+      } else {
+        (void)hipGetLastError();               // (the last call's stream is gone)
+        HIP_TRY(hipDeviceSynchronize());
+      }
+    }
+  }
+  ctx->last_stream = s;
+  ctx->any_call = true;
+  return AGG_OK;
 }
 
 // Stream choreography shared by ag_gemm and gemm_rs. `launch` enqueues the consumer kernel on
@@ -709,14 +737,19 @@ extern "C" int agg_ctx_create(int device, agg_ctx** out) {
   step(hipEventCreateWithFlags(&ctx->ev_kernel, hipEventDisableTiming), "hipEventCreate");
   step(hipEventCreateWithFlags(&ctx->ev_user, hipEventDisableTiming), "hipEventCreate");
   step(hipEventCreateWithFlags(&ctx->ev_upload, hipEventDisableTiming), "hipEventCreate");
+  step(hipEventCreateWithFlags(&ctx->ev_order, hipEventDisableTiming), "hipEventCreate");
   for (int j = 0; j < kMaxCopyStreams; ++j)
     step(hipEventCreateWithFlags(&ctx->ev_copy[j], hipEventDisableTiming), "hipEventCreate");
   if (rc == AGG_OK) step(make_own_queue_stream(ctx, &ctx->ks), "hipExtStreamCreateWithCUMask");
   step(hipHostMalloc(reinterpret_cast<void**>(&ctx->up_host), kTabHostWords * sizeof(uint32_t)),
        "hipHostMalloc(tables)");
   step(hipMalloc(reinterpret_cast<void**>(&ctx->moe_ws), kMoeWorkspaces * kMoeWsStride), "hipMalloc(moe workspaces)");
-  for (int j = 0; j < kMoeWorkspaces && rc == AGG_OK; ++j)
-    step(hipMemset(ctx->moe_ws + j * kMoeWsStride, 0, size_t(kMoeCounters) * 4), "hipMemset(moe counters)");
+  if (rc == AGG_OK) {
+    const std::vector<uint32_t> zeros(kMoeCounters, 0u);
+    for (int j = 0; j < kMoeWorkspaces; ++j)
+      step(hipMemcpy(ctx->moe_ws + j * kMoeWsStride, zeros.data(), zeros.size() * sizeof(uint32_t), hipMemcpyHostToDevice),
+           "hipMemcpy(moe counters)");
+  }
   if (rc == AGG_OK) rc = static_scratch_setup(device);
   step(hipSetDevice(prev), "hipSetDevice");
   if (rc != AGG_OK) {
@@ -758,7 +791,7 @@ extern "C" int agg_ctx_destroy(agg_ctx* ctx) {
   step(hipSetDevice(ctx->device), "hipSetDevice");
   step(hipDeviceSynchronize(), "hipDeviceSynchronize");
   if (ctx->scratch) step(hipFree(ctx->scratch), "hipFree(scratch)");
-  for (hipEvent_t e : {ctx->ev_fork, ctx->ev_kernel, ctx->ev_user, ctx->ev_upload})
+  for (hipEvent_t e : {ctx->ev_fork, ctx->ev_kernel, ctx->ev_user, ctx->ev_upload, ctx->ev_order})
     if (e) step(hipEventDestroy(e), "hipEventDestroy");
   if (ctx->up_host) step(hipHostFree(ctx->up_host), "hipHostFree");
   if (ctx->ws) step(hipFree(ctx->ws), "hipFree(ws)");
@@ -789,6 +822,8 @@ extern "C" int agg_ctx_reset(agg_ctx* ctx, agg_stream stream) {
   }
   HIP_TRY(launch_fill_u32(ctx->scratch, kScrWords, 0u, S(stream)));
   HIP_TRY(launch_fill_u32(ctx->scratch + kScrFailed, 1, 0xFFFFFFFFu, S(stream)));
+  for (int j = 0; j < kMoeWorkspaces; ++j)
+    HIP_TRY(launch_fill_u32(reinterpret_cast<uint32_t*>(ctx->moe_ws + j * kMoeWsStride), kMoeCounters, 0u, S(stream)));
   if (ctx->used_static) {
     // the device's static scratch too (shared by every ctx on the device)
     std::lock_guard<std::mutex> lock(g_static_mu);
@@ -1020,6 +1055,7 @@ int ag_gemm_impl(agg_ctx* ctx, int world, int rank, int64_t m_shard, int64_t n, 
   if ((m + ts.bm - 1) / ts.bm > AGG_MAX_ROW_TILES)
     return fail(AGG_E_UNSUPPORTED, "%lld row tiles exceed %d", (long long)((m + ts.bm - 1) / ts.bm), AGG_MAX_ROW_TILES);
   HIP_TRY(hipSetDevice(ctx->device));
+  if (int rc = order_calls(ctx, S(stream))) return rc;
   const int cps = int(m_shard / chunk_rows);
   if (world > 1)
     if (int rc = bind_flags(ctx, kFlagsAg, flags, size_t(world) * cps)) return rc;
@@ -1277,6 +1313,7 @@ extern "C" int gemm_rs(agg_ctx* ctx, int world, int rank, int64_t m, int64_t n, 
   if (world * ((mb + ts.bm - 1) / ts.bm) > AGG_MAX_ROW_TILES)
     return fail(AGG_E_UNSUPPORTED, "row tiles exceed %d", AGG_MAX_ROW_TILES);
   HIP_TRY(hipSetDevice(ctx->device));
+  if (int rc = order_calls(ctx, S(stream))) return rc;
   const int cpb = int(mb / chunk_rows);
   if (world > 1) {
     if (int rc = bind_flags(ctx, kFlagsRsRecv, flags, size_t(world) * cpb)) return rc;
@@ -1405,6 +1442,7 @@ extern "C" int gemm_ar(agg_ctx* ctx, int world, int rank, int64_t m, int64_t n, 
   const TileShape ts = tile_for(ctx, 2, AGG_BF16, m, n, k);
   if ((m + ts.bm - 1) / ts.bm > AGG_MAX_ROW_TILES) return fail(AGG_E_UNSUPPORTED, "row tiles exceed %d", AGG_MAX_ROW_TILES);
   HIP_TRY(hipSetDevice(ctx->device));
+  if (int rc = order_calls(ctx, S(stream))) return rc;
   const int cpb = int(m / chunk_rows);
   if (world > 1) {
     if (int rc = bind_flags(ctx, kFlagsArRecv, flags, size_t(world) * cpb)) return rc;
@@ -1542,6 +1580,7 @@ extern "C" int ffn_chain(agg_ctx* ctx, int world, int rank, int64_t m_shard, int
   if ((m + ts.bm - 1) / ts.bm * 2 + world > AGG_MAX_ROW_TILES)
     return fail(AGG_E_UNSUPPORTED, "row tiles exceed %d", AGG_MAX_ROW_TILES);
   HIP_TRY(hipSetDevice(ctx->device));
+  if (int rc = order_calls(ctx, S(stream))) return rc;
   if (world > 1) {
     if (int rc = bind_flags(ctx, kFlagsAg, flags, size_t(world) * cps)) return rc;
     if (int rc = bind_flags(ctx, kFlagsRsRecv, rs_flags, size_t(world) * cpb)) return rc;

@@ -96,8 +96,8 @@ enum agg_mode {
 /* ---- context -------------------------------------------------------------------------- */
 
 /* Create a ctx on HIP device `device`. Allocates the ctx's device scratch (claim counters, status
- * word, completion counters and the tables the kernel reads, 78 KiB) and pinned host staging for
- * those tables, creates its kernel stream, and, for the first ctx on a device, finds and clears
+ * word, completion counters and the tables the kernel reads, 78 KiB), moe_gemm's workspaces (32 MiB)
+ * and pinned host staging for those tables, creates its kernel stream, and, for the first ctx on a device, finds and clears
  * that device's static scratch (ag_gemm_noalloc). AGG_E_UNSUPPORTED unless the device's
  * architecture is gfx950.
  * Passage: section "The first move was to expose the overlap": symmetric memory and signaling as

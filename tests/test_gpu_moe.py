@@ -689,3 +689,30 @@ def test_moe_layer(gpu, T, dtype, held):
             layer.run(torch.zeros(T + 4, H, device="cuda"))
     finally:
         layer.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_split_k_in_a_replayed_graph_and_after_reset(ctx, dtype):
+    """K in parts, captured and replayed between eager calls of other rows; then after a reset."""
+    x = _Experts([1, 3], 256, 4096, dtype, True, True, seed=5)
+    assert B.agg_moe_gemm_shape(dtype, 4, 2, 256, 4096, True)[1] > 1
+    want = x.run(ctx)
+    x.check(want)
+    a, b, off, tok, sa, sb = x.held
+    out = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_gemm(ctx, 4, 2, 256, 4096, dtype, a, b, off, out, gated=True, slot_token=tok, a_scale=sa, b_scale=sb,
+                   stream=torch.cuda.current_stream())
+    first = tok.clone()
+    for i in range(5):
+        perm = torch.tensor([0, 1 + (1 + i) % 3, 1 + (2 + i) % 3, 1 + i % 3], device="cuda")
+        tok.copy_(first[perm])
+        out.fill_(5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[perm]), i
+        x.check(x.run(ctx))
+    B.agg_ctx_reset(ctx, torch.cuda.current_stream())
+    assert torch.equal(x.run(ctx), want)
