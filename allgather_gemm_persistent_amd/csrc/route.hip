@@ -8,6 +8,8 @@ namespace agg {
 
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 constexpr float kNone = -__builtin_inff();   // the key of an expert that cannot be chosen
 
 // The value of another lane of the same token: step 0 exchanges neighbours, step 1 pairs, step 2
@@ -72,38 +74,49 @@ __device__ inline int group_rank(const float* score, int groups, int g) {
   return before;
 }
 
-// Drop the keys of the groups that do not stay, where group g is the G rows of experts g * G .. of a
-// lane: its two largest keys meet over the lanes in registers. `score`: the token's room in LDS.
-template <int STEPS, int V, int G>
-__device__ inline void keep_groups(float (&key)[V], int sigmoid, int top_groups, float* score, int lane) {
-  constexpr int L = 1 << STEPS, N = V / G;
-  if constexpr (N >= 1) {
+// Drop the keys of the groups that do not stay, where a token's L * V experts fill its lanes and the
+// groups' sizes are powers of two, no less than L and V. The keys cross LDS, so that lane i gets the V
+// consecutive experts from i * V (padded by 16 bytes, which puts the lanes' 16-byte reads on different
+// banks), all of one group; a group's lanes are neighbours. `room`: the token's LDS, L * (V + 4) floats;
+// `score`: its groups' scores. (8 groups of 256 experts: 213 vector instructions a wave, 353 where each
+// group's members are read from LDS one at a time; 19.8 us and 23.5 for the kernel at 32768 tokens.)
+template <int STEPS, int V>
+__device__ inline void keep_groups(float (&key)[V], int sigmoid, int groups, int top_groups, float* room,
+                                   float* score, int lane) {
+  constexpr int L = 1 << STEPS;
+  static_assert(L >= V, "a row of experts across the lanes is whole chunks");
 #pragma unroll
-    for (int g = 0; g < N; ++g) {
-      float b0 = key[g * G], b1 = kNone;
+  for (int v = 0; v < V; ++v) room[v * (L + L / V * 4) + lane + lane / V * 4] = key[v];
+  wave_sync();
+  float b0 = kNone, b1 = kNone;
 #pragma unroll
-      for (int i = 1; i < G; ++i) {
-        b1 = fmaxf(b1, fminf(b0, key[g * G + i]));
-        b0 = fmaxf(b0, key[g * G + i]);
-      }
-      each_step<0, STEPS>([&](auto i) {
-        const float o0 = __builtin_bit_cast(float, other_lane<decltype(i)::value>(__builtin_bit_cast(int, b0)));
-        const float o1 = __builtin_bit_cast(float, other_lane<decltype(i)::value>(__builtin_bit_cast(int, b1)));
-        b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
-        b0 = fmaxf(b0, o0);
-      });
-      if (lane == g % L) score[g] = group_key(sigmoid, b0, b1);
+  for (int q = 0; q < V / 4; ++q) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(room + lane * (V + 4) + q * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      b1 = __builtin_amdgcn_fmed3f(b0, b1, x[i]);        // (b1 <= b0: the new second)
+      b0 = fmaxf(b0, x[i]);
     }
-    wave_sync();
-    uint32_t kept = 0;
-#pragma unroll
-    for (int g0 = 0; g0 < N; g0 += L)
-      if (g0 + lane < N && group_rank(score, N, g0 + lane) < top_groups) kept |= 1u << (g0 + lane);
-    each_step<0, STEPS>([&](auto i) { kept |= (uint32_t)other_lane<decltype(i)::value>((int)kept); });
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (!(kept & (1u << (v / G)))) key[v] = kNone;
   }
+  const int parts = L / groups;
+  each_step<0, STEPS>([&](auto i) {
+    if ((1 << decltype(i)::value) < parts) {
+      const float o0 = __builtin_bit_cast(float, other_lane<decltype(i)::value>(__builtin_bit_cast(int, b0)));
+      const float o1 = __builtin_bit_cast(float, other_lane<decltype(i)::value>(__builtin_bit_cast(int, b1)));
+      b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
+      b0 = fmaxf(b0, o0);
+    }
+  });
+  const int g = lane / parts;
+  if (lane % parts == 0) score[g] = group_key(sigmoid, b0, b1);
+  wave_sync();
+  uint32_t kept = lane % parts == 0 && group_rank(score, groups, g) < top_groups ? 1u << g : 0u;
+  each_step<0, STEPS>([&](auto i) { kept |= (uint32_t)other_lane<decltype(i)::value>((int)kept); });
+  // (v * L / size is the same on all lanes)
+  const int shift = __builtin_ctz((uint32_t)(L * V / groups));
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (!(kept & (1u << ((v * L) >> shift)))) key[v] = kNone;
 }
 
 }  // namespace
@@ -118,13 +131,14 @@ __device__ inline void keep_groups(float (&key)[V], int sigmoid, int top_groups,
 // (key, lowest index) one after another, a picked key becoming kNone. Chosen experts' scores are
 // computed again from their logits, by the lane that writes them.
 //
-// Bound by instructions at many tokens (the sigmoid first): 32768 tokens of 256 experts in fp32 are
-// 33.6 MB, 5 us of reading.
-template <int STEPS, int V, bool BF16>
+// Bound by instructions at many tokens: 32768 tokens of 256 experts in fp32 are 33.6 MB, 6.6 us of
+// copying. 6.2 us for top 1 over softmax, 13.3 for top 8, 16.5 over the sigmoid, 17.6 with a bias, 19.8
+// with 8 groups of which 4 stay. FULL drops the bounds of experts that fill the lanes.
+template <int STEPS, int V, bool BF16, bool FULL>
 __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
   constexpr int L = 1 << STEPS, TOKENS = 256 / L, E = L * V;
   constexpr int OUT = AGG_MAX_TOP_K > L ? AGG_MAX_TOP_K / L : 1;   // choices a lane writes
-  __shared__ float keys[TOKENS][E + 1];
+  __shared__ __attribute__((aligned(16))) float keys[TOKENS][L * (V + 4)];
   __shared__ float group_score[TOKENS][AGG_MAX_GROUPS];
   constexpr int LIST = 2 * L;               // candidates a token's list holds
   struct __attribute__((aligned(8))) Candidate {
@@ -146,7 +160,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
   for (int v = 0; v < V; ++v) {
     const int e = v * L + lane;
     float x = kNone;
-    if (live && e < a.experts) x = logit(e);
+    if (live && (FULL || e < a.experts)) x = logit(e);
     if (x != x) x = kNone;                  // a NaN logit: never chosen
     key[v] = x;
     top = fmaxf(top, x);
@@ -189,21 +203,18 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = v * L + lane;
-      if (e < a.experts) key[v] += a.bias[e];
+      if (FULL || e < a.experts) key[v] += a.bias[e];
       if (key[v] != key[v]) key[v] = kNone;
     }
   }
 
   if (a.groups > 1) {
     const int size = a.experts / a.groups;
-    // groups of one, two or four whole rows of experts across the lanes: scored in registers;
-    // others: through LDS
-    const bool whole = a.experts == E && size % L == 0 && a.groups <= 32;
     uint32_t kept[2] = {0, 0};              // a bit for each group that stays
-    if (whole && size == L) keep_groups<STEPS, V, 1>(key, a.sigmoid, a.top_groups, group_score[slot], lane);
-    else if (whole && size == 2 * L) keep_groups<STEPS, V, 2>(key, a.sigmoid, a.top_groups, group_score[slot], lane);
-    else if (whole && size == 4 * L) keep_groups<STEPS, V, 4>(key, a.sigmoid, a.top_groups, group_score[slot], lane);
-    else {
+    // (64 .. 1024 experts and up to 8 or 16 groups, both powers of two; else one member after another)
+    if (FULL && (a.groups & (a.groups - 1)) == 0 && a.groups <= (L < V ? L : V)) {
+      keep_groups<STEPS, V>(key, a.sigmoid, a.groups, a.top_groups, keys[slot], group_score[slot], lane);
+    } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int e = v * L + lane;
@@ -357,8 +368,14 @@ template <int STEPS, int V>
 static hipError_t launch_route_lv(const RouteArgs& a, hipStream_t stream) {
   constexpr int64_t tokens = 256 >> STEPS;
   const dim3 grid((unsigned)((a.tokens + tokens - 1) / tokens)), block(256);
-  if (a.logits_bf16) hipLaunchKernelGGL((route_kernel<STEPS, V, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((route_kernel<STEPS, V, false>), grid, block, 0, stream, a);
+  const bool full = a.experts == (V << STEPS);    // no lane without an expert
+  if (a.logits_bf16) {
+    if (full) hipLaunchKernelGGL((route_kernel<STEPS, V, true, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((route_kernel<STEPS, V, true, false>), grid, block, 0, stream, a);
+  } else {
+    if (full) hipLaunchKernelGGL((route_kernel<STEPS, V, false, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((route_kernel<STEPS, V, false, false>), grid, block, 0, stream, a);
+  }
   return hipGetLastError();
 }
 
