@@ -776,8 +776,13 @@ __device__ inline void static_for(F&& f) {
 // tiles is known on the device alone. Every workgroup builds the same prefix sums of row tiles over the
 // experts in LDS, and the tiles are dealt without counters, so nothing has to be cleared between
 // launches. An expert's last row tile, where 256-row tiles would leave more than half of it empty, is a
-// low tile: it has half the MFMA rows, or a quarter where that is enough. Low tiles come last, first to the workgroups
-// that are a whole tile short (ExpertDeal).
+// low tile: it has half the MFMA rows, or a quarter where that is enough. Low tiles come last, first to
+// the workgroups that are a whole tile short (ExpertDeal).
+//
+// Bound by the matrix units and the power that they draw: 10240 rows over 8 experts of 8192 x 7168 bf16,
+// gated, take 971 us (1239 TFLOP/s, what the library reaches on one 8192^3 product; the matrix units are
+// busy 0.69 of the cycles at 1.77 GHz), 16384 rows in fp8 826-850 us (2330, the library's 8192^3 2750;
+// busy 0.60 at 1.72 GHz, and seven to eight tiles a workgroup, of which the last is not full).
 
 // The end of expert e - 1 and the start of expert e, kept inside [0, slots] and in order whatever
 // the array holds, so that no store leaves `out`.
