@@ -247,6 +247,30 @@ def test_route(ctx, T, E, k, groups, top_groups, dtype, score, renorm):
     assert (np.abs(w - want_w) <= want_w * (E * EPS32 + FINE)).all(), np.abs(w - want_w).max()
 
 
+@pytest.mark.parametrize("E", [64, 128, 256, 512, 1024])
+@pytest.mark.parametrize("groups", [2, 4, 8, 16, 32])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups(ctx, E, groups, score):
+    """Few candidates, so that groups hold none, one or several: 16 values of logits, whose sigmoids'
+    sums of two are equal or far apart, most experts disabled, whole groups and the last experts among
+    them."""
+    T, k, top_groups = 37, 6, max(1, groups // 3)
+    values = torch.randn(16, generator=_gen(groups)).sort().values
+    sums = torch.sort((values.double().sigmoid()[:, None] + values.double().sigmoid()[None, :]).reshape(-1)).values
+    gap = sums.diff()
+    assert gap[gap > 1e-12].min() > 1e-6
+    x = values[torch.randint(0, 16, (T, E), generator=_gen(E))]
+    x[torch.rand(T, E, generator=_gen(E + 1)) < 0.9] = -math.inf
+    x[5, E // groups:] = -math.inf
+    x[6, :E - E // groups] = -math.inf
+    x[7] = -math.inf
+    x[7, E - 1] = 0.5
+    want_ids, want_w = _route_ref(x.double().numpy(), None, score, groups, top_groups, k, True, 1.0)
+    ids, w = _run_route(ctx, x.cuda(), k, score=score, groups=groups, top_groups=top_groups)
+    np.testing.assert_array_equal(ids, want_ids)
+    assert (np.abs(w - want_w) <= want_w * (E * EPS32 + FINE)).all(), np.abs(w - want_w).max()
+
+
 @pytest.mark.parametrize("T,E,k,groups,top_groups", [(70, 64, 4, 1, 1), (33, 256, 8, 8, 4), (9, 1024, 8, 16, 2)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_bias(ctx, T, E, k, groups, top_groups, score):
