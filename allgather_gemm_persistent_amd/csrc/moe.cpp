@@ -123,6 +123,7 @@ int need(const void* p, const char* what) {
 }
 
 constexpr int64_t kMostRows = int64_t(1) << 30;
+constexpr int64_t kMostStride = int64_t(1) << 31;
 
 #define CHECK(expr)                  \
   do {                               \
@@ -132,6 +133,7 @@ constexpr int64_t kMostRows = int64_t(1) << 30;
 // elements from one row to the next: at least `cols`, and rows that start on 16 bytes
 int check_stride(int64_t ld, int64_t cols, int elem, const char* what) {
   if (ld < cols) return fail(AGG_E_ARG, "%s: a row stride of %lld is below the %lld columns", what, (long long)ld, (long long)cols);
+  if (ld > kMostStride) return fail(AGG_E_UNSUPPORTED, "%s: a row stride of %lld is beyond 2^31", what, (long long)ld);
   if ((ld * elem) % 16) return fail(AGG_E_ARG, "%s: a row stride of %lld bytes is not a multiple of 16", what, (long long)(ld * elem));
   return AGG_OK;
 }
@@ -157,6 +159,7 @@ extern "C" int agg_check_norm_args(int64_t rows, int64_t cols, int x_dtype, cons
   CHECK(need(x, "x"));
   CHECK(need(out, "out"));
   CHECK(check_stride(ld_x, cols, x_dtype == AGG_FP32 ? 4 : 2, "x"));
+  if (ld_out > kMostStride) return fail(AGG_E_UNSUPPORTED, "out: a row stride of %lld is beyond 2^31", (long long)ld_out);
   if (ld_out < cols || ld_out % 8) return fail(AGG_E_ARG, "out: a row stride of %lld is below the columns or no multiple of 8", (long long)ld_out);
   if (weight && misaligned(weight)) return fail(AGG_E_ARG, "weight is not 16-byte aligned");
   if (residual) {
@@ -185,7 +188,7 @@ extern "C" int agg_check_route_args(int64_t tokens, int experts, int top_k, int 
     return fail(AGG_E_ARG, "top_k %d: 1 to %d, and no more than the experts of the kept groups", top_k, AGG_MAX_TOP_K);
   if (!std::isfinite(scale)) return fail(AGG_E_ARG, "scale is not finite");
   if (ld < experts) return fail(AGG_E_ARG, "a row stride of %lld is below the %d experts", (long long)ld, experts);
-  if (tokens > kMostRows) return fail(AGG_E_UNSUPPORTED, "tokens beyond 2^30");
+  if (tokens > kMostRows || ld > kMostStride) return fail(AGG_E_UNSUPPORTED, "tokens beyond 2^30 or a row stride beyond 2^31");
   if (tokens == 0) return AGG_OK;
   if (!logits || !ids || !weights) return fail(AGG_E_ARG, "logits, ids or weights is NULL");
   return AGG_OK;
@@ -199,7 +202,7 @@ extern "C" int agg_check_plan_args(int64_t tokens, int top_k, const int32_t* ids
   if (top_k < 1 || top_k > AGG_MAX_TOP_K) return fail(AGG_E_ARG, "top_k %d not in [1, %d]", top_k, AGG_MAX_TOP_K);
   if (first < 0) return fail(AGG_E_ARG, "first %d is negative", first);
   if (n_local < 1 || n_local > AGG_MAX_EXPERTS) return fail(AGG_E_ARG, "n_local %d not in [1, %d]", n_local, AGG_MAX_EXPERTS);
-  if (tokens * top_k > kMostRows || (tokens * top_k / AGG_PLAN_PAIRS + 1) * (n_local + 1) >= (int64_t(1) << 31))
+  if (tokens > kMostRows || tokens * top_k > kMostRows || (tokens * top_k / AGG_PLAN_PAIRS + 1) * (n_local + 1) >= (int64_t(1) << 31))
     return fail(AGG_E_UNSUPPORTED, "%lld pairs are too many", (long long)(tokens * top_k));
   if (!offsets) return fail(AGG_E_ARG, "offsets is NULL");
   if (tokens == 0) return AGG_OK;

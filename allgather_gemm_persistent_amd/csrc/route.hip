@@ -366,8 +366,18 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
 }
 
 template <int STEPS, int V>
-static hipError_t launch_route_lv(const RouteArgs& a, hipStream_t stream) {
+static hipError_t launch_route_lv(RouteArgs a, hipStream_t stream) {
   constexpr int64_t tokens = 256 >> STEPS;
+  // (a launch holds fewer than 2^32 threads: more tokens go in further ones)
+  constexpr int64_t most = tokens << 23;
+  for (; a.tokens > most; a.tokens -= most) {
+    RouteArgs p = a;
+    p.tokens = most;
+    if (hipError_t e = launch_route_lv<STEPS, V>(p, stream)) return e;
+    a.logits = static_cast<const char*>(a.logits) + most * a.ld * (a.logits_bf16 ? 2 : 4);
+    a.ids += most * a.top_k;
+    a.weights += most * a.top_k;
+  }
   const dim3 grid((unsigned)((a.tokens + tokens - 1) / tokens)), block(256);
   const bool full = a.experts == (V << STEPS);    // no lane without an expert
   if (a.logits_bf16) {
@@ -393,11 +403,12 @@ hipError_t launch_route(const RouteArgs& a, int cus, hipStream_t stream) {
 //
 // Pair p = token * top_k + choice goes into the bucket of its expert, or, where the expert is not
 // one of this rank's n_local (or is -1), into a last bucket that gets no slot. Blocks of kPlanPairs
-// pairs: the first kernel counts each block's buckets, the second adds up what comes before its
-// block and gives every pair its place; up to kPlanAlone pairs the second does without the first.
+// pairs: the first kernel counts each block's buckets, the last gives every pair its place from what
+// comes before its block, which it counts itself (up to kPlanAlone pairs, without the first kernel),
+// adds up from the counts, or takes from a kernel between them that did.
 // Counts are sums of ones, so no order of additions changes them, and the places follow the pairs' order.
 //
-// Bound by latency: the ids of 32768 tokens' 8 choices are 1 MB, and the two kernels take 4.6 and 6 us;
+// Bound by latency: the ids of 32768 tokens' 8 choices are 1 MB, and the two kernels take 4 and 6 us;
 // a plan of one block takes 3 us.
 
 namespace {
@@ -411,6 +422,7 @@ __device__ inline int bucket_of(const PlanArgs& a, int64_t p) {
 
 constexpr int kPlanThreads = 1024;
 constexpr int64_t kPlanAlone = 12 * kPlanPairs;
+constexpr int64_t kPlanCounts = 20000;               // counts that every block adds up
 
 // Block b of R * kPlanPairs pairs.
 template <int R>
@@ -428,7 +440,41 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs
   for (int e = threadIdx.x; e < buckets; e += kPlanThreads) a.work[(int64_t)blockIdx.x * buckets + e] = count[e];
 }
 
-template <int R, bool ALONE>
+// The counts of `blocks` blocks, in place, become the sums over the blocks before each; one more row gets
+// the sums over all. A wave a bucket, its lanes over blocks.
+__global__ void __launch_bounds__(256) plan_scan_kernel(const PlanArgs a, int blocks) {
+  constexpr int U = 4;                               // loads on their way together
+  const int lane = threadIdx.x & 63, buckets = a.n_local + 1;
+  const int e = (int)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (e >= buckets) return;
+  int sum = 0;
+  for (int b0 = 0; b0 < blocks; b0 += 64 * U) {
+    int c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * 64 + lane;
+      c[u] = b < blocks ? a.work[(int64_t)b * buckets + e] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      int incl = c[u];
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(incl, d);
+        if (lane >= d) incl += o;
+      }
+      const int b = b0 + u * 64 + lane;
+      if (b < blocks) a.work[(int64_t)b * buckets + e] = sum + incl - c[u];
+      sum += __shfl(incl, 63);
+    }
+  }
+  if (lane == 0) a.work[(int64_t)blocks * buckets + e] = sum;
+}
+
+// How a block learns what comes before it: from all the pairs, from the blocks' counts, or from their sums.
+enum PlanFrom { kFromPairs, kFromCounts, kFromSums };
+
+template <int R, PlanFrom FROM>
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs a) {
   constexpr int W = kPlanThreads / 64;               // waves
   __shared__ int count[W][AGG_MAX_EXPERTS + 1];      // pairs of this block, by wave and bucket
@@ -467,7 +513,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
   }
 
   // totals of every bucket and what the blocks before this one hold of it
-  if (ALONE && blocks > 1) {
+  if (FROM == kFromSums) {
+    for (int e = tid; e < buckets; e += kPlanThreads) {
+      total[e] = a.work[(int64_t)blocks * buckets + e];
+      place[e] = a.work[(int64_t)block * buckets + e];
+    }
+    __syncthreads();
+  } else if (FROM == kFromPairs && blocks > 1) {
     // from the pairs themselves, kBatch loads on their way together
     constexpr int kBatch = 8;
     const int pairs = (int)a.pairs, mine = block * R * kPlanPairs;
@@ -554,31 +606,35 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
   }
 }
 
-template <int R, bool ALONE>
+template <int R, PlanFrom FROM>
 static hipError_t launch_plan_r(const PlanArgs& a, hipStream_t stream) {
   const int64_t blocks = a.pairs > 0 ? (a.pairs + R * kPlanPairs - 1) / (R * kPlanPairs) : 1;
-  if (!ALONE) {
+  if (FROM != kFromPairs) {
     hipLaunchKernelGGL(plan_count_kernel<R>, dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  hipLaunchKernelGGL((plan_place_kernel<R, ALONE>), dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, a);
+  if (FROM == kFromSums) {
+    hipLaunchKernelGGL(plan_scan_kernel, dim3((unsigned)((a.n_local + 4) / 4)), dim3(256), 0, stream, a, (int)blocks);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  hipLaunchKernelGGL((plan_place_kernel<R, FROM>), dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, a);
   return hipGetLastError();
 }
 
-// Every block reads every block's counts, so large plans take larger blocks. Microseconds for 64 experts:
-//   pairs          4096  8192  12288  16384  131072  262144  524288  1048576
-//   one launch      5.1   5.8    6.7    7.3
-//   1024 a block    6.7   6.8    7.1    7.1     8.3    10.3    18.5     45.8
-//   2048            7.2   7.9    8.0    8.1     8.8     9.5    11.8     20.9
-//   4096            9.7   9.9   10.3   10.4    11.3    11.8    12.7     16.1
-// (256 experts: 19.1, 14.0 and 14.4 at 262144 pairs, 131, 45.6 and 25.8 at 1048576)
+// Up to kPlanAlone pairs every block counts them all. Beyond, it adds up the blocks' counts while these are
+// few, and else takes them summed by a third launch (larger blocks then cost less). Microseconds:
+//   pairs         4096  8192  12288  16384  131072   131072  262144  262144  262144   1048576  16777216
+//   experts         64    64     64     64      64      256      64     256    1024       256       256
+//   one launch     5.1   5.8    6.7    7.3
+//   counts         6.7   6.8    7.1    7.1     8.3     12.7    10.3    19.3    51.1     131.5
+//   sums, 2048 a block                        10.6     11.3    11.1    12.1    14.8      19.8       200
+//   sums, 4096                                13.3     14.2    13.7    14.8    16.8      19.0       158
 hipError_t launch_plan(const PlanArgs& a, hipStream_t stream) {
   static_assert(kPlanThreads == kPlanPairs, "a pair a thread and round");
-  // few pairs: every block counts them all itself, cheaper than the launch that would count them once
-  if (a.pairs <= kPlanAlone) return launch_plan_r<1, true>(a, stream);
-  if (a.pairs <= 128 * kPlanPairs) return launch_plan_r<1, false>(a, stream);
-  if (a.pairs <= 256 * kPlanPairs) return launch_plan_r<2, false>(a, stream);
-  return launch_plan_r<4, false>(a, stream);
+  if (a.pairs <= kPlanAlone) return launch_plan_r<1, kFromPairs>(a, stream);
+  if (a.pairs / kPlanPairs * (a.n_local + 1) <= kPlanCounts) return launch_plan_r<1, kFromCounts>(a, stream);
+  if (a.pairs <= 1024 * kPlanPairs) return launch_plan_r<2, kFromSums>(a, stream);
+  return launch_plan_r<4, kFromSums>(a, stream);
 }
 
 }  // namespace agg

@@ -188,7 +188,20 @@ static hipError_t launch_norm_tv(const NormArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_norm(const NormArgs& a, int cus, hipStream_t stream) {
+hipError_t launch_norm(const NormArgs& all, int cus, hipStream_t stream) {
+  NormArgs a = all;
+  // (a launch holds fewer than 2^32 threads: more rows go in further ones)
+  constexpr int64_t kMost = 1 << 21;
+  for (; a.rows > kMost; a.rows -= kMost) {
+    NormArgs p = a;
+    p.rows = kMost;
+    if (hipError_t e = launch_norm(p, cus, stream)) return e;
+    a.x = static_cast<const char*>(a.x) + kMost * a.ld_x * (a.x_fp32 ? 4 : 2);
+    if (a.residual) a.residual += kMost * a.ld_r;
+    if (a.residual_out) a.residual_out += kMost * a.ld_ro;
+    a.out = static_cast<char*>(a.out) + kMost * a.ld_out * (a.out_fp8 ? 1 : 2);
+    if (a.scales) a.scales += kMost;
+  }
   const int64_t chunks = a.cols / 8;
   if (chunks <= 64) return launch_norm_tv<64, 1>(a, stream);
   if (chunks <= 128) return launch_norm_tv<64, 2>(a, stream);

@@ -525,8 +525,8 @@ int agg_ctx_set_chain_fused(agg_ctx* ctx, int on);
  * every group is multiplied by its expert's weight (moe_gemm), and the choices' results are summed
  * back to tokens (moe_combine). They are forward operators, like the others here.
  *
- * Every call launches on `stream` alone (one kernel; moe_plan two beyond 12288 pairs,
- * moe_combine one per 65535 tokens), is capturable and allocates nothing. Of the ctx they use its device and, in moe_gemm with few rows
+ * Every call launches on `stream` alone (one kernel; moe_plan two or three
+ * beyond 12288 pairs, moe_combine one per 65535 tokens), is capturable and allocates nothing. Of the ctx they use its device and, in moe_gemm with few rows
  * and few experts, one of four workspaces of partial sums, each given to one of the first four
  * streams that need one (a later stream's calls go without, slower): calls on several streams do not
  * meet, but a graph that holds calls captured on a stream must not be replayed while other calls

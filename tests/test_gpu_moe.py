@@ -310,6 +310,28 @@ def test_route_many_tokens_distinct_logits(ctx):
     assert (np.abs(w - want) <= want * (E * EPS32 + FINE)).all()
 
 
+def test_more_rows_than_a_launch_holds(ctx):
+    """Rows and tokens beyond 2^32 threads (64 and 8 of them a row): equal rows, so equal results, to the
+    last."""
+    rows = (1 << 26) + 5
+    x = torch.tensor([1.0, -2.0, 3.0, 0.5, -0.25, 4.0, -6.0, 7.0], device="cuda").bfloat16().repeat(rows, 1)
+    out = torch.zeros(rows, 8, dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.zeros(rows, device="cuda")
+    B.quant_rows(ctx, rows, 8, x, out, scales=scales, stream=torch.cuda.current_stream())
+    assert bool((scales == scales[0]).all()) and abs(float(scales[0]) * 448 / 7 - 1) < 1e-6
+    bits = out.view(torch.uint8).view(torch.int64).reshape(-1)
+    assert bool((bits == bits[0]).all())
+    np.testing.assert_allclose(out[-1].float().cpu().numpy() * float(scales[0]), x[-1].float().cpu().numpy(), rtol=2.0 ** -4)
+    del x, out, scales, bits
+    tokens = (1 << 29) + 7
+    ids = torch.full((tokens, 1), -7, dtype=torch.int32, device="cuda")
+    w = torch.zeros(tokens, 1, device="cuda")
+    B.moe_route(ctx, tokens, 1, 1, torch.ones(tokens, 1, dtype=torch.bfloat16, device="cuda"), ids, w,
+                stream=torch.cuda.current_stream())
+    assert bool((ids == 0).all()) and bool((w == 1).all())
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------------------ the plan
 
 def _plan_ref(ids, first, n):
@@ -329,7 +351,9 @@ def _plan_ref(ids, first, n):
 @pytest.mark.parametrize("T,k,n,first,total", [
     (0, 2, 8, 0, 8), (1, 1, 1, 0, 1), (1, 16, 64, 0, 64), (16, 2, 64, 0, 64), (63, 1, 5, 0, 5), (1023, 1, 8, 0, 8),
     (1024, 1, 8, 0, 8), (1025, 1, 8, 4, 16), (512, 2, 32, 96, 256), (4951, 4, 60, 0, 60), (5000, 8, 1024, 0, 1024),
-    (32768, 8, 32, 128, 256), (3000, 3, 255, 1, 256), (700, 4, 256, 0, 300)])
+    (32768, 8, 32, 128, 256), (3000, 3, 255, 1, 256), (700, 4, 256, 0, 300), (12288, 1, 64, 0, 64),
+    (12289, 1, 64, 3, 70), (30001, 1, 900, 0, 1000), (40007, 8, 128, 0, 128), (1048579, 1, 20, 0, 30),
+    (150001, 9, 77, 5, 90)])
 def test_plan(ctx, T, k, n, first, total):
     rng = np.random.default_rng(T + n)
     ids = rng.integers(-1, total, (T, k)).astype(np.int32)

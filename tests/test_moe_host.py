@@ -37,7 +37,9 @@ def test_norm_args_ok(lib, kw):
     (dict(out=None), B.AGG_E_ARG), (dict(x=FAKE + 2), B.AGG_E_ARG), (dict(w=FAKE + 8), B.AGG_E_ARG),
     (dict(r=FAKE + 4), B.AGG_E_ARG), (dict(ro=FAKE + 4), B.AGG_E_ARG), (dict(lx=63), B.AGG_E_ARG),
     (dict(lx=68), B.AGG_E_ARG), (dict(lr=56), B.AGG_E_ARG), (dict(lro=65), B.AGG_E_ARG), (dict(lo=60), B.AGG_E_ARG),
-    (dict(cols=32776, lx=32776), B.AGG_E_UNSUPPORTED), (dict(rows=(1 << 30) + 1), B.AGG_E_UNSUPPORTED)])
+    (dict(cols=32776, lx=32776), B.AGG_E_UNSUPPORTED), (dict(rows=(1 << 30) + 1), B.AGG_E_UNSUPPORTED),
+    (dict(lx=1 << 32), B.AGG_E_UNSUPPORTED), (dict(lr=1 << 62), B.AGG_E_UNSUPPORTED),
+    (dict(lro=1 << 62), B.AGG_E_UNSUPPORTED), (dict(lo=1 << 62), B.AGG_E_UNSUPPORTED)])
 def test_norm_args_rejected(lib, kw, code):
     assert _norm(lib, **kw) == code
     assert B.last_error()
@@ -63,7 +65,8 @@ def test_route_args_ok(lib):
     (dict(experts=1024, stride=1024, groups=128), B.AGG_E_ARG), (dict(groups=4, top_groups=5), B.AGG_E_ARG),
     (dict(top_groups=0), B.AGG_E_ARG), (dict(score=2), B.AGG_E_ARG), (dict(ld=B.AGG_FP8_E4M3), B.AGG_E_ARG),
     (dict(scale=float("nan")), B.AGG_E_ARG), (dict(stride=63), B.AGG_E_ARG), (dict(logits=None), B.AGG_E_ARG),
-    (dict(ids=None), B.AGG_E_ARG), (dict(weights=None), B.AGG_E_ARG), (dict(tokens=(1 << 30) + 1), B.AGG_E_UNSUPPORTED)])
+    (dict(ids=None), B.AGG_E_ARG), (dict(weights=None), B.AGG_E_ARG), (dict(tokens=(1 << 30) + 1), B.AGG_E_UNSUPPORTED),
+    (dict(stride=1 << 62), B.AGG_E_UNSUPPORTED)])
 def test_route_args_rejected(lib, kw, code):
     assert _route(lib, **kw) == code
     assert B.last_error()
@@ -82,6 +85,7 @@ def test_plan_args(lib):
                dict(ids=None), dict(st=None), dict(ts=None), dict(work=None)):
         assert _plan(lib, **kw) == B.AGG_E_ARG, kw
     assert _plan(lib, tokens=1 << 30) == B.AGG_E_UNSUPPORTED
+    assert _plan(lib, tokens=1 << 62, k=16) == B.AGG_E_UNSUPPORTED   # (the product of the two wraps to 0)
 
 
 def _gemm(lib, **kw):
@@ -108,7 +112,7 @@ def test_gemm_args_ok(lib):
     (dict(rows=0), B.AGG_E_ARG), (dict(st=None, rows=31), B.AGG_E_ARG), (dict(a=None), B.AGG_E_ARG),
     (dict(b=None), B.AGG_E_ARG), (dict(off=None), B.AGG_E_ARG), (dict(out=None), B.AGG_E_ARG),
     (dict(a=FAKE + 8), B.AGG_E_ARG), (dict(b=FAKE + 2), B.AGG_E_ARG), (dict(out=FAKE + 2), B.AGG_E_ARG),
-    (dict(rows=1 << 20, k=8192, la=8192), B.AGG_E_UNSUPPORTED),
+    (dict(rows=1 << 20, k=8192, la=8192), B.AGG_E_UNSUPPORTED), (dict(rows=16, la=1 << 60), B.AGG_E_UNSUPPORTED),
     (dict(n=1 << 16, k=1 << 14, la=1 << 14), B.AGG_E_UNSUPPORTED),
     (dict(n=1 << 15, k=1 << 14, la=1 << 14, gated=1), B.AGG_E_UNSUPPORTED)])
 def test_gemm_args_rejected(lib, kw, code):
