@@ -32,6 +32,8 @@ __device__ inline u32x4 narrow(const float (&v)[8]) {
 // a float inside e4m3's range; a NaN stays one
 __device__ inline float clamp_e4m3(float v) { return v != v ? v : fminf(fmaxf(v, -448.0f), 448.0f); }
 
+constexpr float kNormal = 1.17549435e-38f;   // the least float of full precision, 2^-126
+
 template <int T, typename F>
 __device__ inline uint32_t block_reduce(uint32_t v, F op, uint32_t* lds) {
 #pragma unroll
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
   }
   if constexpr (OUT8) {
     float scale = a.scale;
+    bool clamp = true;
     if (a.scales) {
       // the largest |y| by its bit pattern: a NaN is larger than every number and is kept
       uint32_t m = 0;
@@ -133,14 +136,16 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
       m = block_reduce<T>(m, [](uint32_t x, uint32_t y) { return x > y ? x : y; }, lds[1]);
       const float top = __builtin_bit_cast(float, m) / 448.0f;
       scale = top > 0.0f ? top : 1.0f;      // a row of zeros, or with a NaN: 1
+      clamp = !(top >= kNormal);
       if (tid == 0) a.scales[row] = scale;
     }
     // one reciprocal a row instead of a division an element (27 -> 21 us at 4951 x 7168, where the
     // divisions cost more than the memory): y * (1 / scale) and y / scale differ by a unit of fp32 at
     // most, far below e4m3's. Scales so small that the reciprocal overflows divide. With a scale of the
-    // row's own, |y| / scale is at most 448 but for that unit, which the conversion rounds away; a
-    // given scale needs the clamp
-    const bool small = !(fabsf(scale) >= 1.2e-38f);
+    // row's own, |y| / scale is at most 448 but for a few units, which the conversion rounds away (up to
+    // 464); but a subnormal one, a multiple of 2^-149, can be a third below max|y| / 448, and the 1 of a
+    // row with a NaN has nothing to do with the other elements: these, and a given scale, need the clamp
+    const bool small = !(scale >= kNormal);
     const float by = 1.0f / scale;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = s[i][e] / scale;
       }
-      if (!a.scales) {
+      if (clamp) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = clamp_e4m3(q[e]);
       }

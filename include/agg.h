@@ -547,9 +547,9 @@ int agg_ctx_set_chain_fused(agg_ctx* ctx, int on);
  *   weight           bf16[cols]
  *   out, out_dtype   AGG_BF16, or AGG_FP8_E4M3: with `scales` (fp32[rows], 4-byte aligned) row r is
  *                    e4m3(y / scales[r]) with scales[r] = max|y| / 448 written by the call (1 for a
- *                    row of zeros or one that holds a NaN); with scales NULL, e4m3(y / scale) for
- *                    the given scale (> 0), values beyond +-448 saturating: the operand of an fp8
- *                    ag_gemm with scale_a = scale. A NaN stays a NaN
+ *                    row whose quotient is zero or that holds a NaN); with scales NULL, e4m3(y /
+ *                    scale) for the given scale (> 0): the operand of an fp8 ag_gemm with scale_a =
+ *                    scale. Values beyond +-448 saturate, a NaN stays a NaN
  * cols and the strides are multiples of 8, row starts of x and the residuals of 16 bytes; cols at
  * most AGG_MAX_NORM_COLS. residual_out may be residual or a bf16 x, out may be x, at equal strides
  * and types (each row is read before it is written).

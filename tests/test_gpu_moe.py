@@ -175,6 +175,42 @@ def test_quant_rows_of_the_smallest_and_largest_numbers(ctx):
     _check_fp8(q.cpu(), scales.cpu(), x.double(), 1)
 
 
+@pytest.mark.parametrize("xd", ["bf16", "fp32"])
+def test_quant_rows_beside_a_nan_saturates(ctx, xd):
+    """The scale of a row with a NaN is 1: its other elements are rounded to e4m3 as they are, those
+    beyond +-448 to +-448, infinities among them."""
+    x = torch.randn(3, 1032, generator=_gen(6)) * 300
+    x[1, 5], x[1, 6], x[1, 7], x[1, 8], x[1, 9] = math.nan, 1000.0, -464.5, math.inf, -math.inf
+    x = x if xd == "fp32" else x.bfloat16()
+    q, scales = torch.empty(3, 1032, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(3, device="cuda")
+    B.quant_rows(ctx, 3, 1032, x.cuda(), q, scales=scales, stream=torch.cuda.current_stream())
+    q, want = q.cpu(), x[1].float()
+    assert scales[1].item() == 1 and torch.isnan(q[1, 5].float())
+    assert q[1, 6:10].float().tolist() == [448, -448, 448, -448]
+    keep = torch.arange(1032) != 5
+    want = want[keep].clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert (want.float().abs() == 448).sum() > 100 and torch.equal(q[1, keep].float(), want.float())
+    _check_fp8(q[[0, 2]], scales.cpu()[[0, 2]], x[[0, 2]].double(), 1)
+
+
+@pytest.mark.parametrize("units", [1, 200, 225, 448, 600, 671, 700, 1000, 6000, 448 * 8388608, 500 * 8388608])
+def test_fp8_rows_of_subnormal_scales(ctx, units):
+    """A largest element of `units` times 2^-149, whose scale is rounded to a multiple of 2^-149 (or to
+    none: then it is 1): every element is its quotient by that scale, kept inside +-448."""
+    tiny = 2.0 ** -149
+    x = torch.linspace(-1, 1, 520, dtype=torch.float64) * units
+    x = (x.round() * tiny).float()[None].repeat(2, 1)
+    q, scales = torch.empty(2, 520, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(2, device="cuda")
+    B.quant_rows(ctx, 2, 520, x.cuda(), q, scales=scales, stream=torch.cuda.current_stream())
+    scale = scales.cpu().double()
+    want = units * tiny / 448
+    # (the quotient is rounded to 24 bits, or to a multiple of 2^-149)
+    assert (scale == 1).all() if units <= 224 else ((scale - want).abs() <= max(want * EPS32, tiny / 2)).all()
+    # the kernel's quotient is rounded to fp32 before the conversion
+    exact = (x.double() / scale[:, None]).clamp(-448, 448)
+    _within(q.float(), exact, torch.maximum(exact.abs() * 2.0 ** -4, torch.tensor(2.0 ** -10)) + exact.abs() * FINE, "fp8")
+
+
 # ------------------------------------------------------------------------------ routing
 
 def _route_ref(x, bias, score, groups, top_groups, k, renorm, scale):
