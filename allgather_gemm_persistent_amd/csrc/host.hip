@@ -139,7 +139,8 @@ struct agg_ctx {
                                              //   counters are in the device's static scratch)
   hipEvent_t ev_upload = nullptr;
   bool upload_pending = false;
-  // the stream of the last call that used the ctx's scratch, and the event a call on another one waits for
+  // the stream of the last call, captured ones aside, that used the ctx's scratch, and the event a call on
+  // another one waits for
   hipStream_t last_stream = nullptr;
   bool any_call = false;
   hipEvent_t ev_order = nullptr;
@@ -266,23 +267,26 @@ int grid_for(agg_ctx* ctx, int64_t tiles, bool overlapped) {
   return int(std::max<int64_t>(g, 1));
 }
 
+bool capturing(hipStream_t s) {
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  return s && hipStreamIsCapturing(s, &st) == hipSuccess && st != hipStreamCaptureStatusNone;
+}
+
 // A ctx serialises its calls, which share its scratch: a call on another stream than the last one's
-// starts after it. Under a stream capture the order is the caller's (an event recorded outside a
-// capture cannot be waited for inside it).
+// starts after it. A call under capture enqueues nothing, so it neither waits nor counts as the last
+// one: its order, at every replay, is the caller's. (So is that of a call whose predecessor's stream has
+// begun a capture since: an event recorded there would belong to the capture.) The event is recorded
+// only where the stream changes: after every call it would take 2.9 us of each.
 int order_calls(agg_ctx* ctx, hipStream_t s) {
   const hipStream_t last = ctx->last_stream;
-  if (ctx->any_call && last != s) {
-    auto capturing = [](hipStream_t x) {
-      hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-      return x && hipStreamIsCapturing(x, &st) == hipSuccess && st != hipStreamCaptureStatusNone;
-    };
-    if (!capturing(s) && !capturing(last)) {
-      if (hipEventRecord(ctx->ev_order, last) == hipSuccess) {
-        HIP_TRY(hipStreamWaitEvent(s, ctx->ev_order, 0));
-      } else {
-        (void)hipGetLastError();               // (the last call's stream is gone)
-        HIP_TRY(hipDeviceSynchronize());
-      }
+  if (ctx->any_call && last == s) return AGG_OK;
+  if (capturing(s)) return AGG_OK;
+  if (ctx->any_call && !capturing(last)) {
+    if (hipEventRecord(ctx->ev_order, last) == hipSuccess) {
+      HIP_TRY(hipStreamWaitEvent(s, ctx->ev_order, 0));
+    } else {
+      (void)hipGetLastError();                 // (the last call's stream is gone)
+      HIP_TRY(hipDeviceSynchronize());
     }
   }
   ctx->last_stream = s;
