@@ -139,11 +139,13 @@ struct agg_ctx {
                                              //   counters are in the device's static scratch)
   hipEvent_t ev_upload = nullptr;
   bool upload_pending = false;
-  // the stream of the last call, captured ones aside, that used the ctx's scratch, and the event a call on
-  // another one waits for
+  // the stream of the last call, captured ones aside, that used the ctx's scratch; the event a call on
+  // another one waits for, whether the last call recorded it, and how many more calls do
   hipStream_t last_stream = nullptr;
   bool any_call = false;
   hipEvent_t ev_order = nullptr;
+  bool order_recorded = false;
+  int order_turns = 0;
   // moe_gemm's workspaces, each the counters and then the partial sums, and the streams they belong to
   uint8_t* moe_ws = nullptr;
   agg_stream moe_stream[kMoeWorkspaces] = {};
@@ -272,27 +274,49 @@ bool capturing(hipStream_t s) {
   return s && hipStreamIsCapturing(s, &st) == hipSuccess && st != hipStreamCaptureStatusNone;
 }
 
-// A ctx serialises its calls, which share its scratch: a call on another stream than the last one's
-// starts after it. A call under capture enqueues nothing, so it neither waits nor counts as the last
-// one: its order, at every replay, is the caller's. (So is that of a call whose predecessor's stream has
-// begun a capture since: an event recorded there would belong to the capture.) The event is recorded
-// only where the stream changes: after every call it would take 2.9 us of each.
-int order_calls(agg_ctx* ctx, hipStream_t s) {
-  const hipStream_t last = ctx->last_stream;
-  if (ctx->any_call && last == s) return AGG_OK;
-  if (capturing(s)) return AGG_OK;
-  if (ctx->any_call && !capturing(last)) {
-    if (hipEventRecord(ctx->ev_order, last) == hipSuccess) {
-      HIP_TRY(hipStreamWaitEvent(s, ctx->ev_order, 0));
-    } else {
-      (void)hipGetLastError();                 // (the last call's stream is gone)
-      HIP_TRY(hipDeviceSynchronize());
+// A call's turn. A ctx serialises its calls, which share its scratch: a call on another stream than the
+// last one's starts after it. The last one's stream may be gone by then, or in the middle of a capture,
+// so nothing is asked of it: either an event was recorded on it right after that call, or the device is
+// waited for. An event after every call would take 2.9 us of each, so one is recorded after the ctx's
+// first kFirstTurns calls and after the kTurns calls from a change of streams on: a program that stays
+// on a stream pays nothing, one that warms up on one stream and goes on on another, or that takes turns
+// between streams, does not wait on the host. A call under capture enqueues nothing, so it neither waits
+// nor counts as the last one: its order, at every replay, is the caller's.
+class Turn {
+ public:
+  Turn(agg_ctx* ctx, hipStream_t s) : ctx_(ctx), s_(s) {
+    if (ctx->any_call && ctx->last_stream == s) return;
+    if (capturing(s)) return;
+    if (ctx->any_call) {
+      if (ctx->order_recorded) {
+        if (hipError_t e = hipStreamWaitEvent(s, ctx->ev_order, 0))
+          rc = fail(AGG_E_HIP, "hipStreamWaitEvent: %s", hipGetErrorString(e));
+      } else if (hipError_t e = hipDeviceSynchronize()) {
+        (void)hipGetLastError();
+        rc = fail(AGG_E_STATE, "a call on another stream than the last one's cannot wait for it: %s", hipGetErrorString(e));
+      }
+      if (rc) return;
     }
+    ctx->order_turns = ctx->any_call ? kTurns : kFirstTurns;
+    ctx->last_stream = s;
+    ctx->any_call = true;
   }
-  ctx->last_stream = s;
-  ctx->any_call = true;
-  return AGG_OK;
-}
+  ~Turn() {
+    if (!ctx_->order_recorded && ctx_->order_turns == 0) return;
+    // (a call under capture, or one that was refused its turn, leaves the last one's event)
+    if (rc || ctx_->last_stream != s_ || capturing(s_)) return;
+    ctx_->order_recorded = ctx_->order_turns > 0 && hipEventRecord(ctx_->ev_order, s_) == hipSuccess;
+    if (ctx_->order_turns > 0) --ctx_->order_turns;
+  }
+  Turn(const Turn&) = delete;
+  Turn& operator=(const Turn&) = delete;
+  int rc = AGG_OK;
+
+ private:
+  static constexpr int kFirstTurns = 4, kTurns = 16;
+  agg_ctx* const ctx_;
+  const hipStream_t s_;
+};
 
 // Stream choreography shared by ag_gemm and gemm_rs. `launch` enqueues the consumer kernel on
 // ctx->ks, `put_all` the producer's copies and flags on the copy streams.
@@ -1059,7 +1083,8 @@ int ag_gemm_impl(agg_ctx* ctx, int world, int rank, int64_t m_shard, int64_t n, 
   if ((m + ts.bm - 1) / ts.bm > AGG_MAX_ROW_TILES)
     return fail(AGG_E_UNSUPPORTED, "%lld row tiles exceed %d", (long long)((m + ts.bm - 1) / ts.bm), AGG_MAX_ROW_TILES);
   HIP_TRY(hipSetDevice(ctx->device));
-  if (int rc = order_calls(ctx, S(stream))) return rc;
+  const Turn turn(ctx, S(stream));
+  if (turn.rc) return turn.rc;
   const int cps = int(m_shard / chunk_rows);
   if (world > 1)
     if (int rc = bind_flags(ctx, kFlagsAg, flags, size_t(world) * cps)) return rc;
@@ -1317,7 +1342,8 @@ extern "C" int gemm_rs(agg_ctx* ctx, int world, int rank, int64_t m, int64_t n, 
   if (world * ((mb + ts.bm - 1) / ts.bm) > AGG_MAX_ROW_TILES)
     return fail(AGG_E_UNSUPPORTED, "row tiles exceed %d", AGG_MAX_ROW_TILES);
   HIP_TRY(hipSetDevice(ctx->device));
-  if (int rc = order_calls(ctx, S(stream))) return rc;
+  const Turn turn(ctx, S(stream));
+  if (turn.rc) return turn.rc;
   const int cpb = int(mb / chunk_rows);
   if (world > 1) {
     if (int rc = bind_flags(ctx, kFlagsRsRecv, flags, size_t(world) * cpb)) return rc;
@@ -1446,7 +1472,8 @@ extern "C" int gemm_ar(agg_ctx* ctx, int world, int rank, int64_t m, int64_t n, 
   const TileShape ts = tile_for(ctx, 2, AGG_BF16, m, n, k);
   if ((m + ts.bm - 1) / ts.bm > AGG_MAX_ROW_TILES) return fail(AGG_E_UNSUPPORTED, "row tiles exceed %d", AGG_MAX_ROW_TILES);
   HIP_TRY(hipSetDevice(ctx->device));
-  if (int rc = order_calls(ctx, S(stream))) return rc;
+  const Turn turn(ctx, S(stream));
+  if (turn.rc) return turn.rc;
   const int cpb = int(m / chunk_rows);
   if (world > 1) {
     if (int rc = bind_flags(ctx, kFlagsArRecv, flags, size_t(world) * cpb)) return rc;
@@ -1584,7 +1611,8 @@ extern "C" int ffn_chain(agg_ctx* ctx, int world, int rank, int64_t m_shard, int
   if ((m + ts.bm - 1) / ts.bm * 2 + world > AGG_MAX_ROW_TILES)
     return fail(AGG_E_UNSUPPORTED, "row tiles exceed %d", AGG_MAX_ROW_TILES);
   HIP_TRY(hipSetDevice(ctx->device));
-  if (int rc = order_calls(ctx, S(stream))) return rc;
+  const Turn turn(ctx, S(stream));
+  if (turn.rc) return turn.rc;
   if (world > 1) {
     if (int rc = bind_flags(ctx, kFlagsAg, flags, size_t(world) * cps)) return rc;
     if (int rc = bind_flags(ctx, kFlagsRsRecv, rs_flags, size_t(world) * cpb)) return rc;
