@@ -50,6 +50,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "kernels.h"
@@ -66,7 +67,6 @@ constexpr int kDefaultReservedCus = 32;
 // AGG_PULL_AUTO pulls gathers of at most this many remote bytes (latency-bound transfers)
 constexpr int64_t kPullMaxBytes = int64_t(4) << 20;
 constexpr int kTimingRing = 256;          // launches whose kernel duration is kept
-constexpr size_t kMoeWsStride = size_t(kMoeCounters) * 4 + size_t(kMoeWsBytes);
 
 enum FlagSlot { kFlagsAg = 0, kFlagsRsRecv = 1, kFlagsRsSend = 2, kFlagsArRecv = 3, kFlagsArSend = 4, kFlagSlots = 5 };
 
@@ -93,6 +93,16 @@ struct StaticScratch {
 };
 std::mutex g_static_mu;
 StaticScratch g_static[kMaxDevices];
+
+// A workspace of moe_gemm's split K: kMoeCounters counters, then `bytes` for partial sums.
+struct MoeWorkspace {
+  uint8_t* mem;
+  size_t bytes;
+  hipStream_t stream;           // whose calls use it: the eager ones, or those of one capture
+  bool captured;
+  unsigned long long capture;   // that capture's id
+  MoeWorkspace* next;
+};
 
 }  // namespace
 
@@ -146,10 +156,7 @@ struct agg_ctx {
   hipEvent_t ev_order = nullptr;
   bool order_recorded = false;
   int order_turns = 0;
-  // moe_gemm's workspaces, each the counters and then the partial sums, and the streams they belong to
-  uint8_t* moe_ws = nullptr;
-  agg_stream moe_stream[kMoeWorkspaces] = {};
-  int moe_streams = 0;
+  MoeWorkspace* moe_ws = nullptr;            // moe_gemm's workspaces, the newest first
 };
 
 namespace {
@@ -771,13 +778,6 @@ extern "C" int agg_ctx_create(int device, agg_ctx** out) {
   if (rc == AGG_OK) step(make_own_queue_stream(ctx, &ctx->ks), "hipExtStreamCreateWithCUMask");
   step(hipHostMalloc(reinterpret_cast<void**>(&ctx->up_host), kTabHostWords * sizeof(uint32_t)),
        "hipHostMalloc(tables)");
-  step(hipMalloc(reinterpret_cast<void**>(&ctx->moe_ws), kMoeWorkspaces * kMoeWsStride), "hipMalloc(moe workspaces)");
-  if (rc == AGG_OK) {
-    const std::vector<uint32_t> zeros(kMoeCounters, 0u);
-    for (int j = 0; j < kMoeWorkspaces; ++j)
-      step(hipMemcpy(ctx->moe_ws + j * kMoeWsStride, zeros.data(), zeros.size() * sizeof(uint32_t), hipMemcpyHostToDevice),
-           "hipMemcpy(moe counters)");
-  }
   if (rc == AGG_OK) rc = static_scratch_setup(device);
   step(hipSetDevice(prev), "hipSetDevice");
   if (rc != AGG_OK) {
@@ -792,16 +792,49 @@ namespace agg {
 
 int ctx_units(const agg_ctx* ctx) { return ctx->cus; }
 int ctx_device(const agg_ctx* ctx) { return ctx->device; }
-bool ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, float** ws, uint32_t** counts) {
-  int i = 0;
-  while (i < ctx->moe_streams && ctx->moe_stream[i] != stream) ++i;
-  if (i == kMoeWorkspaces) return false;
-  if (i == ctx->moe_streams) ctx->moe_stream[ctx->moe_streams++] = stream;
-  uint8_t* const p = ctx->moe_ws + i * kMoeWsStride;
-  *counts = reinterpret_cast<uint32_t*>(p);
-  *ws = reinterpret_cast<float*>(p + size_t(kMoeCounters) * 4);
-  return true;
+
+// Eager calls on one stream run one after another and share a workspace; a stream's handle comes back
+// only after its destruction, which waits for the stream's work (34 ms for 36 ms of it, measured), so
+// a new stream under an old handle finds the counters at zero. The calls of one capture on one stream
+// follow each other in the graph and share one too, which no other graph and no eager call uses. That
+// of a capture lives as long as the ctx, since the graph may, so it is no larger than the call asks for.
+int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws, uint32_t** counts) {
+  const hipStream_t s = S(stream);
+  const bool captured = capturing(s);
+  unsigned long long capture = 0;
+  if (captured) {
+    hipStreamCaptureStatus st;
+    HIP_TRY(hipStreamGetCaptureInfo(s, &st, &capture));
+  }
+  MoeWorkspace* w = ctx->moe_ws;
+  while (w && !(w->stream == s && w->captured == captured && w->capture == capture && w->bytes >= bytes)) w = w->next;
+  if (!w) {
+    constexpr size_t kCounterBytes = size_t(kMoeCounters) * sizeof(uint32_t);
+    const size_t room = captured ? (bytes + 65535) / 65536 * 65536 : size_t(kMoeWsBytes);
+    w = new (std::nothrow) MoeWorkspace{nullptr, room, s, captured, capture, ctx->moe_ws};
+    if (!w) return fail(AGG_E_HIP, "moe_gemm: no host memory for a workspace");
+    // (an allocation is no work of the capture; the mode says so to the runtime, which otherwise
+    // refuses it beside one)
+    hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+    const hipError_t enter = hipThreadExchangeStreamCaptureMode(&mode);
+    hipError_t e = hipMalloc(reinterpret_cast<void**>(&w->mem), kCounterBytes + room);
+    if (enter == hipSuccess) (void)hipThreadExchangeStreamCaptureMode(&mode);
+    // the counters are cleared on the call's own stream: by a graph, at every replay
+    if (e == hipSuccess) {
+      e = launch_fill_u32(reinterpret_cast<uint32_t*>(w->mem), kMoeCounters, 0u, s);
+      if (e != hipSuccess) (void)hipFree(w->mem);
+    }
+    if (e != hipSuccess) {
+      delete w;
+      return fail(AGG_E_HIP, "moe_gemm's workspace: %s", hipGetErrorString(e));
+    }
+    ctx->moe_ws = w;
+  }
+  *counts = reinterpret_cast<uint32_t*>(w->mem);
+  *ws = reinterpret_cast<float*>(w->mem + size_t(kMoeCounters) * sizeof(uint32_t));
+  return AGG_OK;
 }
+
 TileShape ctx_forced_tile(const agg_ctx* ctx) { return TileShape{ctx->force_bm, ctx->force_bn}; }
 
 }  // namespace agg
@@ -823,7 +856,11 @@ extern "C" int agg_ctx_destroy(agg_ctx* ctx) {
     if (e) step(hipEventDestroy(e), "hipEventDestroy");
   if (ctx->up_host) step(hipHostFree(ctx->up_host), "hipHostFree");
   if (ctx->ws) step(hipFree(ctx->ws), "hipFree(ws)");
-  if (ctx->moe_ws) step(hipFree(ctx->moe_ws), "hipFree(moe workspaces)");
+  while (MoeWorkspace* w = ctx->moe_ws) {
+    step(hipFree(w->mem), "hipFree(moe workspace)");
+    ctx->moe_ws = w->next;
+    delete w;
+  }
   for (int j = 0; j < kTimingRing; ++j) {
     if (ctx->ev_t0[j]) step(hipEventDestroy(ctx->ev_t0[j]), "hipEventDestroy");
     if (ctx->ev_t1[j]) step(hipEventDestroy(ctx->ev_t1[j]), "hipEventDestroy");
@@ -850,8 +887,8 @@ extern "C" int agg_ctx_reset(agg_ctx* ctx, agg_stream stream) {
   }
   HIP_TRY(launch_fill_u32(ctx->scratch, kScrWords, 0u, S(stream)));
   HIP_TRY(launch_fill_u32(ctx->scratch + kScrFailed, 1, 0xFFFFFFFFu, S(stream)));
-  for (int j = 0; j < kMoeWorkspaces; ++j)
-    HIP_TRY(launch_fill_u32(reinterpret_cast<uint32_t*>(ctx->moe_ws + j * kMoeWsStride), kMoeCounters, 0u, S(stream)));
+  for (MoeWorkspace* w = ctx->moe_ws; w; w = w->next)
+    HIP_TRY(launch_fill_u32(reinterpret_cast<uint32_t*>(w->mem), kMoeCounters, 0u, S(stream)));
   if (ctx->used_static) {
     // the device's static scratch too (shared by every ctx on the device)
     std::lock_guard<std::mutex> lock(g_static_mu);

@@ -1,6 +1,6 @@
 // The C entry points of the mixture-of-experts operators: checks, then one or two launches on the
-// caller's stream. What they use of the ctx, beside its device, is a workspace of the call's stream
-// (moe_gemm with a split K), so calls on several streams do not meet.
+// caller's stream. What they use of the ctx, beside its device, is a workspace of the call's stream or
+// capture (moe_gemm with a split K), so calls on several streams do not meet.
 #include "moe.h"
 #include "plan.h"
 
@@ -93,8 +93,11 @@ extern "C" int moe_gemm(agg_ctx* ctx, int64_t slots, int n_experts, int64_t n, i
                                       : choose_expert_shape(dtype, slots, n_experts, n, k, gated, units);
   if (shape.stream) {
     StreamArgs s{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(b), static_cast<uint16_t*>(out),
-                 cols, k, x, shape.strips, shape.ksplit, nullptr, kMoeWsBytes, nullptr};
-    if (s.ksplit > 1 && !ctx_moe_workspace(ctx, stream, &s.ws, &s.counts)) s.ksplit = 1;
+                 cols, k, x, shape.strips, shape.ksplit, nullptr, 0, nullptr};
+    if (s.ksplit > 1) {
+      s.ws_bytes = int64_t(s.ksplit) * slots * cols * int64_t(sizeof(float));
+      if (int rc = ctx_moe_workspace(ctx, stream, size_t(s.ws_bytes), &s.ws, &s.counts)) return rc;
+    }
     HIP_TRY(launch_expert_stream(s, dtype, S(stream)));
     return AGG_OK;
   }

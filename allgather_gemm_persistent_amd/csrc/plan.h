@@ -83,13 +83,13 @@ int ctx_device(const agg_ctx* ctx);
 // The tile shape agg_ctx_set_tile forces; {0, 0}: none.
 TileShape ctx_forced_tile(const agg_ctx* ctx);
 
-// The workspace of moe_gemm's split K on one stream: partial sums, and a counter for every strip of
-// every expert. A ctx has kMoeWorkspaces of them and gives one to each stream that asks (the first
-// kMoeWorkspaces streams; false for a later one), so calls on different streams do not meet.
+// The workspace of moe_gemm's split K for calls on `stream`, with room for `bytes` (at most kMoeWsBytes)
+// of partial sums, and kMoeCounters counters, one for every strip of every expert, that are zero when a
+// call starts and when it ends. Every stream has one of its own, and every capture on it, so calls that
+// are not ordered do not meet. Returns an AGG_E_* code.
 constexpr int64_t kMoeWsBytes = int64_t(8) << 20;
 constexpr int kMoeCounters = 4096;
-constexpr int kMoeWorkspaces = 4;
-bool ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, float** ws, uint32_t** counts);
+int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws, uint32_t** counts);
 
 // How moe_gemm multiplies: stream: strips of the output's columns with K in ksplit parts; otherwise
 // tiles of `tile`.

@@ -99,10 +99,10 @@ enum agg_mode {
 /* ---- context -------------------------------------------------------------------------- */
 
 /* Create a ctx on HIP device `device`. Allocates the ctx's device scratch (claim counters, status
- * word, completion counters and the tables the kernel reads, 78 KiB), moe_gemm's workspaces (32 MiB)
- * and pinned host staging for those tables, creates its kernel stream, and, for the first ctx on a
- * device, finds and clears that device's static scratch (ag_gemm_noalloc). AGG_E_UNSUPPORTED unless
- * the device's architecture is gfx950.
+ * word, completion counters and the tables the kernel reads, 78 KiB) and pinned host staging for
+ * those tables, creates its kernel stream, and, for the first ctx on a device, finds and clears
+ * that device's static scratch (ag_gemm_noalloc). AGG_E_UNSUPPORTED unless the device's
+ * architecture is gfx950.
  * Passage: section "The first move was to expose the overlap": symmetric memory and signaling as
  *  the building blocks; the ctx holds the signaling state (epoch, counters) of the calls.
  */
@@ -528,12 +528,14 @@ int agg_ctx_set_chain_fused(agg_ctx* ctx, int on);
  * every group is multiplied by its expert's weight (moe_gemm), and the choices' results are summed
  * back to tokens (moe_combine). They are forward operators, like the others here.
  *
- * Every call launches on `stream` alone (one kernel; moe_plan two or three
- * beyond 12288 pairs, moe_combine one per 65535 tokens), is capturable and allocates nothing. Of the ctx they use its device and, in moe_gemm with few rows
- * and few experts, one of four workspaces of partial sums, each given to one of the first four
- * streams that need one (a later stream's calls go without, slower): calls on several streams do not
- * meet, but a graph that holds calls captured on a stream must not be replayed while other calls
- * captured or made on that stream run. Strides `ld_*` are elements from one row to the next. Device
+ * Every call launches on `stream` alone (one kernel; moe_plan two or three beyond 12288 pairs,
+ * moe_combine one per 65535 tokens) and is capturable. Of the ctx they use its device and, in moe_gemm
+ * with few rows and few experts, a workspace of partial sums (agg_moe_gemm_shape: *ksplit > 1). Every
+ * stream has one of its own (8 MiB, taken by its first such call), and so has every capture on a stream
+ * (what its calls need, kept until the ctx is destroyed); nothing else is allocated. Calls on
+ * several streams and graphs therefore do not meet, and a call's result does not depend on the stream
+ * or graph that it runs in; only two replays of one capture must not run at once, as for the arrays
+ * they share. Strides `ld_*` are elements from one row to the next. Device
  * arrays are 16-byte aligned unless stated. None of the results depends on timing: no
  * floating-point atomics.
  * Passage: section "DITRON adds three levels of tiling" (AllToAll among the collectives, whose

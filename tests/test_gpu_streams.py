@@ -1,5 +1,6 @@
 """Calls of one ctx on several streams: a call starts after the last one, whichever stream that was on,
-and calls that are only captured in between change nothing about it."""
+and calls that are only captured in between change nothing about it; the experts' products with a split K
+do not meet and give the same bits everywhere."""
 
 import ctypes
 
@@ -134,4 +135,106 @@ def test_calls_that_take_turns_between_streams(gpu):
             assert torch.equal(run(streams), want)
         assert B.agg_ctx_status(ctx, here) == (0, -1)
     finally:
+        B.agg_ctx_destroy(ctx)
+
+
+# ------------------------------------------------------------------------------ a split K
+
+class _Split:
+    """A call whose K is split over workgroups."""
+    ROWS, E, COLS, DEPTH = 3, 2, 1024, 4096
+
+    def __init__(self, seed):
+        g = torch.Generator().manual_seed(seed)
+        assert B.agg_moe_gemm_shape("bf16", self.ROWS, self.E, self.COLS, self.DEPTH)[1] > 1
+        self.a = torch.randn(self.ROWS, self.DEPTH, generator=g).bfloat16().cuda()
+        self.b = (torch.randn(self.E, self.DEPTH, self.COLS, generator=g) / 64).bfloat16().cuda()
+        self.off = torch.tensor([0, 1 + seed % 2, self.ROWS], dtype=torch.int32, device="cuda")
+        self.out = torch.zeros(self.ROWS, self.COLS, dtype=torch.bfloat16, device="cuda")
+        self.want = None
+
+    def run(self, ctx, stream):
+        B.moe_gemm(ctx, self.ROWS, self.E, self.COLS, self.DEPTH, "bf16", self.a, self.b, self.off, self.out,
+                   stream=stream)
+
+    def check(self):
+        """The bits of the first run, which is compared with 64 bits."""
+        torch.cuda.synchronize()
+        if self.want is None:
+            a, b, cut = self.a.double().cpu(), self.b.double().cpu(), int(self.off[1])
+            ref = torch.cat([a[:cut] @ b[0], a[cut:] @ b[1]])
+            size = torch.cat([a[:cut].abs() @ b[0].abs(), a[cut:].abs() @ b[1].abs()])
+            # (half a unit of bfloat16, and 4096 fp32 products and sums)
+            assert ((self.out.double().cpu() - ref).abs() <= ref.abs() * 2.0 ** -8 + size * self.DEPTH * 2.0 ** -23).all()
+            self.want = self.out.clone()
+        assert torch.equal(self.out, self.want)
+        self.out.zero_()
+        torch.cuda.synchronize()
+
+
+def test_split_k_gives_the_same_bits_on_every_stream(gpu):
+    """One call after another, each on a stream that the ctx has not seen, short-lived ones among them."""
+    ctx, x = B.agg_ctx_create(0), _Split(1)
+    try:
+        streams = [torch.cuda.current_stream()] + [torch.cuda.Stream() for _ in range(7)]
+        for s in streams + streams[::-1]:
+            x.run(ctx, s)
+            x.check()
+        for _ in range(6):
+            with _Stream() as one, _Stream() as two:
+                for s in (one, two, one):
+                    x.run(ctx, s)
+                    x.check()
+    finally:
+        B.agg_ctx_destroy(ctx)
+
+
+def test_split_k_on_many_streams_at_once(gpu):
+    """Calls on eight streams, none of which waits for another, over and over."""
+    ctx, xs = B.agg_ctx_create(0), [_Split(i) for i in range(8)]
+    try:
+        for x in xs:
+            x.run(ctx, torch.cuda.current_stream())
+            x.check()
+        streams = [torch.cuda.Stream() for _ in xs]
+        for _ in range(5):
+            for _ in range(20):
+                for x, s in zip(xs, streams):
+                    x.run(ctx, s)
+            for x in xs:
+                x.check()
+    finally:
+        torch.cuda.synchronize()
+        B.agg_ctx_destroy(ctx)
+
+
+def test_split_k_in_graphs_replayed_at_once(gpu):
+    """Two graphs from torch's one capture stream, replayed on two streams while eager calls run on a
+    third, and after a reset."""
+    ctx, xs = B.agg_ctx_create(0), [_Split(i) for i in range(3)]
+    try:
+        for x in xs:
+            x.run(ctx, torch.cuda.current_stream())
+            x.check()
+        graphs = []
+        for x in xs[:2]:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                for _ in range(4):
+                    x.run(ctx, torch.cuda.current_stream())
+            graphs.append(graph)
+        streams = [torch.cuda.Stream() for _ in xs]
+        for turn in range(6):
+            for _ in range(10):
+                for graph, s in zip(graphs, streams):
+                    with torch.cuda.stream(s):
+                        graph.replay()
+                xs[2].run(ctx, streams[2])
+            for x in xs:
+                x.check()
+            if turn == 3:
+                B.agg_ctx_reset(ctx, torch.cuda.current_stream())
+                torch.cuda.synchronize()
+    finally:
+        torch.cuda.synchronize()
         B.agg_ctx_destroy(ctx)
