@@ -59,6 +59,9 @@ __device__ inline float reciprocal(float d) {
   return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
 }
 constexpr float kReciprocalMost = 8.5e37f;   // below 2^126
+// Scores are lost below 2^-128 (a sigmoid's exponential overflows) or rounded to multiples of 2^-149: at
+// most 2^-68 of a sum of 2^-60 or more. Below that sum sigmoid(x) is exp(x) to the last bit.
+constexpr float kScoresLost = 8.673617380e-19f;   // 2^-60
 
 // A group's score from its two largest keys.
 __device__ inline float group_key(int sigmoid, float b0, float b1) { return sigmoid && b1 > kNone ? b0 + b1 : b0; }
@@ -354,6 +357,22 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
   float scale = a.scale;
   if (a.renorm) {
     total = token_reduce<STEPS>(total, [](float x, float y) { return x + y; });
+    if (total < kScoresLost) {
+      // the chosen logits lie so far below the others (softmax, where a bias chooses) or below zero
+      // (sigmoid) that their scores are lost or few bits are left of them: both scores are then
+      // proportional to exp(x), which is taken from the largest chosen logit
+      float most = kNone;
+#pragma unroll
+      for (int o = 0; o < OUT; ++o) most = fmaxf(most, live && mine[o] >= 0 ? logit(mine[o]) : kNone);
+      most = token_reduce<STEPS>(most, [](float x, float y) { return fmaxf(x, y); });
+      total = 0.0f;
+#pragma unroll
+      for (int o = 0; o < OUT; ++o) {
+        w[o] = live && mine[o] >= 0 ? expf(logit(mine[o]) - most) : 0.0f;
+        total += w[o];
+      }
+      total = token_reduce<STEPS>(total, [](float x, float y) { return x + y; });
+    }
     scale = total > 0.0f ? a.scale / total : 0.0f;
   }
 #pragma unroll

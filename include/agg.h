@@ -583,8 +583,10 @@ enum { AGG_SCORE_SOFTMAX = 0, AGG_SCORE_SIGMOID = 1 };
  *   (softmax) or the sum of its two largest (sigmoid); only the top_groups best groups' experts
  *   stay candidates.
  *   ids[t, j], weights[t, j], j < top_k: the candidates by descending key, ties (experts and
- *   groups) to the lowest index; weight = p * scale, with renorm p over the sum of the chosen p.
- *   Where fewer than top_k candidates are left: id -1 and weight 0.
+ *   groups) to the lowest index; weight = p * scale, with renorm p over the sum of the chosen p
+ *   (also where these are too small for fp32). Where fewer than top_k candidates are left: id -1
+ *   and weight 0. Keys are fp32: sigmoid scores that are equal there, as all are for x below -88.7
+ *   (0) or above 17 (1), tie.
  */
 int moe_route(agg_ctx* ctx, int64_t tokens, int experts, int top_k, int logits_dtype,
               const void* logits, int64_t ld, const float* bias, int score, int groups,

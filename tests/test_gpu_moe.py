@@ -334,6 +334,33 @@ def test_route_bias(ctx, T, E, k, groups, top_groups, score):
     assert (np.abs(w - want_w)[same] <= want_w[same] * (E * EPS32 + FINE) + 1e-9).all()
 
 
+@pytest.mark.parametrize("T,E,k,groups,top_groups", [
+    (9, 7, 7, 1, 1), (70, 64, 4, 1, 1), (33, 60, 2, 1, 1), (40, 256, 8, 8, 4), (17, 256, 8, 1, 1), (5, 1000, 16, 1, 1),
+    (9, 1024, 16, 16, 5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("low,high", [(-300, -95), (-100, -80), (-110, -60), (-86, -69)])
+def test_route_renormalises_scores_that_underflow(ctx, T, E, k, groups, top_groups, score, low, high):
+    """A bias chooses experts whose scores are below fp32's numbers, or just above: the weights are their
+    scores' shares all the same. Logits and biases are multiples of 1/8 and 1/16, so differences of
+    logits are exact, and a key is its bias wherever a choice depends on it."""
+    g = _gen(T + E)
+    x = torch.randint(low * 8, high * 8 + 1, (T, E), generator=g).float() / 8
+    bias = (torch.randperm(E, generator=g).float() + 1) / 16
+    if score == "softmax":          # experts that take all the probability, never chosen unless all are
+        x[:, ::5] = 0
+        bias[::5] -= 1000
+    if T > 5:
+        x[3] = -math.inf
+        x[4, 1:] = -math.inf
+    want_ids, want_w = _route_ref(x.double().numpy(), bias.double().numpy(), score, groups, top_groups, k, True, 2.5)
+    ids, w = _run_route(ctx, x.cuda(), k, score=score, bias=bias.cuda(), groups=groups, top_groups=top_groups, scale=2.5)
+    np.testing.assert_array_equal(ids, want_ids)
+    held = (want_ids >= 0).any(1)
+    np.testing.assert_allclose(w.sum(1)[held], 2.5, rtol=(k + 2) * EPS32)
+    # (beside fp32's roundings: 2^-49 of the sum for what lies below its numbers)
+    assert (np.abs(w - want_w) <= want_w * (E * EPS32 + FINE) + k * 2.5 * 2.0 ** -49).all(), np.abs(w - want_w).max()
+
+
 def test_route_many_tokens_distinct_logits(ctx):
     """Every token's logits are a permutation of distinct values: the order is known without a sort."""
     T, E, k = 3001, 256, 8
