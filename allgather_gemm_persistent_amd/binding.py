@@ -194,6 +194,13 @@ def _stream(s):
     return int(s)
 
 
+def cuda_device(device="cuda") -> torch.device:
+    """`device` with its index: a cuda device without one is torch's current device. A ctx belongs to
+    one device, its calls' tensors lie there."""
+    d = torch.device(device)
+    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
 def _ptr_array(seq):
     if seq is None:
         return None

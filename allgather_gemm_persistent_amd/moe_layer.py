@@ -31,7 +31,7 @@ class MoeLayer:
 
     def __init__(self, tokens, top_k, norm, router, w_up, w_down, up_scale=None, down_scale=None, first=0,
                  score="softmax", bias=None, groups=1, top_groups=1, scale=1.0, eps=1e-6, device="cuda"):
-        self.device = torch.device(device)
+        self.device = B.cuda_device(device)
         to = lambda t: None if t is None else t.to(self.device).contiguous()  # noqa: E731
         self.norm, self.router, self.w_up, self.w_down = to(norm), to(router), to(w_up), to(w_down)
         self.up_scale, self.down_scale, self.bias = to(up_scale), to(down_scale), to(bias)
@@ -57,7 +57,7 @@ class MoeLayer:
         if self.dtype == "fp8":
             self.x8, self.x_scale = new(tokens, h, dtype=fp8), new(tokens, dtype=f32)
             self.mid8, self.mid_scale = new(pairs, self.inner, dtype=fp8), new(pairs, dtype=f32)
-        self.ctx = B.agg_ctx_create(self.device.index or 0)
+        self.ctx = B.agg_ctx_create(self.device.index)
 
     def run(self, x, residual=None, stream=None):
         """x: tokens x hidden, bf16 or fp32 (what gemm_ar or gemm_rs left); residual: bf16 or None, then

@@ -28,7 +28,7 @@ class AgWorkload:
         self.n = b_kn.shape[1]
         self.m = world * self.m_shard
         self.scale_a, self.scale_b = float(scale_a), float(scale_b)
-        self.device = torch.device(device)
+        self.device = B.cuda_device(device)
         tdt = shards[0].dtype
         self.peers = [s.to(self.device) if p != rank else None for p, s in enumerate(shards)]
         self.local = shards[rank].to(self.device)
@@ -42,7 +42,7 @@ class AgWorkload:
         self.b = self.device_weight(b_kn)
         self.c = torch.zeros(self.m, self.n, dtype=torch.bfloat16, device=self.device)
         self.copy_stream = None     # the ctx runs the copies on its own streams
-        self.ctx = B.agg_ctx_create(self.device.index or 0)
+        self.ctx = B.agg_ctx_create(self.device.index)
         B.agg_ctx_set_producer(self.ctx, producer)
         if tile:
             B.agg_ctx_set_tile(self.ctx, *tile)
@@ -120,7 +120,7 @@ class RsWorkload:
         self.m, self.k = a.shape
         self.n = b_kn.shape[1]
         self.mb = self.m // world
-        self.device = torch.device(device)
+        self.device = B.cuda_device(device)
         self.a = a.to(self.device)
         self.b = b_kn.contiguous().to(self.device)
         self.peers = [peers[p].to(self.device) if p != rank else None for p in range(world)]
@@ -132,7 +132,7 @@ class RsWorkload:
                                 device=self.device)
         self.out = torch.zeros(self.mb, self.n, dtype=torch.float32, device=self.device)
         self.copy_stream = None     # the ctx runs the copies on its own streams
-        self.ctx = B.agg_ctx_create(self.device.index or 0)
+        self.ctx = B.agg_ctx_create(self.device.index)
         B.agg_ctx_set_producer(self.ctx, producer)
         if tile:
             B.agg_ctx_set_tile(self.ctx, *tile)
@@ -168,7 +168,7 @@ class ArWorkload:
         self.world, self.rank, self.chunk_rows = world, rank, chunk_rows
         self.m, self.k = a.shape
         self.n = b_kn.shape[1]
-        self.device = torch.device(device)
+        self.device = B.cuda_device(device)
         self.a = a.to(self.device)
         self.b = b_kn.contiguous().to(self.device)
         self.peers = [peers[p].to(self.device) if p != rank else None for p in range(world)]
@@ -179,7 +179,7 @@ class ArWorkload:
         self.send = torch.zeros(self.m, self.n, dtype=torch.float32, device=self.device)
         self.out = torch.zeros(self.m, self.n, dtype=torch.float32, device=self.device)
         self.copy_stream = None
-        self.ctx = B.agg_ctx_create(self.device.index or 0)
+        self.ctx = B.agg_ctx_create(self.device.index)
         B.agg_ctx_set_producer(self.ctx, producer)
         if tile:
             B.agg_ctx_set_tile(self.ctx, *tile)
@@ -218,7 +218,7 @@ class FfnWorkload:
         self.m_shard, self.k1 = shards[0].shape
         self.n1, self.n2 = w1.shape[1], w2.shape[1]
         self.m = world * self.m_shard
-        self.device = torch.device(device)
+        self.device = B.cuda_device(device)
         dev = self.device
         self.peers = [s.to(dev) if p != rank else None for p, s in enumerate(shards)]
         self.local = shards[rank].to(dev)
@@ -237,7 +237,7 @@ class FfnWorkload:
         self.send = torch.zeros(max(world - 1, 1), self.m_shard, self.n2, dtype=torch.float32, device=dev)
         self.out = torch.zeros(self.m_shard, self.n2, dtype=torch.float32, device=dev)
         self.copy_stream = None
-        self.ctx = B.agg_ctx_create(dev.index or 0)
+        self.ctx = B.agg_ctx_create(dev.index)
         B.agg_ctx_set_producer(self.ctx, producer)
 
     def reset_local(self):

@@ -180,3 +180,35 @@ def test_binding_refuses_what_the_call_would_read_wrongly(lib):
     with pytest.raises(B.AggError, match="contiguous and hold"):
         B.moe_plan(None, 4, 2, torch.zeros(7, dtype=torch.int32), 0, 8, None, None, None, None)
     assert B.moe_plan_words(512, 2, 7) == 16
+
+
+# ------------------------------------------------------------------------------ the layer
+
+class _Weight:
+    """A tensor that lies wherever it was sent."""
+
+    def __init__(self, *shape, places):
+        self.shape, self.dtype, self.places = shape, torch.bfloat16, places
+
+    def to(self, device):
+        self.places.append(torch.device(device))
+        return self
+
+    def contiguous(self):
+        return self
+
+
+@pytest.mark.parametrize("device,current,want", [("cuda", 3, 3), ("cuda", 0, 0), ("cuda:2", 3, 2),
+                                                 (torch.device("cuda", 1), 0, 1)])
+def test_layer_and_its_ctx_on_one_device(monkeypatch, device, current, want):
+    """Without an index a layer lies on torch's current device, its ctx and every buffer with it."""
+    from allgather_gemm_persistent_amd import moe_layer
+    places, ctxs = [], []
+    new = lambda *shape, dtype, device: places.append(torch.device(device))  # noqa: E731
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(torch, "empty", new)
+    monkeypatch.setattr(torch, "zeros", new)
+    monkeypatch.setattr(B, "agg_ctx_create", lambda index=0: ctxs.append(index))
+    w = lambda *shape: _Weight(*shape, places=places)  # noqa: E731
+    moe_layer.MoeLayer(4, 2, w(64), w(64, 8), w(8, 64, 64), w(8, 32, 64), bias=w(8), device=device)
+    assert ctxs == [want] and len(places) > 10 and set(places) == {torch.device("cuda", want)}
