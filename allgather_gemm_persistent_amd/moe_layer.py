@@ -26,11 +26,12 @@ class MoeLayer:
     norm: bf16[hidden]; router: bf16 hidden x experts; w_up: n_local x hidden x 2 inner (gate columns,
     then up columns); w_down: n_local x inner x hidden, both bf16, or float8_e4m3fn with up_scale
     (n_local x 2 inner) and down_scale (n_local x hidden), fp32. Experts [first, first + n_local) are
-    this rank's. `tokens` is the most a call takes.
+    this rank's. score, bias, groups, top_groups, renorm and scale are moe_route's. `tokens` is the most
+    a call takes.
     """
 
     def __init__(self, tokens, top_k, norm, router, w_up, w_down, up_scale=None, down_scale=None, first=0,
-                 score="softmax", bias=None, groups=1, top_groups=1, scale=1.0, eps=1e-6, device="cuda"):
+                 score="softmax", bias=None, groups=1, top_groups=1, scale=1.0, eps=1e-6, device="cuda", renorm=True):
         self.device = B.cuda_device(device)
         to = lambda t: None if t is None else t.to(self.device).contiguous()  # noqa: E731
         self.norm, self.router, self.w_up, self.w_down = to(norm), to(router), to(w_up), to(w_down)
@@ -39,7 +40,7 @@ class MoeLayer:
         self.n_local, self.inner = w_down.shape[0], w_down.shape[1]
         self.dtype = "fp8" if w_up.dtype == torch.float8_e4m3fn else "bf16"
         self.tokens, self.top_k, self.first, self.eps = tokens, top_k, first, eps
-        self.routing = dict(score=score, groups=groups, top_groups=top_groups, scale=scale)
+        self.routing = dict(score=score, groups=groups, top_groups=top_groups, renorm=renorm, scale=scale)
         pairs, h = tokens * top_k, self.hidden
         bf16, fp8, f32, i32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
         new = lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device=self.device)  # noqa: E731

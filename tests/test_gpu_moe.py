@@ -802,6 +802,25 @@ def test_moe_layer(gpu, T, dtype, held):
         layer.close()
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_moe_layer_weights(gpu, score, renorm):
+    """A layer whose weights are the chosen probabilities themselves, times a scale, or their shares."""
+    from allgather_gemm_persistent_amd.moe_layer import random_layer
+    T, H, F, E, k = 21, 128, 64, 16, 4
+    layer = random_layer(T, H, F, E, k, seed=3, score=score, renorm=renorm, scale=1.5)
+    try:
+        out = layer.run(torch.randn(T, H, generator=_gen(4)).cuda()).cpu()
+        ids, w = layer.ids.cpu(), layer.weights.cpu().double()
+        want_ids, want_w = _route_ref(layer.logits.cpu().double().numpy(), None, score, 1, 1, k, renorm, 1.5)
+        assert (ids.numpy() == want_ids).all()
+        assert (np.abs(w.numpy() - want_w) <= want_w * (E * EPS32 + FINE)).all()
+        terms = layer.y.cpu().double()[layer.token_slot.cpu().long()] * w[:, :, None]
+        _within(out, terms.sum(1), terms.abs().sum(1) * (k + 1) * EPS32 + 1e-30, "combine")
+    finally:
+        layer.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 def test_split_k_in_a_replayed_graph_and_after_reset(ctx, dtype):
     """K in parts, captured and replayed between eager calls of other rows; then after a reset."""
