@@ -45,7 +45,11 @@ class MoeLayer:
         bf16, fp8, f32, i32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
         new = lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device=self.device)  # noqa: E731
         self.x = new(tokens, h, dtype=bf16)                     # normalised rows
-        self.logits = new(tokens, self.experts, dtype=bf16)
+        # (the product wants rows of whole 16 bytes: experts that are no multiple of 8 are padded)
+        pad = -self.experts % 8
+        self.router_b = torch.nn.functional.pad(self.router, (0, pad)).contiguous() if pad else self.router
+        self.logits_c = new(tokens, self.experts + pad, dtype=bf16)
+        self.logits = self.logits_c[:, :self.experts] if pad else self.logits_c
         self.ids, self.weights = new(tokens, top_k, dtype=i32), new(tokens, top_k, dtype=f32)
         self.offsets = new(self.n_local + 1, dtype=i32)
         self.slot_token, self.token_slot = new(pairs, dtype=i32), new(tokens, top_k, dtype=i32)
@@ -71,8 +75,8 @@ class MoeLayer:
         pairs, fp8 = t * k, self.dtype == "fp8"
         B.rms_norm(self.ctx, t, h, x, self.norm, self.x, residual=residual, residual_out=residual, eps=self.eps,
                    stream=s)
-        B.ag_gemm(self.ctx, 1, 0, t, self.experts, h, t, "bf16", 1.0, 1.0, None, self.x, None, self.router,
-                  self.logits, stream=s)
+        B.ag_gemm(self.ctx, 1, 0, t, self.router_b.shape[1], h, t, "bf16", 1.0, 1.0, None, self.x, None,
+                  self.router_b, self.logits_c, stream=s)
         B.moe_route(self.ctx, t, self.experts, k, self.logits, self.ids, self.weights, bias=self.bias, stream=s,
                     **self.routing)
         B.moe_plan(self.ctx, t, k, self.ids, self.first, self.n_local, self.offsets, self.slot_token,

@@ -821,6 +821,29 @@ def test_moe_layer_weights(gpu, score, renorm):
         layer.close()
 
 
+@pytest.mark.parametrize("T,E,k", [(1, 60, 4), (33, 60, 4), (300, 7, 2), (20, 1, 1)])
+def test_moe_layer_of_any_number_of_experts(gpu, T, E, k):
+    """Expert counts whose router has no rows of whole 16 bytes."""
+    from allgather_gemm_persistent_amd.moe_layer import random_layer
+    H, F = 128, 64
+    layer = random_layer(T, H, F, E, k, seed=E)
+    try:
+        out = layer.run(torch.randn(T, H, generator=_gen(T)).cuda()).cpu()
+        xn, logits = layer.x.cpu(), layer.logits.cpu()
+        assert logits.shape == (T, E)
+        ref = xn.double() @ layer.router.double().cpu()
+        size = xn.double().abs() @ layer.router.double().cpu().abs()
+        _within(logits, ref, ref.abs() * HALF_BF16 + size * H * EPS32 + 1e-30, "logits")
+        want_ids, want_w = _route_ref(logits.double().numpy(), None, "softmax", 1, 1, k, True, 1.0)
+        assert (layer.ids.cpu().numpy() == want_ids).all()
+        w = layer.weights.cpu().double()
+        assert (np.abs(w.numpy() - want_w) <= want_w * (E * EPS32 + FINE)).all()
+        terms = layer.y.cpu().double()[layer.token_slot.cpu().long()] * w[:, :, None]
+        _within(out, terms.sum(1), terms.abs().sum(1) * (k + 1) * EPS32 + 1e-30, "combine")
+    finally:
+        layer.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 def test_split_k_in_a_replayed_graph_and_after_reset(ctx, dtype):
     """K in parts, captured and replayed between eager calls of other rows; then after a reset."""
