@@ -592,8 +592,8 @@ def _rows(x, rows, cols, what, dtype=None):
         raise AggError(AGG_E_ARG, what, "must have contiguous columns")
     if not x.is_cuda and shape[0] and cols:
         raise AggError(AGG_E_ARG, what, f"must be a device tensor, got {x.device}")
-    # (a single row, or none, may carry any stride)
-    return x.data_ptr(), ld if rows > 1 or ld > cols else cols
+    # (a single row, or none, may carry any stride: none is taken)
+    return x.data_ptr(), ld if rows > 1 else cols
 
 
 def _flat(x, count, what, dtype):

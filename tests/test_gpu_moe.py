@@ -211,6 +211,32 @@ def test_fp8_rows_of_subnormal_scales(ctx, units):
     _within(q.float(), exact, torch.maximum(exact.abs() * 2.0 ** -4, torch.tensor(2.0 ** -10)) + exact.abs() * FINE, "fp8")
 
 
+@pytest.mark.parametrize("extra", [1, 5, 36])
+def test_a_single_row_of_any_stride(ctx, extra):
+    """Where there is one row no stride is taken, so one that no other row could have is no error."""
+    cols, s = 64, torch.cuda.current_stream()
+    wide = lambda t: _strided(t, extra)  # noqa: E731
+    x, r, w = torch.randn(1, cols, generator=_gen(extra)), torch.randn(1, cols, generator=_gen(1)).bfloat16(), torch.ones(cols).bfloat16()
+    out, ro = wide(torch.zeros(1, cols).bfloat16()), wide(torch.zeros(1, cols).bfloat16())
+    B.rms_norm(ctx, 1, cols, wide(x), w.cuda(), out, residual=wide(r), residual_out=ro, stream=s)
+    ref, y = _norm_ref(x, r, w, 1e-6)
+    _within(out, y, y.abs() * (HALF_BF16 + cols * EPS32 + FINE) + 1e-30, "y")
+    _within(ro, ref, ref.abs() * (HALF_BF16 + EPS32), "residual_out")
+    q, scales = wide(torch.zeros(1, cols).to(torch.float8_e4m3fn)), torch.zeros(1, device="cuda")
+    B.quant_rows(ctx, 1, cols, wide(x), q, scales=scales, stream=s)
+    _check_fp8(q.cpu(), scales.cpu(), x.double(), 1)
+    a, b = wide(r), torch.randn(1, cols, 16, generator=_gen(2)).bfloat16()
+    c = torch.zeros(1, 16, dtype=torch.bfloat16, device="cuda")
+    B.moe_gemm(ctx, 1, 1, 16, cols, "bf16", a, b.cuda(), torch.tensor([0, 1], dtype=torch.int32, device="cuda"), c, stream=s)
+    ref, size = r.double() @ b[0].double(), r.double().abs() @ b[0].double().abs()
+    _within(c, ref, ref.abs() * HALF_BF16 + size * (cols * EPS32 + FINE), "product")
+    # two rows of such a stride are still refused
+    with pytest.raises(B.AggError) as e:
+        B.quant_rows(ctx, 2, cols, _strided(torch.zeros(2, cols).bfloat16(), 4), torch.zeros(2, cols, dtype=torch.float8_e4m3fn, device="cuda"),
+                     scales=torch.zeros(2, device="cuda"), stream=s)
+    assert e.value.code == B.AGG_E_ARG
+
+
 # ------------------------------------------------------------------------------ routing
 
 def _route_ref(x, bias, score, groups, top_groups, k, renorm, scale):
