@@ -138,6 +138,19 @@ int check_stride(int64_t ld, int64_t cols, int elem, const char* what) {
   return AGG_OK;
 }
 
+// what moe_gemm takes of its sizes
+int check_moe_sizes(int64_t slots, int n_experts, int64_t n, int64_t k, int dtype, int gated, int64_t a_rows) {
+  if (slots < 0 || n < 0 || k < 0 || a_rows < 0) return fail(AGG_E_ARG, "negative size");
+  if (n_experts < 1 || n_experts > AGG_MAX_EXPERTS) return fail(AGG_E_ARG, "%d experts, not 1 to %d", n_experts, AGG_MAX_EXPERTS);
+  if (dtype != AGG_BF16 && dtype != AGG_FP8_E4M3) return fail(AGG_E_ARG, "unknown dtype %d", dtype);
+  const int eb = dtype == AGG_FP8_E4M3 ? 1 : 2;
+  if ((k * eb) % 16) return fail(AGG_E_ARG, "k * %d bytes = %lld is not a multiple of 16", eb, (long long)(k * eb));
+  if ((n * eb) % 16 || n % 8) return fail(AGG_E_ARG, "n %lld: rows of b and out are multiples of 16 bytes", (long long)n);
+  if (slots > kMostRows || a_rows > kMostRows || n > kMostRows || k > kMostRows) return fail(AGG_E_UNSUPPORTED, "dimension beyond 2^30");
+  if (k * n * (gated ? 2 : 1) * eb >= (int64_t(1) << 31)) return fail(AGG_E_UNSUPPORTED, "one expert's weight is 2 GiB or more");
+  return AGG_OK;
+}
+
 }  // namespace
 
 extern "C" int agg_check_norm_args(int64_t rows, int64_t cols, int x_dtype, const void* x, int64_t ld_x,
@@ -215,14 +228,8 @@ extern "C" int agg_check_moe_gemm_args(int64_t slots, int n_experts, int64_t n, 
                                        const int32_t* slot_token, const void* b, const float* b_scale,
                                        const int32_t* offsets, const void* out) {
   clear_error();
-  if (slots < 0 || n < 0 || k < 0 || a_rows < 0) return fail(AGG_E_ARG, "negative size");
-  if (n_experts < 1 || n_experts > AGG_MAX_EXPERTS) return fail(AGG_E_ARG, "%d experts, not 1 to %d", n_experts, AGG_MAX_EXPERTS);
-  if (dtype != AGG_BF16 && dtype != AGG_FP8_E4M3) return fail(AGG_E_ARG, "unknown dtype %d", dtype);
+  CHECK(check_moe_sizes(slots, n_experts, n, k, dtype, gated, a_rows));
   const int eb = dtype == AGG_FP8_E4M3 ? 1 : 2;
-  if ((k * eb) % 16) return fail(AGG_E_ARG, "k * %d bytes = %lld is not a multiple of 16", eb, (long long)(k * eb));
-  if ((n * eb) % 16 || n % 8) return fail(AGG_E_ARG, "n %lld: rows of b and out are multiples of 16 bytes", (long long)n);
-  if (slots > kMostRows || a_rows > kMostRows || n > kMostRows || k > kMostRows) return fail(AGG_E_UNSUPPORTED, "dimension beyond 2^30");
-  if (k * n * (gated ? 2 : 1) * eb >= (int64_t(1) << 31)) return fail(AGG_E_UNSUPPORTED, "one expert's weight is 2 GiB or more");
   if (slots == 0 || n == 0) return AGG_OK;
   CHECK(need(offsets, "offsets"));
   CHECK(need(out, "out"));
@@ -261,7 +268,9 @@ extern "C" int agg_moe_gemm_shape(int dtype, int64_t slots, int n_experts, int64
                                   int* ksplit, int* bm, int* bn) {
   clear_error();
   if (!ksplit || !bm || !bn) return fail(AGG_E_ARG, "agg_moe_gemm_shape: NULL output");
-  const ExpertShape s = choose_expert_shape(dtype, slots, std::max(n_experts, 1), n, k, gated, 256);
+  CHECK(check_moe_sizes(slots, n_experts, n, k, dtype, gated, 0));
+  // (a product without columns has no strips to divide the units among)
+  const ExpertShape s = choose_expert_shape(dtype, slots, n_experts, std::max<int64_t>(n, 1), k, gated, 256);
   *ksplit = s.stream ? s.ksplit : 0;
   *bm = s.stream ? 0 : s.tile.bm;
   *bn = s.stream ? 0 : s.tile.bn;

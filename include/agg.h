@@ -741,7 +741,8 @@ int agg_check_combine_args(int64_t tokens, int top_k, int64_t n, int64_t slots, 
                            const void* out);
 
 /* How moe_gemm multiplies a call on a whole MI355X: *ksplit > 0: the weights streamed through
- * registers, K in that many parts (then *bm = *bn = 0); *ksplit 0: tiles of *bm x *bn.
+ * registers, K in that many parts (then *bm = *bn = 0); *ksplit 0: tiles of *bm x *bn. Sizes that
+ * moe_gemm refuses are refused; sizes without work still name a kernel.
  */
 int agg_moe_gemm_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated,
                        int* ksplit, int* bm, int* bn);

@@ -182,6 +182,23 @@ def test_binding_refuses_what_the_call_would_read_wrongly(lib):
     assert B.moe_plan_words(512, 2, 7) == 16
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-64), B.AGG_E_ARG),
+    (dict(k=-64), B.AGG_E_ARG), (dict(slots=-4), B.AGG_E_ARG), (dict(n_experts=0), B.AGG_E_ARG),
+    (dict(n_experts=-2), B.AGG_E_ARG), (dict(n_experts=1025), B.AGG_E_ARG), (dict(dtype=5), B.AGG_E_ARG),
+    (dict(n=60), B.AGG_E_ARG), (dict(k=60), B.AGG_E_ARG), (dict(slots=1 << 62), B.AGG_E_UNSUPPORTED),
+    (dict(n=1 << 62, k=1 << 62), B.AGG_E_UNSUPPORTED), (dict(n=1 << 20, k=1 << 20), B.AGG_E_UNSUPPORTED)])
+def test_moe_gemm_shape_refuses_what_the_product_does(kw, code):
+    """Sizes of no product are an error, and sizes without work are not, rather than the end of the
+    process (no columns, and sizes whose products wrap, were a division by zero)."""
+    args = dict(dtype="bf16", slots=4, n_experts=2, n=64, k=64)
+    for empty in (dict(), dict(n=0), dict(slots=0), dict(k=0), dict(n=0, slots=0, k=0)):
+        assert B.agg_moe_gemm_shape(**{**args, **empty})[0] in ("stream", "tiles")
+    with pytest.raises(B.AggError) as e:
+        B.agg_moe_gemm_shape(**{**args, **kw})
+    assert e.value.code == code
+
+
 # ------------------------------------------------------------------------------ the layer
 
 class _Weight:
