@@ -46,7 +46,7 @@ struct CombineArgs {
   int64_t tokens, n, slots;
   int top_k, out_fp32;
 };
-hipError_t launch_combine(const CombineArgs& a, int cus, hipStream_t stream);
+hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
 
 // ---- routing
 struct RouteArgs {
@@ -59,7 +59,7 @@ struct RouteArgs {
   int logits_bf16, sigmoid, renorm;
   float scale;
 };
-hipError_t launch_route(const RouteArgs& a, int cus, hipStream_t stream);
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 
 // (token, choice) pairs of one block of the plan's kernels
 constexpr int kPlanPairs = AGG_PLAN_PAIRS;

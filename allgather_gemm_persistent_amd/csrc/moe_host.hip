@@ -62,7 +62,7 @@ extern "C" int moe_route(agg_ctx* ctx, int64_t tokens, int experts, int top_k, i
   if (tokens == 0) return AGG_OK;
   const RouteArgs a{logits, bias, ids, weights, tokens, ld, experts, top_k, groups, top_groups,
                     logits_dtype == AGG_BF16, score == AGG_SCORE_SIGMOID, renorm != 0, scale};
-  HIP_TRY(launch_route(a, ctx_units(ctx), S(stream)));
+  HIP_TRY(launch_route(a, S(stream)));
   return AGG_OK;
 }
 
@@ -134,6 +134,6 @@ extern "C" int moe_combine(agg_ctx* ctx, int64_t tokens, int top_k, int64_t n, i
   if (tokens == 0 || n == 0) return AGG_OK;
   const CombineArgs a{static_cast<const uint16_t*>(y), token_slot, weights, out, tokens, n, slots, top_k,
                       out_dtype == AGG_FP32};
-  HIP_TRY(launch_combine(a, ctx_units(ctx), S(stream)));
+  HIP_TRY(launch_combine(a, S(stream)));
   return AGG_OK;
 }

@@ -139,7 +139,7 @@ __device__ inline void keep_groups(float (&key)[V], int sigmoid, int groups, int
 // with 8 groups of which 4 stay. FULL drops the bounds of experts that fill the lanes.
 template <int STEPS, int V, bool BF16, bool FULL>
 __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
-  constexpr int L = 1 << STEPS, TOKENS = 256 / L, E = L * V;
+  constexpr int L = 1 << STEPS, TOKENS = 256 / L;
   constexpr int OUT = AGG_MAX_TOP_K > L ? AGG_MAX_TOP_K / L : 1;   // choices a lane writes
   __shared__ __attribute__((aligned(16))) float keys[TOKENS][L * (V + 4)];
   __shared__ float group_score[TOKENS][AGG_MAX_GROUPS];
@@ -409,8 +409,7 @@ static hipError_t launch_route_lv(RouteArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_route(const RouteArgs& a, int cus, hipStream_t stream) {
-  (void)cus;
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
   if (a.experts <= 64) return launch_route_lv<3, 8>(a, stream);
   if (a.experts <= 128) return launch_route_lv<4, 8>(a, stream);
   if (a.experts <= 256) return launch_route_lv<4, 16>(a, stream);

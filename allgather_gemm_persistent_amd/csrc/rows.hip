@@ -264,8 +264,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
   }
 }
 
-hipError_t launch_combine(const CombineArgs& a, int cus, hipStream_t stream) {
-  (void)cus;
+hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
   // (grid.y is limited to 65535 blocks: more tokens go in further launches)
   for (int64_t t0 = 0; t0 < a.tokens; t0 += 65535) {
     CombineArgs p = a;
