@@ -21,9 +21,10 @@ double ceil_div(double a, double b) { return std::ceil(a / b); }
 
 // The kernel whose time is expected to be the least. The times are fits to measured calls (8 experts of
 // 8192 x 7168 and 3584 x 8192, 8 of 1024 x 4096, 30 of 1000 x 1032, 32 of 2048 x 1536, 60 of 256 x
-// 2816; 1 to 400 rows an expert, bf16 and fp8) and choose the fastest of the kernels, or one within 10%
-// of it, on 9 of 10 of them (and on 40 random calls within 11% on average, the single runs' noise among
-// it). What they stand for, at 8 experts of 8192 x 7168 bf16, us:
+// 2816; 1 to 400 rows an expert, bf16 and fp8). Against every kernel forced, the choice is within 10% of
+// the fastest in 68 of 84 such calls and in 36 of 40 random ones; it takes 4.9% and 3.3% longer on
+// average and at worst 1.51 times as long (32 experts of 2048 x 1536 bf16, 192 rows each). What the fits
+// stand for, at 8 experts of 8192 x 7168 bf16, us:
 //   rows an expert      4    16    48    96   192   384
 //   streaming         152   159   329   620  1128  2139
 //   256 x 256 tiles   175   174   175   184   211   404

@@ -7,6 +7,11 @@ moe_gemm -> moe_combine. With fp8 experts the normalised rows and the rows betwe
 are quantised with a scale per row (quant_rows). A rank that holds a part of the experts gets the sum
 over its own; the ranks' sums meet in a ReduceScatter or AllReduce of the caller's.
 
+Roundings between the steps: the normalised rows, the router's logits and the rows after each product are
+bf16, what the operators between them read and write (the weights of a choice are fp32, and so are the sums
+inside every step and the layer's output). With fp8 experts the normalised rows are quantised from their
+bf16 form, which the router takes, since rms_norm has one output.
+
 PyTorch provides device memory and streams only; every step runs in libagg.
 """
 

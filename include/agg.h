@@ -620,8 +620,10 @@ int moe_plan(agg_ctx* ctx, int64_t tokens, int top_k, const int32_t* ids, int fi
  *   a_scale          fp8: fp32[a_rows]; b_scale: fp32[n_experts, columns of b]: each row and each
  *                    column of the product times its scale. Both ignored for bf16
  *   out              slots x n bf16, rounded once from the fp32 product
- * Few rows an expert stream the weights through registers, more take tiles (agg_moe_gemm_shape); a
- * shape forced by agg_ctx_set_tile applies here too.
+ * Few rows an expert stream the weights through registers, more take tiles (agg_moe_gemm_shape): the
+ * choice counts `slots`, so a bound far above the rows that are there gives a kernel for more rows
+ * than there are (the result is right, the call slower). A shape forced by agg_ctx_set_tile applies
+ * here too.
  * Limits: k * elem, n * elem and n * 2 bytes multiples of 16, one expert's weight below 2 GiB, and
  * with slot_token A below 2 GiB.
  */
