@@ -149,13 +149,12 @@ struct agg_ctx {
                                              //   counters are in the device's static scratch)
   hipEvent_t ev_upload = nullptr;
   bool upload_pending = false;
-  // the stream of the last call, captured ones aside, that used the ctx's scratch; the event a call on
-  // another one waits for, whether the last call recorded it, and how many more calls do
+  // whether the call in turn is not captured; of the last such call, its stream and the event that its
+  // end completes (ev_order, or the end of a timed launch)
+  bool eager = false;
   hipStream_t last_stream = nullptr;
-  bool any_call = false;
+  hipEvent_t order_event = nullptr;
   hipEvent_t ev_order = nullptr;
-  bool order_recorded = false;
-  int order_turns = 0;
   MoeWorkspace* moe_ws = nullptr;            // moe_gemm's workspaces, the newest first
 };
 
@@ -283,47 +282,34 @@ bool capturing(hipStream_t s) {
 
 // A call's turn. A ctx serialises its calls, which share its scratch: a call on another stream than the
 // last one's starts after it. The last one's stream may be gone by then, or in the middle of a capture,
-// so nothing is asked of it: either an event was recorded on it right after that call, or the device is
-// waited for. An event after every call would take 2.9 us of each, so one is recorded after the ctx's
-// first kFirstTurns calls and after the kTurns calls from a change of streams on: a program that stays
-// on a stream pays nothing, one that warms up on one stream and goes on on another, or that takes turns
-// between streams, does not wait on the host. A call under capture enqueues nothing, so it neither waits
-// nor counts as the last one: its order, at every replay, is the caller's.
+// and a wait for the whole device would end every capture in progress, so each call leaves an event
+// behind: its last kernel carries one (the dispatch completes it: nothing on the GPU, 0.6 us at most on the
+// host; a record after it would take 2.9 us of the GPU), and a call that ends in joins of other streams
+// records one. A call under capture enqueues nothing, so it neither waits nor leaves an event: its
+// order, at every replay, is the caller's.
 class Turn {
  public:
-  Turn(agg_ctx* ctx, hipStream_t s) : ctx_(ctx), s_(s) {
-    if (ctx->any_call && ctx->last_stream == s) return;
-    if (capturing(s)) return;
-    if (ctx->any_call) {
-      if (ctx->order_recorded) {
-        if (hipError_t e = hipStreamWaitEvent(s, ctx->ev_order, 0))
-          rc = fail(AGG_E_HIP, "hipStreamWaitEvent: %s", hipGetErrorString(e));
-      } else if (hipError_t e = hipDeviceSynchronize()) {
-        (void)hipGetLastError();
-        rc = fail(AGG_E_STATE, "a call on another stream than the last one's cannot wait for it: %s", hipGetErrorString(e));
+  Turn(agg_ctx* ctx, hipStream_t s) : ctx_(ctx) {
+    ctx->eager = !capturing(s);
+    if (!ctx->eager) return;
+    if (ctx->order_event && ctx->last_stream != s)
+      if (hipError_t e = hipStreamWaitEvent(s, ctx->order_event, 0)) {
+        rc = fail(AGG_E_HIP, "hipStreamWaitEvent: %s", hipGetErrorString(e));
+        return;
       }
-      if (rc) return;
-    }
-    ctx->order_turns = ctx->any_call ? kTurns : kFirstTurns;
     ctx->last_stream = s;
-    ctx->any_call = true;
   }
-  ~Turn() {
-    if (!ctx_->order_recorded && ctx_->order_turns == 0) return;
-    // (a call under capture, or one that was refused its turn, leaves the last one's event)
-    if (rc || ctx_->last_stream != s_ || capturing(s_)) return;
-    ctx_->order_recorded = ctx_->order_turns > 0 && hipEventRecord(ctx_->ev_order, s_) == hipSuccess;
-    if (ctx_->order_turns > 0) --ctx_->order_turns;
-  }
+  ~Turn() { ctx_->eager = false; }
   Turn(const Turn&) = delete;
   Turn& operator=(const Turn&) = delete;
   int rc = AGG_OK;
 
  private:
-  static constexpr int kFirstTurns = 4, kTurns = 16;
   agg_ctx* const ctx_;
-  const hipStream_t s_;
 };
+
+// The event that a launch of the call in turn carries, and that the next call on another stream waits for.
+hipEvent_t order_event(agg_ctx* ctx) { return ctx->eager ? ctx->order_event = ctx->ev_order : nullptr; }
 
 // Stream choreography shared by ag_gemm and gemm_rs. `launch` enqueues the consumer kernel on
 // ctx->ks, `put_all` the producer's copies and flags on the copy streams.
@@ -381,21 +367,24 @@ int schedule(agg_ctx* ctx, int mode, hipStream_t s, hipStream_t us,
     HIP_TRY(hipEventRecord(ctx->ev_kernel, ks));
     HIP_TRY(hipStreamWaitEvent(s, ctx->ev_kernel, 0));
   }
+  if (hipEvent_t e = order_event(ctx)) HIP_TRY(hipEventRecord(e, s));
   return AGG_OK;
 }
 
 // Enqueue the consumer kernel: launch(t0, t1) with the ring's next timing event pair when timing
 // is on and this launch is one of the sampled ones (the launch itself records the kernel's start
-// and end in them: no marker packets on the stream), or with null events.
+// and end in them: no marker packets on the stream), or with the event of the call's order alone.
 template <typename F>
 int timed_launch(agg_ctx* ctx, F launch) {
-  if (!ctx->timing_every || ctx->calls++ % uint64_t(ctx->timing_every) != 0) {
-    HIP_TRY(launch(nullptr, nullptr));
+  // (a launch under capture is not timed: its events would be the graph's)
+  if (!ctx->timing_every || !ctx->eager || ctx->calls++ % uint64_t(ctx->timing_every) != 0) {
+    HIP_TRY(launch(nullptr, order_event(ctx)));
     return AGG_OK;
   }
   const int slot = int(ctx->launches % kTimingRing);
   HIP_TRY(launch(ctx->ev_t0[slot], ctx->ev_t1[slot]));
   ++ctx->launches;
+  ctx->order_event = ctx->ev_t1[slot];
   return AGG_OK;
 }
 
@@ -637,7 +626,7 @@ int launch_cu(agg_ctx* ctx, hipStream_t ls, const GemmArgs& g, TileShape ts, int
     return launch_gemm(*tail.g, tail.ts.bm, tail.ts.bn, dtype, epi, tail.grid, ls, nullptr, t1);
   };
   if (timed) return timed_launch(ctx, go);
-  HIP_TRY(go(nullptr, nullptr));
+  HIP_TRY(go(nullptr, order_event(ctx)));
   return AGG_OK;
 }
 

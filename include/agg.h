@@ -41,10 +41,9 @@
  *    respect to the host, except that a non-NULL delay_us makes the calling thread wait between
  *    chunk enqueues (a test device: it emulates late peers).
  *  - A ctx serialises its calls: use one ctx from one host thread with one main stream.
- *    (A call of the collectives on another stream than the last one's starts after it; the first such
- *    change after many calls on one stream waits for the device on the host. A call under capture runs
- *    when its graph is replayed; the caller orders replays and the ctx's other calls. A replay of a
- *    collective reads the row and arrival order that the ctx's last eager call left, so capture it
+ *    (A call of the collectives on another stream than the last one's starts after it. A call under
+ *    capture runs when its graph is replayed; the caller orders replays and the ctx's other calls. A
+ *    replay of a collective reads the row and arrival order that the ctx's last eager call left, so capture it
  *    after an eager call of the same arguments and replay it before one of others.)
  *  - Matrix layouts are row-major: A and the gather buffer M x K (K contiguous), the weight B
  *    K x N (N contiguous), C M x N. The kernel turns B's rows into K-packed MFMA fragments with

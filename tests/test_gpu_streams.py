@@ -138,6 +138,69 @@ def test_calls_that_take_turns_between_streams(gpu):
         B.agg_ctx_destroy(ctx)
 
 
+def test_calls_beside_a_capture_in_progress(gpu):
+    """While a stream is being captured, work of others: many calls on one stream, then one on another,
+    which waits for them; the capture goes on."""
+    g = torch.Generator().manual_seed(4)
+    a = [torch.randn(M, K, generator=g).bfloat16().cuda() for _ in range(2)]
+    b = torch.randn(K, N, generator=g).bfloat16().cuda()
+    ctx = B.agg_ctx_create(0)
+    try:
+        want = [torch.zeros(M, N, dtype=torch.bfloat16, device="cuda") for _ in a]
+        for x, c in zip(a, want):
+            _gemm(ctx, x, b, c, torch.cuda.current_stream())
+        got, count = [torch.zeros_like(c) for c in want], torch.zeros(1, device="cuda")
+        captured, first, second = (torch.cuda.Stream() for _ in range(3))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(captured):
+            graph.capture_begin()
+            count.add_(1)
+            for _ in range(30):
+                _gemm(ctx, a[0], b, got[0], first)
+            _gemm(ctx, a[1], b, got[1], second)
+            count.add_(1)
+            graph.capture_end()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        for i in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert count.item() == 2 * (i + 1)
+        assert B.agg_ctx_status(ctx, torch.cuda.current_stream()) == (0, -1)
+    finally:
+        B.agg_ctx_destroy(ctx)
+
+
+@pytest.mark.parametrize("producer", ["cu", "kernel", "sdma"])
+@pytest.mark.parametrize("timing", [0, 1])
+def test_the_order_of_calls_with_every_producer(gpu, producer, timing):
+    """Gathers of two ranks on changing streams, with and without timing events: every result is whole."""
+    from allgather_gemm_persistent_amd.workload import AgWorkload
+    g = torch.Generator().manual_seed(5)
+    shards = [torch.randn(128, 256, generator=g).bfloat16() for _ in range(2)]
+    b = torch.randn(256, 256, generator=g).bfloat16()
+    w = AgWorkload(2, 0, shards, b, 64, producer=producer)
+    try:
+        B.agg_ctx_set_timing(w.ctx, timing)
+        w.run("overlap")
+        torch.cuda.synchronize()
+        want = w.c.clone()
+        ref = torch.cat(shards).double() @ b.double()
+        assert ((want.double().cpu() - ref).abs() <= ref.abs() * 2.0 ** -8 + 256 * 2.0 ** -23 * 16 * 256).all()
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        for i in range(24):
+            s = streams[i * i % 3]
+            w.run(("overlap", "serial", "gemm_only")[i % 3], stream=s)
+            if i % 8 == 7:
+                torch.cuda.synchronize()
+                assert torch.equal(w.c, want) and w.status() == (0, -1)
+                w.c.zero_()
+                torch.cuda.synchronize()
+    finally:
+        w.close()
+
+
 # ------------------------------------------------------------------------------ a split K
 
 class _Split:
