@@ -37,6 +37,15 @@ _c_int, _c_i64, _c_u32, _c_u64, _c_f32 = (ctypes.c_int, ctypes.c_int64, ctypes.c
 _vp, _sz = ctypes.c_void_p, ctypes.c_size_t
 _i32p, _u32p = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_uint32)
 
+
+
+class _CacheStruct(ctypes.Structure):
+    """agg_kv_cache."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("pages", _c_i64), ("ld_page", _c_i64),
+                ("ld_token", _c_i64), ("ld_head", _c_i64), ("dtype", _c_int), ("page_size", _c_int),
+                ("kv_heads", _c_int), ("head_dim", _c_int)]
+
+
 _SIGNATURES = {
     "agg_ctx_create": [_c_int, ctypes.POINTER(_vp)],
     "agg_ctx_destroy": [_vp],
@@ -96,6 +105,16 @@ _SIGNATURES = {
     "moe_gemm": [_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_int, _c_i64, _vp, _c_i64, _vp, _vp, _vp,
                  _vp, _vp, _vp, _vp],
     "moe_combine": [_vp, _c_i64, _c_int, _c_i64, _c_i64, _vp, _vp, _vp, _c_int, _vp, _vp],
+    "kv_write": [_vp, _vp, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_int,
+                 _c_int, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp],
+    "kv_read": [_vp, _vp, _c_i64, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp],
+    "paged_attn": [_vp, _vp, _c_i64, _c_int, _vp, _c_i64, _c_f32, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64,
+                   _c_int, _vp, _c_i64, _vp, _vp],
+    "agg_check_kv_write_args": [_vp, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64,
+                                _c_int, _c_int, _vp, _vp, _c_i64, _c_i64, _c_i64],
+    "agg_check_kv_read_args": [_vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64],
+    "agg_check_paged_attn_args": [_vp, _c_i64, _c_int, _vp, _c_i64, _c_f32, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64,
+                                  _c_int, _vp, _c_i64],
     "agg_check_norm_args": [_c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_f32,
                             _c_int, _vp, _c_i64, _vp, _c_f32],
     "agg_check_route_args": [_c_i64, _c_int, _c_int, _c_int, _vp, _c_i64, _c_int, _c_int, _c_int, _c_f32,
@@ -687,3 +706,117 @@ def agg_moe_gemm_shape(dtype, slots: int, n_experts: int, n: int, k: int, gated:
     _call("agg_moe_gemm_shape", _dtype(dtype), slots, n_experts, n, k, int(gated), ctypes.byref(parts),
           ctypes.byref(bm), ctypes.byref(bn))
     return ("stream", parts.value) if parts.value else ("tiles", (bm.value, bn.value))
+
+
+# ------------------------------------------------------------------------------ attention over a paged cache
+
+class KvCache:
+    """A paged cache of keys and values, for kv_write, kv_read and paged_attn: made once and kept as long as its
+    tensors are used.
+
+    k, v: pages x page_size x kv_heads x head_dim, bfloat16 or float8_e4m3fn, of equal strides with contiguous
+    channels (a permuted view of a tensor whose heads come first will do). With 8 bits k_scale and v_scale:
+    float32, pages x kv_heads x page_size, contiguous.
+    """
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        dt = _tensor_dtype(k, "k")
+        if dt == AGG_FP32 or v.dtype is not k.dtype:
+            raise AggError(AGG_E_ARG, "KvCache", f"k and v are {k.dtype} and {v.dtype}, not both bf16 or fp8")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise AggError(AGG_E_ARG, "KvCache", f"k and v have shapes {tuple(k.shape)} and {tuple(v.shape)}, not equal "
+                                                 "ones of four dimensions")
+        pages, page_size, heads, dim = k.shape
+        one = [n != 1 for n in k.shape]                  # (a dimension of one element may carry any stride)
+        sk, sv = k.stride(), v.stride()
+        if [s for s, o in zip(sk, one) if o] != [s for s, o in zip(sv, one) if o] and pages:
+            raise AggError(AGG_E_ARG, "KvCache", f"k and v have different strides {sk} and {sv}")
+        if sk[3] != 1 and dim != 1 and pages:
+            raise AggError(AGG_E_ARG, "KvCache", "the channels of a head must be contiguous")
+        for x, what in ((k, "k"), (v, "v")):
+            if not x.is_cuda and x.numel():
+                raise AggError(AGG_E_ARG, what, f"must be a device tensor, got {x.device}")
+        if dt == AGG_FP8_E4M3:
+            for x, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if x is None or tuple(x.shape) != (pages, heads, page_size):
+                    raise AggError(AGG_E_ARG, what, f"must have shape {(pages, heads, page_size)}, has "
+                                                    f"{None if x is None else tuple(x.shape)}")
+        else:
+            k_scale = v_scale = None
+        ps = [_flat(x, pages * heads * page_size, what, torch.float32) for x, what in ((k_scale, "k_scale"), (v_scale, "v_scale"))]
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, dim
+        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), *ps, pages, *sk[:3], dt, page_size, heads, dim)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _table(table):
+    """(pointer, sequences, pages of each, elements from one row to the next) of a table of pages."""
+    if table.dtype is not torch.int32 or table.dim() != 2:
+        raise AggError(AGG_E_ARG, "table", f"is {table.dtype} of {table.dim()} dimensions, not int32 of two")
+    seqs, pages = table.shape
+    ld, step = table.stride()
+    if step != 1 and pages > 1:
+        raise AggError(AGG_E_ARG, "table", "must have contiguous rows")
+    if not table.is_cuda and seqs and pages:
+        raise AggError(AGG_E_ARG, "table", f"must be a device tensor, got {table.device}")
+    return table.data_ptr(), seqs, pages, ld if seqs > 1 else pages
+
+
+def _token_seq(token_seq, tokens, seqs, what):
+    if token_seq is None and tokens > seqs:
+        raise AggError(AGG_E_ARG, what, f"is needed for {tokens} tokens of {seqs} sequences")
+    return _flat(token_seq, tokens, what, torch.int32)
+
+
+def kv_write(ctx, cache, tokens: int, k, v, positions, table, *, token_seq=None, q=None, q_out=None, rope=None,
+             rope_pairs: bool = False, stream=None) -> None:
+    """The tokens' keys and values, rows of kv_heads * head_dim, into their places of the cache (in the
+    cache's type), and q_out = q; keys and queries rotated by `rope` (float32, a row of cosines and then sines
+    for each position) if there is one."""
+    cols, bf16 = cache.kv_heads * cache.head_dim, torch.bfloat16
+    pk, lk = _rows(k, tokens, cols, "k", bf16)
+    pv, lv = _rows(v, tokens, cols, "v", bf16)
+    heads, pq, lq, po, lo = 0, None, 0, None, 0
+    if q is not None:
+        heads = q.shape[-1] // cache.head_dim
+        pq, lq = _rows(q, tokens, heads * cache.head_dim, "q", bf16)
+        if q_out is None:
+            raise AggError(AGG_E_ARG, "q_out", "is needed with q")
+        po, lo = _rows(q_out, tokens, heads * cache.head_dim, "q_out", bf16)
+    rows, dim = 0, 0
+    if rope is not None:
+        if rope.dim() != 2:
+            raise AggError(AGG_E_ARG, "rope", f"has {rope.dim()} dimensions, not two")
+        rows, dim = rope.shape
+    pt, seqs, pages, lt = _table(table)
+    _call("kv_write", ctx, cache.ref, tokens, heads, pq, lq, po, lo, pk, lk, pv, lv,
+          _flat(rope, rows * dim, "rope", torch.float32), rows, dim, int(rope_pairs),
+          _flat(positions, tokens, "positions", torch.int32), _token_seq(token_seq, tokens, seqs, "token_seq"), pt, seqs,
+          pages, lt, _stream(stream))
+
+
+def kv_read(ctx, cache, tokens: int, positions, table, k_out, v_out, *, token_seq=None, stream=None) -> None:
+    """k_out, v_out = the tokens' rows of the cache, bfloat16 or float32; zeros where a token has no place."""
+    cols, dt = cache.kv_heads * cache.head_dim, _tensor_dtype(k_out, "k_out")
+    pk, lk = _rows(k_out, tokens, cols, "k_out")
+    pv, lv = _rows(v_out, tokens, cols, "v_out", k_out.dtype)
+    pt, seqs, pages, lt = _table(table)
+    _call("kv_read", ctx, cache.ref, tokens, _flat(positions, tokens, "positions", torch.int32),
+          _token_seq(token_seq, tokens, seqs, "token_seq"), pt, seqs, pages, lt, dt, pk, lk, pv, lv, _stream(stream))
+
+
+def paged_attn(ctx, cache, rows: int, q, lens, table, out, *, scale: float, row_seq=None, window: int = 0, lse=None,
+               stream=None) -> None:
+    """out = softmax(scale * q K^T) V over the first lens[r] tokens of each row's sequence (the last `window` of
+    them, if it is not 0), bfloat16 or float32; lse = the logarithms of the sums."""
+    cols = q.shape[-1]
+    heads = cols // cache.head_dim
+    if heads * cache.head_dim != cols:
+        raise AggError(AGG_E_ARG, "q", f"has {cols} columns, not whole heads of {cache.head_dim}")
+    pq, lq = _rows(q, rows, cols, "q", torch.bfloat16)
+    po, lo = _rows(out, rows, cols, "out")
+    pt, seqs, pages, lt = _table(table)
+    _call("paged_attn", ctx, cache.ref, rows, heads, pq, lq, scale, _flat(lens, rows, "lens", torch.int32),
+          _token_seq(row_seq, rows, seqs, "row_seq"), pt, seqs, pages, lt, window, _tensor_dtype(out, "out"), po, lo,
+          _flat(lse, rows * heads, "lse", torch.float32), _stream(stream))

@@ -1,0 +1,85 @@
+// The C entry points of the attention operators: checks, then one launch on the caller's stream.
+#include "attn.h"
+#include "plan.h"
+
+using namespace agg;
+
+namespace {
+
+#define HIP_TRY(expr)                                                                   \
+  do {                                                                                  \
+    hipError_t e_ = (expr);                                                             \
+    if (e_ != hipSuccess) return fail(AGG_E_HIP, "%s: %s", #expr, hipGetErrorString(e_)); \
+  } while (0)
+
+hipStream_t S(agg_stream s) { return reinterpret_cast<hipStream_t>(s); }
+
+int enter(const agg_ctx* ctx) {
+  if (!ctx) return fail(AGG_E_ARG, "ctx is NULL");
+  HIP_TRY(hipSetDevice(ctx_device(ctx)));
+  return AGG_OK;
+}
+
+// (a dimension of one element may come with any stride: none is taken)
+agg_kv_cache without_idle_strides(const agg_kv_cache& c) {
+  agg_kv_cache r = c;
+  if (r.pages == 1) r.ld_page = 0;
+  if (r.kv_heads == 1) r.ld_head = 0;
+  return r;
+}
+
+}  // namespace
+
+extern "C" int kv_write(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens, int q_heads, const void* q, int64_t ld_q,
+                        void* q_out, int64_t ld_q_out, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                        const float* rope, int64_t rope_rows, int rope_dim, int rope_pairs, const int32_t* positions,
+                        const int32_t* token_seq, const int32_t* table, int64_t seqs, int64_t seq_pages,
+                        int64_t ld_table, agg_stream stream) {
+  if (int rc = agg_check_kv_write_args(cache, tokens, q_heads, q, ld_q, q_out, ld_q_out, k, ld_k, v, ld_v, rope, rope_rows,
+                                       rope_dim, rope_pairs, positions, table, seqs, seq_pages, ld_table))
+    return rc;
+  if (int rc = enter(ctx)) return rc;
+  // (no sequence, page or table: no token has a place)
+  if (tokens == 0 || seqs == 0 || seq_pages == 0 || cache->pages == 0) return AGG_OK;
+  const KvWriteArgs a{without_idle_strides(*cache), {positions, token_seq, table, seqs, seq_pages, ld_table},
+                      static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+                      static_cast<uint16_t*>(q_out), ld_q, ld_q_out, ld_k, ld_v, rope, tokens, rope_rows, q_heads,
+                      rope_dim, rope_pairs};
+  HIP_TRY(launch_kv_write(a, ctx_units(ctx), S(stream)));
+  return AGG_OK;
+}
+
+extern "C" int kv_read(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens, const int32_t* positions,
+                       const int32_t* token_seq, const int32_t* table, int64_t seqs, int64_t seq_pages, int64_t ld_table,
+                       int out_dtype, void* k_out, int64_t ld_k, void* v_out, int64_t ld_v, agg_stream stream) {
+  if (int rc = agg_check_kv_read_args(cache, tokens, positions, table, seqs, seq_pages, ld_table, out_dtype, k_out, ld_k,
+                                      v_out, ld_v))
+    return rc;
+  if (int rc = enter(ctx)) return rc;
+  if (tokens == 0) return AGG_OK;
+  const KvReadArgs a{without_idle_strides(*cache), {positions, token_seq, table, seqs, seq_pages, ld_table}, k_out, v_out,
+                     ld_k, ld_v, tokens, out_dtype == AGG_FP32};
+  HIP_TRY(launch_kv_read(a, ctx_units(ctx), S(stream)));
+  return AGG_OK;
+}
+
+extern "C" int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows, int q_heads, const void* q, int64_t ld_q,
+                          float scale, const int32_t* lens, const int32_t* row_seq, const int32_t* table, int64_t seqs,
+                          int64_t seq_pages, int64_t ld_table, int64_t window, int out_dtype, void* out, int64_t ld_out,
+                          float* lse, agg_stream stream) {
+  if (int rc = agg_check_paged_attn_args(cache, rows, q_heads, q, ld_q, scale, lens, table, seqs, seq_pages, ld_table,
+                                         window, out_dtype, out, ld_out))
+    return rc;
+  if (int rc = enter(ctx)) return rc;
+  if (rows == 0) return AGG_OK;
+  const int group = q_heads / cache->kv_heads;
+  // as many of a head's queries at once as there are (a head's keys and values are read again for more), up to
+  // what the registers hold
+  const int most = cache->head_dim > 128 ? 2 : 4;
+  const int tiles = group <= 16 ? 1 : group <= 32 || most == 2 ? 2 : 4;
+  const AttnArgs a{without_idle_strides(*cache), static_cast<const uint16_t*>(q), out, lse, lens, row_seq, table, seqs,
+                   seq_pages, ld_table, rows, ld_q, ld_out, window, scale * 1.442695041f, q_heads, group, tiles,
+                   out_dtype == AGG_FP32};
+  HIP_TRY(launch_attn(a, S(stream)));
+  return AGG_OK;
+}

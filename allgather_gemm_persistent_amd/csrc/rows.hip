@@ -1,38 +1,11 @@
 // Operators on whole rows, bound by memory: the residual's addition with the RMS norm and its
 // 8-bit output (rms_norm, quant_rows), and the experts' weighted sum (moe_combine).
+#include "convert.h"
 #include "moe.h"
 
 namespace agg {
 
 namespace {
-
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-__device__ inline void widen(const u32x4& p, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __builtin_bit_cast(float, p[i] << 16);
-    v[2 * i + 1] = __builtin_bit_cast(float, p[i] & 0xFFFF0000u);
-  }
-}
-
-// eight floats as bfloat16, nearest even
-__device__ inline u32x4 narrow(const float (&v)[8]) {
-  u32x4 p;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * i], v[2 * i + 1]}, bf16x2));
-  return p;
-}
-
-// a float inside e4m3's range; a NaN stays one
-__device__ inline float clamp_e4m3(float v) { return v != v ? v : fminf(fmaxf(v, -448.0f), 448.0f); }
-
-constexpr float kNormal = 1.17549435e-38f;   // the least float of full precision, 2^-126
 
 template <int T, typename F>
 __device__ inline uint32_t block_reduce(uint32_t v, F op, uint32_t* lds) {
@@ -162,13 +135,7 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = clamp_e4m3(q[e]);
       }
-      u32x2 p;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
-        p[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], v, true);
-      }
-      *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.out) + row * a.ld_out + c * 8) = p;
+      *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.out) + row * a.ld_out + c * 8) = narrow_e4m3(q);
     }
   } else {
 #pragma unroll

@@ -74,7 +74,8 @@ enum agg_status {
 enum agg_dtype {
   AGG_BF16 = 0,           /* bfloat16 operands */
   AGG_FP8_E4M3 = 1,       /* OCP float8 E4M3 ("fn": max 448, no inf) operands, per-tensor scales */
-  AGG_FP32 = 2            /* float32: rows of rms_norm, quant_rows, moe_route and moe_combine only */
+  AGG_FP32 = 2            /* float32: rows of rms_norm, quant_rows, moe_route, moe_combine, kv_read and
+                             paged_attn only */
 };
 
 enum agg_mode {
@@ -96,6 +97,9 @@ enum agg_mode {
 #define AGG_MAX_TOP_K 16          /* experts a token takes */
 #define AGG_MAX_NORM_COLS 32768   /* columns of rms_norm and quant_rows */
 #define AGG_PLAN_PAIRS 1024       /* (token, choice) pairs a block of moe_plan sorts */
+#define AGG_MAX_HEADS 1024        /* heads of queries of one call, and heads of a cache */
+#define AGG_MAX_HEAD_DIM 256      /* width of a head of a cache */
+#define AGG_MAX_PAGE 4096         /* tokens of a page of a cache */
 
 /* ---- context -------------------------------------------------------------------------- */
 
@@ -642,6 +646,100 @@ int moe_combine(agg_ctx* ctx, int64_t tokens, int top_k, int64_t n, int64_t slot
                 const int32_t* token_slot, const float* weights, int out_dtype, void* out,
                 agg_stream stream);
 
+/* ---- A decode step's attention: a paged cache and the attention that reads it ---------------
+ *
+ * The attention half of a decoder layer around the collectives (the routed half stands above): the
+ * projection's rows are rotated and their keys and values written into a cache (kv_write), the new
+ * tokens attend to it (paged_attn), and its rows can be read back (kv_read). They are forward
+ * operators, like the others here.
+ *
+ * A cache holds `pages` pages of page_size tokens; a table gives each sequence its pages in order, so
+ * position p of sequence s lies in page table[s * ld_table + p / page_size] at p % page_size. What
+ * a table holds past a sequence's pages is never looked at; a page number outside [0, pages) is no
+ * page: its positions cannot be written, read as zeros, and are left out of the attention. Sequences
+ * may share pages (a common prefix).
+ *
+ * Every call launches one kernel on `stream` and is capturable. Of the ctx they use its device and,
+ * in paged_attn, a workspace of the stream or capture (as moe_gemm's: nothing else is allocated, calls on several
+ * streams and graphs do not meet, two replays of one capture must not run at once). Device arrays are
+ * 16-byte aligned, the int32 and fp32 ones 4-byte aligned. No floating-point atomics.
+ * Passage: none (the pages give no attention; the formulas are the plain definitions stated here).
+ */
+
+/* A paged cache of keys and values. The struct is read during the call only; its arrays are the
+ * caller's.
+ *   k, v             pages x page_size x kv_heads x head_dim, AGG_BF16 or AGG_FP8_E4M3, both with the
+ *                    strides ld_page, ld_token and ld_head in elements (multiples of 16 bytes; the
+ *                    elements of a head are contiguous), so tokens or heads may come first
+ *   k_scale, v_scale fp8: fp32, pages x kv_heads x page_size contiguous: a row's elements stand for
+ *                    themselves times its scale. Ignored for bf16
+ *   page_size        a multiple of 16, at most AGG_MAX_PAGE
+ *   head_dim         a multiple of 16, at most AGG_MAX_HEAD_DIM
+ */
+typedef struct agg_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;
+  int64_t ld_page, ld_token, ld_head;
+  int dtype, page_size, kv_heads, head_dim;
+} agg_kv_cache;
+
+/* Rotates the new tokens' queries and keys and writes their keys and values into the cache.
+ *   tokens           token t belongs to sequence token_seq[t] (NULL: t) at position positions[t]
+ *   q, q_out         bf16 rows of q_heads * head_dim (strides ld_q, ld_q_out, elements): q_out is the
+ *                    rotated q. NULL with q_heads 0. q_out may be q at the same stride
+ *   k, v             bf16 rows of kv_heads * head_dim (strides ld_k, ld_v)
+ *   rope             fp32, rope_rows x rope_dim: row p holds the cosines and then the sines of
+ *                    position p's rope_dim / 2 angles. NULL (rope_rows, rope_dim 0): no rotation. The first
+ *                    rope_dim channels of a head turn, channel i with i + rope_dim / 2 (rope_pairs 0)
+ *                    or 2i with 2i + 1 (rope_pairs 1), by angle i:
+ *                    (a, b) -> (a cos - b sin, b cos + a sin). rope_dim: a multiple of 16, at most
+ *                    head_dim
+ *   table            int32, seqs rows of seq_pages pages, ld_table elements apart
+ * The cache gets bf16 of the fp32 results, or e4m3 of them over the scale max|row| / 448 of the
+ * token's head (1 for a row whose quotient is zero or that holds a NaN), as rms_norm's. A token whose
+ * sequence is outside [0, seqs), or whose position is outside [0, seq_pages * page_size) or, with rope,
+ * [0, rope_rows), or has no page, is left out: neither the cache nor its row of q_out is written. Two
+ * tokens of one call must not have the same place: the place then holds a mixture of both.
+ */
+int kv_write(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens, int q_heads, const void* q,
+             int64_t ld_q, void* q_out, int64_t ld_q_out, const void* k, int64_t ld_k, const void* v,
+             int64_t ld_v, const float* rope, int64_t rope_rows, int rope_dim, int rope_pairs,
+             const int32_t* positions, const int32_t* token_seq, const int32_t* table, int64_t seqs,
+             int64_t seq_pages, int64_t ld_table, agg_stream stream);
+
+/* Rows of the cache: k_out[t], v_out[t] = the keys and values of token_seq[t] (NULL: t) at
+ * positions[t], AGG_BF16 (rounded once) or AGG_FP32, rows of kv_heads * head_dim. A token without a
+ * place (see kv_write) reads as zeros. Tokens may repeat.
+ */
+int kv_read(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens, const int32_t* positions,
+            const int32_t* token_seq, const int32_t* table, int64_t seqs, int64_t seq_pages,
+            int64_t ld_table, int out_dtype, void* k_out, int64_t ld_k, void* v_out, int64_t ld_v,
+            agg_stream stream);
+
+/* Attention of `rows` new tokens over the cache. Row r reads sequence row_seq[r] (NULL: r) up to
+ * lens[r] tokens (at most seq_pages * page_size; its own token included, if kv_write has put it there);
+ * query head i reads cache head i / (q_heads / kv_heads):
+ *   x_i = scale * sum_d q_d k_id,  out = sum_i softmax(x)_i v_i,  lse = log sum_i exp(x_i)
+ * over positions i in [max(0, lens[r] - window), lens[r]) that have a page (window 0: all). A row
+ * without any (lens[r] <= 0, or a sequence outside [0, seqs)) gets zeros, and -inf in lse.
+ *   q                bf16 rows of q_heads * head_dim; q_heads a multiple of kv_heads
+ *   out, out_dtype   AGG_BF16 or AGG_FP32 rows of q_heads * head_dim
+ *   lse              fp32 [rows, q_heads] or NULL: with it, parts of a sequence that lie on several
+ *                    ranks can be joined
+ * Sums, maxima and the weights' products are fp32 (the weights enter the matrix units as two bf16
+ * parts each, 16 bits of fraction). The length is split over workgroups and the parts are joined in
+ * their order, so a result does not depend on timing; it may depend, in its last bits, on the other
+ * rows' lengths, by which the work is divided.
+ */
+int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows, int q_heads, const void* q,
+               int64_t ld_q, float scale, const int32_t* lens, const int32_t* row_seq,
+               const int32_t* table, int64_t seqs, int64_t seq_pages, int64_t ld_table,
+               int64_t window, int out_dtype, void* out, int64_t ld_out, float* lse,
+               agg_stream stream);
+
 /* ---- host-only planning (no device needed; used by the calls above) --------------------- */
 
 /* The tile shape the library uses for a call: *bm x *bn output tiles.
@@ -743,6 +841,21 @@ int agg_check_combine_args(int64_t tokens, int top_k, int64_t n, int64_t slots, 
                            const int32_t* token_slot, const float* weights, int out_dtype,
                            const void* out);
 
+/* The argument checks of kv_write, kv_read and paged_attn, run by them first.
+ */
+int agg_check_kv_write_args(const agg_kv_cache* cache, int64_t tokens, int q_heads, const void* q,
+                            int64_t ld_q, const void* q_out, int64_t ld_q_out, const void* k,
+                            int64_t ld_k, const void* v, int64_t ld_v, const float* rope,
+                            int64_t rope_rows, int rope_dim, int rope_pairs, const int32_t* positions,
+                            const int32_t* table, int64_t seqs, int64_t seq_pages, int64_t ld_table);
+int agg_check_kv_read_args(const agg_kv_cache* cache, int64_t tokens, const int32_t* positions,
+                           const int32_t* table, int64_t seqs, int64_t seq_pages, int64_t ld_table,
+                           int out_dtype, const void* k_out, int64_t ld_k, const void* v_out,
+                           int64_t ld_v);
+int agg_check_paged_attn_args(const agg_kv_cache* cache, int64_t rows, int q_heads, const void* q,
+                              int64_t ld_q, float scale, const int32_t* lens, const int32_t* table,
+                              int64_t seqs, int64_t seq_pages, int64_t ld_table, int64_t window,
+                              int out_dtype, const void* out, int64_t ld_out);
 /* How moe_gemm multiplies a call on a whole MI355X: *ksplit > 0: the weights streamed through
  * registers, K in that many parts (then *bm = *bn = 0); *ksplit 0: tiles of *bm x *bn. Sizes that
  * moe_gemm refuses are refused; sizes without work still name a kernel.
