@@ -29,6 +29,7 @@ MODES = {"overlap": AGG_OVERLAP, "serial": AGG_SERIAL, "gemm_only": AGG_GEMM_ONL
          "copy_only": AGG_COPY_ONLY}
 DTYPES = {"bf16": AGG_BF16, "fp8": AGG_FP8_E4M3, "fp32": AGG_FP32}
 SCORES = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 PLAN_PAIRS = 1024
 MAX_ROW_TILES = 1024
 
@@ -110,6 +111,12 @@ _SIGNATURES = {
     "kv_read": [_vp, _vp, _c_i64, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp],
     "paged_attn": [_vp, _vp, _c_i64, _c_int, _vp, _c_i64, _c_f32, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64,
                    _c_int, _vp, _c_i64, _vp, _vp],
+    "linear": [_vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _vp, _vp, _vp, _c_int, _c_int, _vp, _c_i64, _c_int,
+               _vp, _c_i64, _vp],
+    "agg_check_linear_args": [_c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _vp, _vp, _vp, _c_int, _c_int, _vp,
+                              _c_i64, _c_int, _vp, _c_i64],
+    "agg_linear_shape": [_c_int, _c_i64, _c_i64, _c_i64, ctypes.POINTER(_c_int), ctypes.POINTER(_c_int),
+                         ctypes.POINTER(_c_int)],
     "agg_check_kv_write_args": [_vp, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64,
                                 _c_int, _c_int, _vp, _vp, _c_i64, _c_i64, _c_i64],
     "agg_check_kv_read_args": [_vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64],
@@ -820,3 +827,28 @@ def paged_attn(ctx, cache, rows: int, q, lens, table, out, *, scale: float, row_
     _call("paged_attn", ctx, cache.ref, rows, heads, pq, lq, scale, _flat(lens, rows, "lens", torch.int32),
           _token_seq(row_seq, rows, seqs, "row_seq"), pt, seqs, pages, lt, window, _tensor_dtype(out, "out"), po, lo,
           _flat(lse, rows * heads, "lse", torch.float32), _stream(stream))
+
+
+# ------------------------------------------------------------------------------ products with an epilogue
+
+def linear(ctx, m: int, n: int, k: int, dtype, a, b, out, *, a_scale=None, b_scale=None, bias=None, act="none",
+           residual=None, stream=None) -> None:
+    """out = act(A @ B + bias) + residual, bfloat16 or float32; act: "none", "relu", "silu", "gelu" or "gelu_tanh".
+    fp8 operands take a scale for each row of A and each column of B."""
+    dt = _dtype(dtype)
+    el = torch.float8_e4m3fn if dt == AGG_FP8_E4M3 else torch.bfloat16
+    pa, la = _rows(a, m, k, "a", el)
+    pr, lr = _rows(residual, m, n, "residual")
+    po, lo = _rows(out, m, n, "out")
+    _call("linear", ctx, m, n, k, dt, pa, la, _flat(a_scale, m, "a_scale", torch.float32), _flat(b, k * n, "b", el),
+          _flat(b_scale, n, "b_scale", torch.float32), _flat(bias, n, "bias", torch.bfloat16),
+          ACTIVATIONS[act] if isinstance(act, str) else int(act),
+          AGG_BF16 if residual is None else _tensor_dtype(residual, "residual"), pr, lr, _tensor_dtype(out, "out"), po, lo,
+          _stream(stream))
+
+
+def agg_linear_shape(dtype, m: int, n: int, k: int):
+    """How linear multiplies: ("stream", parts of K) or ("tiles", (bm, bn))."""
+    parts, bm, bn = _c_int(), _c_int(), _c_int()
+    _call("agg_linear_shape", _dtype(dtype), m, n, k, ctypes.byref(parts), ctypes.byref(bm), ctypes.byref(bn))
+    return ("stream", parts.value) if parts.value else ("tiles", (bm.value, bn.value))

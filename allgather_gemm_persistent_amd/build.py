@@ -22,11 +22,11 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libagg.so")
 ARCH = "gfx950"
 
-SOURCES = ["plan.cpp", "moe.cpp", "attn.cpp", "host.hip", "moe_host.hip", "attn_host.hip", "kernels.hip", "experts.hip",
-           "attn.hip", "rows.hip", "route.hip", "kv.hip"]
-# sources with GEMM kernel instantiations, whose accumulators are checked; kernels.resources.txt and
-# experts.resources.txt in _build hold the compiler's remarks
-GEMM_SOURCES = ("kernels.hip", "experts.hip")
+SOURCES = ["plan.cpp", "moe.cpp", "attn.cpp", "linear.cpp", "host.hip", "moe_host.hip", "attn_host.hip", "linear_host.hip",
+           "kernels.hip", "experts.hip", "linear.hip", "attn.hip", "rows.hip", "route.hip", "kv.hip"]
+# sources with GEMM kernel instantiations, whose accumulators are checked; *.resources.txt in _build
+# hold the compiler's remarks
+GEMM_SOURCES = ("kernels.hip", "experts.hip", "linear.hip")
 
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -2,284 +2,11 @@
 // e = 0 .. n_experts - 1, with the slots of one expert side by side.
 //
 // Two kernels. Many rows an expert: the persistent MFMA kernel of gemm_kernel.h over the tiles of
-// all experts (kEpiExperts), bound by the matrix units. Few rows an expert: expert_stream_kernel
-// below, bound by reading every weight once.
-#include "gemm_kernel.h"
-#include "moe.h"
+// all experts (kEpiExperts), bound by the matrix units. Few rows an expert: the streaming
+// kernel of stream_kernel.h, bound by reading every weight once.
+#include "stream_kernel.h"
 
 namespace agg {
-
-typedef long i64x1;
-
-__device__ inline f32x4 mfma16(const u32x4& b, const u32x4& a, const f32x4& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c,
-                                                 0, 0, 0);
-}
-__device__ inline f32x4 mfma16(const u32x2& b, const u32x2& a, const f32x4& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(__builtin_bit_cast(i64x1, b), __builtin_bit_cast(i64x1, a), c,
-                                                    0, 0, 0);
-}
-
-// Few rows an expert: a workgroup of 8 waves holds a strip of one expert's output columns (128 bf16
-// or 256 fp8) and a part of K (all of it, or one of ksplit parts), the waves taking blocks of 32 K
-// rows in turn (gated: four waves the gate columns, four the up columns); rows are taken 32 at a time
-// (B is read again for more).
-//
-// B goes from memory to registers, without LDS: lane l loads 16 bytes (CW columns) of each of the 8
-// K rows 8 * (l / 16) .. + 7 of a block at column chunk l % 16, so one instruction reads 256 bytes in
-// a row from 4 rows. The MFMA wants 8 consecutive K of one column in a lane; those are the 8 loaded
-// rows at a fixed column of the lane's chunk, so the transposition stays inside the lane: byte
-// permutes (32 for 8 KiB of bf16, 64 of fp8, far below what the memory leaves time for). Fragment c
-// of the wave then holds column c of every lane's chunk, i.e. MFMA c computes columns chunk * CW + c.
-//
-// Bound by reading B. A kernel that only reads reached 6.9 TB/s from all compute units and 55 GB/s
-// from one; strided pieces of rows came to about 160 pieces a microsecond and compute unit whatever
-// their size (256, 128 or 64 bytes), so the pieces are as long as a wave's tile allows (strips of 128
-// or 64 bytes measured 20% and 130% slower at 8 experts of 8192 x 7168 bf16), the gate and the up
-// columns go to different waves rather than side by side (185 -> 155 us there), and where the strips
-// of the busy experts are fewer than the compute units K is split over workgroups.
-//
-// Sums: a wave adds its blocks in K order, the waves' sums meet in LDS in wave order, and the parts of
-// a split K (fp32, written through to the workspace) are added in part order by the workgroup that
-// finishes a strip last, so nothing depends on timing. The fp8 matrix instruction cuts each of 8
-// products of consecutive K to multiples of 2^-13 of the largest of them before it adds them; what it
-// adds to its accumulator, and every sum here, is fp32.
-constexpr int kStreamWaves = 8;
-
-template <bool FP8, bool GATED>
-__global__ void __launch_bounds__(kStreamWaves * 64) expert_stream_kernel(const StreamArgs a) {
-  constexpr int RB = 2;                      // 16-row blocks at a time
-  constexpr int EL = FP8 ? 1 : 2;
-  constexpr int CW = 16 / EL;                // columns a lane loads
-  constexpr int SC = 16 * CW;                // columns of a strip
-  constexpr int PW = 8;                      // columns of a lane summed in one pass over LDS
-  constexpr int HC = 16 * PW, PC = HC + 4;   // columns of a pass, padded
-  // blocks in the ring: one in use, the others on their way, as the registers allow
-  constexpr int D = FP8 ? 2 : 3;
-  constexpr int KW = GATED ? kStreamWaves / 2 : kStreamWaves;   // waves that share K
-  using Frag = std::conditional_t<FP8, u32x2, u32x4>;
-  __shared__ __attribute__((aligned(16))) float part[kStreamWaves][16][PC];
-  __shared__ int s_last;
-
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int g = lane & 15, kq = lane >> 4;
-  const int expert = blockIdx.y, ksplit = a.ksplit;
-  const int strip = (int)blockIdx.x / ksplit, kpart = (int)blockIdx.x % ksplit;
-  const int lo = __builtin_amdgcn_readfirstlane((int)expert_bound(a.x, expert));
-  const int end = __builtin_amdgcn_readfirstlane((int)expert_bound(a.x, expert + 1));
-  if (lo >= end) return;
-  const int N = (int)a.N, K = (int)a.K, NO = GATED ? N / 2 : N;
-  const int kw = wave % KW;
-  // this lane's chunk of B's columns
-  const int col = strip * SC + g * CW;
-  const uint32_t row_bytes = (uint32_t)N * EL;
-  const uint32_t b0 = col < NO ? (uint32_t)(col + wave / KW * NO) * EL : kOutOfRange;
-  const __amdgpu_buffer_rsrc_t db = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(a.b) + (int64_t)expert * N * K * EL, 0, (int)((int64_t)N * K * EL), kBufferFlags);
-  // this part's blocks of 32 K rows
-  const int all = (K + 31) / 32, per = (all + ksplit - 1) / ksplit;
-  const int first = kpart * per, blocks = first + per < all ? first + per : all;
-  const __amdgpu_buffer_rsrc_t dw = __builtin_amdgcn_make_buffer_rsrc(a.ws, 0, (int)a.ws_bytes, kBufferFlags);
-
-  // one quad of output columns n .. n + 3 of slot s, from its sums
-  auto finish = [&](int64_t s, int n, f32x4 v, f32x4 up) {
-    if constexpr (FP8) {
-      const int64_t ar = a.x.slot_token ? (int64_t)a.x.slot_token[s] : s;
-      const float rs = (ar >= 0 && ar < a.x.a_rows) ? a.x.a_scale[ar] : 0.0f;
-      const float* const bs = a.x.b_scale + (int64_t)expert * N + n;
-      v *= *reinterpret_cast<const f32x4*>(bs) * rs;
-      if constexpr (GATED) up *= *reinterpret_cast<const f32x4*>(bs + NO) * rs;
-    }
-    if constexpr (GATED) v = f32x4{silu(v[0]) * up[0], silu(v[1]) * up[1], silu(v[2]) * up[2], silu(v[3]) * up[3]};
-    u32x2 packed;
-    packed[0] = bf16x2_rne(v[0], v[1]);
-    packed[1] = bf16x2_rne(v[2], v[3]);
-    *reinterpret_cast<u32x2*>(a.c + s * NO + n) = packed;
-  };
-
-  for (int r0 = lo; r0 < end; r0 += 16 * RB) {
-    const int held = end - r0 < 16 * RB ? end - r0 : 16 * RB;
-    const int64_t rows = a.x.slot_token ? a.x.a_rows : (int64_t)held;
-    const __amdgpu_buffer_rsrc_t da = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(a.a) + (a.x.slot_token ? 0 : (int64_t)r0 * a.x.a_stride), 0,
-        (int)((rows - 1) * a.x.a_stride + (int64_t)K * EL), kBufferFlags);
-
-    f32x4 acc[CW][RB];
-#pragma unroll
-    for (int c = 0; c < CW; ++c)
-#pragma unroll
-      for (int r = 0; r < RB; ++r) acc[c][r] = f32x4{};
-
-    struct Block {
-      u32x4 b[8];
-      Frag a[RB];
-    };
-    Block x[D];
-    uint32_t a0[RB];
-    // block kb of 32 K rows; past the end of the part or of K every lane's offset is out of range
-    // (reads zeros):
-    // K is a multiple of 8, so a lane's 8 rows lie inside K or outside it together
-    auto load_b = [&](Block& y, int kb) {
-      const int k0 = kb * 32 + kq * 8;
-      const uint32_t out = kb < blocks && k0 < K ? 0u : kOutOfRange;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int off = (int)((b0 + (uint32_t)(k0 + i) * row_bytes) | out | (b0 & kOutOfRange));
-        // (non-temporal: every byte of B is used once)
-        y.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(db, off, 0, 2));
-      }
-    };
-    auto load_a = [&](Block& y, int kb) {
-      const int k0 = kb * 32 + kq * 8;
-      const uint32_t out = kb < blocks && k0 < K ? 0u : kOutOfRange;
-#pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        const int off = (int)((a0[r] + (uint32_t)k0 * EL) | out | (a0[r] & kOutOfRange));
-        if constexpr (FP8) y.a[r] = __builtin_bit_cast(Frag, __builtin_amdgcn_raw_buffer_load_b64(da, off, 0, 0));
-        else y.a[r] = __builtin_bit_cast(Frag, __builtin_amdgcn_raw_buffer_load_b128(da, off, 0, 0));
-      }
-    };
-    auto compute = [&](const Block& y) {
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        uint32_t q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = y.b[i][d];
-        if constexpr (!FP8) {
-          // dword d holds columns 2d (low half) and 2d + 1
-          u32x4 f0, f1;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            f0[p] = __builtin_amdgcn_perm(q[2 * p + 1], q[2 * p], 0x05040100u);
-            f1[p] = __builtin_amdgcn_perm(q[2 * p + 1], q[2 * p], 0x07060302u);
-          }
-#pragma unroll
-          for (int r = 0; r < RB; ++r) {
-            acc[2 * d][r] = mfma16(f0, y.a[r], acc[2 * d][r]);
-            acc[2 * d + 1][r] = mfma16(f1, y.a[r], acc[2 * d + 1][r]);
-          }
-        } else {
-          // dword d holds columns 4d .. 4d + 3: a 4 x 4 byte transposition of rows 0..3 and of 4..7
-          u32x2 f[4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t* const e = q + 4 * h;
-            const uint32_t t0 = __builtin_amdgcn_perm(e[1], e[0], 0x05010400u), t1 = __builtin_amdgcn_perm(e[1], e[0], 0x07030602u);
-            const uint32_t u0 = __builtin_amdgcn_perm(e[3], e[2], 0x05010400u), u1 = __builtin_amdgcn_perm(e[3], e[2], 0x07030602u);
-            f[0][h] = __builtin_amdgcn_perm(u0, t0, 0x05040100u);
-            f[1][h] = __builtin_amdgcn_perm(u0, t0, 0x07060302u);
-            f[2][h] = __builtin_amdgcn_perm(u1, t1, 0x05040100u);
-            f[3][h] = __builtin_amdgcn_perm(u1, t1, 0x07060302u);
-          }
-#pragma unroll
-          for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[4 * d + c][r] = mfma16(f[c], y.a[r], acc[4 * d + c][r]);
-        }
-      }
-    };
-    // the first block of B is on its way before the rows of A are known; after that the loads keep
-    // the loop's order (block by block, B before A), which its waits count on
-    load_b(x[0], first + kw);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const int s = r0 + r * 16 + g;
-      a0[r] = kOutOfRange;
-      if (s < end) {
-        const int64_t ar = a.x.slot_token ? (int64_t)a.x.slot_token[s] : (int64_t)s - r0;
-        if (ar >= 0 && (!a.x.slot_token || ar < a.x.a_rows)) a0[r] = (uint32_t)ar * (uint32_t)a.x.a_stride;
-      }
-    }
-    load_a(x[0], first + kw);
-#pragma unroll
-    for (int u = 1; u + 1 < D; ++u) {
-      load_b(x[u], first + kw + u * KW);
-      load_a(x[u], first + kw + u * KW);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // (the scheduling barriers keep a block's loads ahead of the products before which they stand:
-    // the compiler otherwise moves them behind, and the loop waits for each block in turn)
-    __builtin_amdgcn_sched_barrier(0);
-    for (int kb = first + kw; kb < blocks; kb += D * KW) {
-#pragma unroll
-      for (int u = 0; u < D; ++u) {
-        load_b(x[(u + D - 1) % D], kb + (u + D - 1) * KW);
-        load_a(x[(u + D - 1) % D], kb + (u + D - 1) * KW);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(x[u]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-
-    // ---- the waves' partial sums, HC columns and 16 rows a pass: lane l holds, of row l % 16,
-    // columns (4 * (l / 16) + i) * CW + c
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      if (r * 16 >= held) break;
-#pragma unroll
-      for (int h = 0; h < CW / PW; ++h) {
-        // pass h takes columns h * PW .. + PW - 1 of every chunk
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int c = 0; c < PW; c += 2)
-            *reinterpret_cast<f32x2*>(&part[wave][g][(4 * kq + i) * PW + c]) =
-                f32x2{acc[h * PW + c][r][i], acc[h * PW + c + 1][r][i]};
-        __syncthreads();
-        // one column quad of one row a thread
-        const int row = tid / (HC / 4), c4 = tid % (HC / 4) * 4;
-        const int64_t s = (int64_t)r0 + r * 16 + row;
-        const int n = strip * SC + c4 / PW * CW + h * PW + c4 % PW;
-        if (s >= end || n >= NO) continue;
-        auto total = [&](int from) {
-          f32x4 v = *reinterpret_cast<const f32x4*>(&part[from][row][c4]);
-#pragma unroll
-          for (int w = 1; w < KW; ++w) v += *reinterpret_cast<const f32x4*>(&part[from + w][row][c4]);
-          return v;
-        };
-        f32x4 v = total(0), up = f32x4{};
-        if constexpr (GATED) up = total(KW);
-        if (ksplit == 1) {
-          finish(s, n, v, up);
-        } else {
-          const int64_t at = ((int64_t)kpart * a.x.slots + s) * N + n;
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), dw, (int)(at * 4), 0, kStoreSystemCoherent);
-          if constexpr (GATED)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, up), dw, (int)((at + NO) * 4), 0,
-                                                   kStoreSystemCoherent);
-        }
-      }
-    }
-    __syncthreads();
-  }
-  if (ksplit == 1) return;
-
-  // ---- a split K: the part that finishes last adds them all, in part order. Its loads bypass the
-  // caches, as the stores did, so no fence is needed; the count is left at zero for the next launch
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  uint32_t* const count = a.counts + (int)blockIdx.y * a.strips + strip;
-  if (tid == 0)
-    s_last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)ksplit - 1;
-  __syncthreads();
-  if (!__builtin_amdgcn_readfirstlane(s_last)) return;
-  for (int e = tid; e < (end - lo) * (SC / 4); e += kStreamWaves * 64) {
-    const int64_t s = (int64_t)lo + e / (SC / 4);
-    const int n = strip * SC + e % (SC / 4) * 4;
-    if (n >= NO) continue;
-    f32x4 v = f32x4{}, up = f32x4{};
-    for (int p = 0; p < ksplit; ++p) {
-      const int64_t at = ((int64_t)p * a.x.slots + s) * N + n;
-      v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(dw, (int)(at * 4), 0, kStoreSystemCoherent));
-      if constexpr (GATED)
-        up += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(dw, (int)((at + NO) * 4), 0, kStoreSystemCoherent));
-    }
-    finish(s, n, v, up);
-  }
-  if (tid == 0) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
 
 template <int BM, int BN, int DT>
 static hipError_t launch_tiles(const GemmArgs& args, int grid, hipStream_t stream) {
@@ -305,11 +32,11 @@ hipError_t launch_expert_tiles(const GemmArgs& args, int bm, int bn, int dtype, 
 hipError_t launch_expert_stream(const StreamArgs& args, int dtype, hipStream_t stream) {
   const dim3 grid((unsigned)(args.strips * args.ksplit), (unsigned)args.x.n_experts), block(kStreamWaves * 64);
   if (dtype == AGG_FP8_E4M3) {
-    if (args.x.gated) hipLaunchKernelGGL((expert_stream_kernel<true, true>), grid, block, 0, stream, args);
-    else hipLaunchKernelGGL((expert_stream_kernel<true, false>), grid, block, 0, stream, args);
+    if (args.x.gated) hipLaunchKernelGGL((expert_stream_kernel<true, true, false>), grid, block, 0, stream, args);
+    else hipLaunchKernelGGL((expert_stream_kernel<true, false, false>), grid, block, 0, stream, args);
   } else {
-    if (args.x.gated) hipLaunchKernelGGL((expert_stream_kernel<false, true>), grid, block, 0, stream, args);
-    else hipLaunchKernelGGL((expert_stream_kernel<false, false>), grid, block, 0, stream, args);
+    if (args.x.gated) hipLaunchKernelGGL((expert_stream_kernel<false, true, false>), grid, block, 0, stream, args);
+    else hipLaunchKernelGGL((expert_stream_kernel<false, false, false>), grid, block, 0, stream, args);
   }
   return hipGetLastError();
 }

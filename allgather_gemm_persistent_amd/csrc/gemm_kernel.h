@@ -29,7 +29,8 @@
 //       sum over ranks in ascending order to `out`; FFN chain -> SiLU and bf16 rows of h for
 //       the first layer's tiles (which release the second layer's rows), the ReduceScatter
 //       epilogue for the second layer's; experts' products -> bf16 rows of the slots, after the
-//       gate's SiLU where the product is gated
+//       gate's SiLU where the product is gated; a product with an epilogue -> bias, activation and
+//       residual on rows staged through LDS
 //   ReduceScatter and the FFN chain then reduce the local block over the whole grid
 //   the last workgroup to finish resets the counters for the next launch.
 // A workgroup waits only on chunk flags or on tiles claimed before its own (split-K parts of a
@@ -846,6 +847,19 @@ __device__ inline void expert_row_tiles(const ExpertArgs& x, int tid, int* first
   __syncthreads();
 }
 
+// The same for one expert of `rows` rows.
+template <int BM, bool LOW>
+__device__ inline void one_row_tiles(int64_t rows, int tid, int* first, int* low) {
+  if (tid == 0) {
+    const int rest = (int)(rows % BM);
+    const bool h = LOW && rest > 0 && rest <= BM / 2;
+    first[0] = low[0] = 0;
+    first[1] = (int)(rows / BM) + (rest > 0 && !h);
+    low[1] = h;
+  }
+  __syncthreads();
+}
+
 struct ExpertTile {
   int expert, row_tile, col_tile;
 };
@@ -1002,10 +1016,132 @@ __device__ inline void expert_epilogue(const GemmArgs& a, const f32x4 (&acc)[FM]
   }
 }
 
+// act(x); fp32 in and out. A NaN stays one.
+__device__ inline float activated(int act, float x) {
+  switch (act) {
+    case AGG_ACT_RELU: return x < 0.0f ? 0.0f : x;
+    case AGG_ACT_SILU: return silu(x);
+    case AGG_ACT_GELU: return 0.5f * x * (1.0f + erff(x * 0.707106781f));
+    // x (1 + tanh u) / 2 = x / (1 + e^-2u)
+    case AGG_ACT_GELU_TANH: return x / (1.0f + __expf(-1.59576912f * (x + 0.044715f * x * x * x)));
+    default: return x;
+  }
+}
+
+// V consecutive elements of a product's row m from column n on: scales are in v already.
+template <int V>
+struct LinearRow {
+  f32x4 r[V / 4];
+  // the residual's elements (all loads of several of these go out before the first is used)
+  __device__ inline void load(const LinearArgs& y, int64_t m, int64_t n) {
+    if (!y.residual) return;
+    if (y.residual_fp32) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i)
+        r[i] = reinterpret_cast<const f32x4*>(static_cast<const float*>(y.residual) + m * y.ld_residual + n)[i];
+    } else {
+      const uint16_t* const p = static_cast<const uint16_t*>(y.residual) + m * y.ld_residual + n;
+      if constexpr (V == 8) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+        r[0] = widen4(u32x2{w[0], w[1]});
+        r[1] = widen4(u32x2{w[2], w[3]});
+      } else {
+        r[0] = widen4(*reinterpret_cast<const u32x2*>(p));
+      }
+    }
+  }
+  static __device__ inline f32x4 widen4(const u32x2& w) {
+    return f32x4{__builtin_bit_cast(float, w[0] << 16), __builtin_bit_cast(float, w[0] & 0xFFFF0000u),
+                 __builtin_bit_cast(float, w[1] << 16), __builtin_bit_cast(float, w[1] & 0xFFFF0000u)};
+  }
+  __device__ inline void store(const LinearArgs& y, int64_t m, int64_t n, f32x4 (&v)[V / 4]) const {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      if (y.bias) v[i] += widen4(*reinterpret_cast<const u32x2*>(y.bias + n + 4 * i));
+      if (y.act != AGG_ACT_NONE) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = activated(y.act, v[i][e]);
+      }
+      if (y.residual) v[i] += r[i];
+    }
+    if (y.out_fp32) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i)
+        reinterpret_cast<f32x4*>(static_cast<float*>(y.out) + m * y.ld_out + n)[i] = v[i];
+    } else {
+      uint16_t* const p = static_cast<uint16_t*>(y.out) + m * y.ld_out + n;
+      if constexpr (V == 8)
+        *reinterpret_cast<u32x4*>(p) = u32x4{bf16x2_rne(v[0][0], v[0][1]), bf16x2_rne(v[0][2], v[0][3]),
+                                             bf16x2_rne(v[1][0], v[1][1]), bf16x2_rne(v[1][2], v[1][3])};
+      else
+        *reinterpret_cast<u32x2*>(p) = u32x2{bf16x2_rne(v[0][0], v[0][1]), bf16x2_rne(v[0][2], v[0][3])};
+    }
+  }
+};
+
+// Epilogue of a tile of a product with one: the accumulators go through LDS (the operand stages, free
+// after the K loop) in passes of RP rows, so that a thread then holds 8 columns of a row: whole lines
+// of the residual and of out, and the activations' code once instead of once an accumulator. The
+// quads of an LDS row are exchanged by the row's number, which keeps the 16 rows that a wave writes at
+// once on different banks. Ends with every thread past its LDS reads only after the tile's last barrier.
+template <int BM, int BN, bool FP8, int FM, int FN, int STAGE_BYTES, int ROWS, typename Row, typename Col>
+__device__ inline void linear_epilogue(const GemmArgs& a, const f32x4 (&acc)[FM][FN], uint8_t* stages, int first_row,
+                                       int blocks, int64_t lo, int64_t hi, int64_t n0, Row qrow, Col qcol) {
+  constexpr int RP0 = STAGE_BYTES / (BN * 4) / ROWS * ROWS, RP = RP0 < BM ? RP0 : BM;
+  static_assert(RP >= ROWS && RP * BN * 4 <= STAGE_BYTES, "LDS passes");
+  constexpr int Q = BN / 4, C = BN / 8, U = 2;
+  static_assert(Q % 8 == 0, "quads are exchanged within eights");
+  const int tid = threadIdx.x;
+  f32x4* const tl = reinterpret_cast<f32x4*>(stages);
+  auto place = [&](int r, int q) { return r * Q + (q ^ (r & 7)); };
+  for (int p0 = 0; p0 < BM && lo + p0 < hi; p0 += RP) {
+    __syncthreads();
+    if (first_row >= p0 && first_row < p0 + RP) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if (i >= blocks) break;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) tl[place(qrow(i) - p0, qcol(j) >> 2)] = acc[i][j];
+      }
+    }
+    __syncthreads();
+    const int rows = hi - lo - p0 < RP ? (int)(hi - lo - p0) : RP;
+    for (int e0 = tid; e0 < rows * C; e0 += kThreads * U) {
+      LinearRow<8> x[U];
+      int64_t m[U], n[U];
+      bool in[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * kThreads;
+        m[u] = lo + p0 + e / C;
+        n[u] = n0 + e % C * 8;
+        in[u] = e < rows * C && n[u] < a.N;
+        if (in[u]) x[u].load(a.y, m[u], n[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!in[u]) continue;
+        const int e = e0 + u * kThreads, r = e / C, q = e % C * 2;
+        f32x4 v[2] = {tl[place(r, q)], tl[place(r, q + 1)]};
+        if constexpr (FP8) {
+          const float rs = a.x.a_scale[m[u]];
+          const f32x4* const bs = reinterpret_cast<const f32x4*>(a.x.b_scale + n[u]);
+          v[0] *= bs[0] * rs;
+          v[1] *= bs[1] * rs;
+        }
+        x[u].store(a.y, m[u], n[u], v);
+      }
+    }
+  }
+}
+
 template <int BM, int BN, int DT, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
   constexpr int NW = kThreads / kWaveLanes, NT = kThreads;   // one wave per SIMD
   constexpr bool FP8 = (DT == AGG_FP8_E4M3);
+  // tiles dealt without counters; a product with an epilogue is one expert that holds every row
+  constexpr bool kGrouped = EPI == kEpiExperts || EPI == kEpiLinear;
+  constexpr int kMostExperts = EPI == kEpiExperts ? AGG_MAX_EXPERTS : 1;
   constexpr bool kSplitTiles = BM * BN <= 128 * 128;
   // 2 x 2 waves over 16x16x32 bf16 or 32x32x64 fp8 MFMA blocks (fp8: 4 x 1 when half the
   // tile's columns are not whole 32-column blocks)
@@ -1050,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
     int job;
     int acq;
     // experts: prefixes of whole and low row tiles
-    int first[EPI == kEpiExperts ? AGG_MAX_EXPERTS + 1 : 1], low[EPI == kEpiExperts ? AGG_MAX_EXPERTS + 1 : 1];
+    int first[kGrouped ? kMostExperts + 1 : 1], low[kGrouped ? kMostExperts + 1 : 1];
     int sums[EPI == kEpiExperts ? 8 : 1];
   };
   static_assert(kStageBytes <= kLdsDmaLimit, "direct-to-LDS destinations must stay below 128 KiB");
@@ -1073,23 +1209,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
   // the list searched first: the one that gives this workgroup its static first tile. The
   // workgroups of one list share an XCD (they are dealt to the XCDs round robin), so its
   // tiles' operand rows stay in that XCD's L2.
-  const int home = EPI == kEpiExperts ? 0 : (int)blockIdx.x % a.n_lists;
+  const int home = kGrouped ? 0 : (int)blockIdx.x % a.n_lists;
 
   // workgroups whose first tile is taken statically (pull: all but the copiers at the end)
   const int nstat = (EPI == kEpiAllGather && (a.pull || a.copiers_last)) ? (int)gridDim.x - a.copy_wgs
                                                                         : (int)gridDim.x;
   // experts: low tiles exist for the 256-row shapes
-  constexpr bool kLowTiles = EPI == kEpiExperts && BM == 256;
+  constexpr bool kLowTiles = kGrouped && BM == 256;
   [[maybe_unused]] auto deal = [&] {
-    if constexpr (EPI == kEpiExperts) {
-      expert_row_tiles<BM, kLowTiles>(a.x, tid, sm.first, sm.low, sm.sums);
+    if constexpr (kGrouped) {
+      if constexpr (EPI == kEpiExperts) expert_row_tiles<BM, kLowTiles>(a.x, tid, sm.first, sm.low, sm.sums);
+      else one_row_tiles<BM, kLowTiles>(a.x.slots, tid, sm.first, sm.low);
       return ExpertDeal(sm.first[a.x.n_experts] * a.n_col_tiles, sm.low[a.x.n_experts] * a.n_col_tiles);
     } else {
       return 0;
     }
   }();
   auto claim_tile = [&](bool first) {
-    if constexpr (EPI == kEpiExperts) {
+    if constexpr (kGrouped) {
       const bool low = deal.next >= deal.end;
       if (tid == 0) {
         ExpertTile t{0, -1, 0};
@@ -1142,7 +1279,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
     // single-operation kernel
     auto tile_body = [&](auto ph1_) {
       const int vcol = __builtin_amdgcn_readfirstlane(s_tile[1]);
-      const int ksplit = EPI == kEpiExperts ? 1 : a.ksplit;
+      const int ksplit = kGrouped ? 1 : a.ksplit;
       const int col_tile = vcol / ksplit, part = vcol - col_tile * ksplit;
       const int expert = EPI == kEpiExperts ? __builtin_amdgcn_readfirstlane(s_tile[2]) : 0;
       // FFN chain: phase 1 (AllGather+GEMM into h) or phase 2 (GEMM+ReduceScatter of h); the
@@ -1158,6 +1295,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
         lo = __builtin_amdgcn_readfirstlane((int)expert_bound(a.x, expert)) + (int64_t)row_tile * BM;
         const int64_t end = __builtin_amdgcn_readfirstlane((int)expert_bound(a.x, expert + 1));
         hi = lo + BM < end ? lo + BM : end;
+        block = tib = 0;
+      } else if constexpr (EPI == kEpiLinear) {
+        lo = (int64_t)row_tile * BM;
+        hi = lo + BM < a.x.slots ? lo + BM : a.x.slots;
         block = tib = 0;
       } else {
         tile_rows<BM>(a, row_tile, (EPI == kEpiReduceScatter || EPI == kEpiFfn) && !ph1, lo, hi, block, tib);
@@ -1274,7 +1415,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
           const int r = (kPairs || kMixed) ? pair_row(j) : (j * NW + wave) * 16 + (lane >> 2);  // tile row
           const uint32_t g = (kPairs || kMixed) ? pair_gk(r) : gk;
           const int64_t gr = lo + r;
-          if constexpr (EPI == kEpiExperts) {
+          if constexpr (EPI == kEpiLinear) {
+            base[j] = gr < hi ? (uint32_t)r * (uint32_t)a.x.a_stride + g : kOutOfRange;
+          } else if constexpr (EPI == kEpiExperts) {
             // the row of A that the slot takes (through slot_token), or, without one, row r of the
             // descriptor that starts at the tile's first slot
             base[j] = kOutOfRange;
@@ -1302,7 +1445,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
       // whose 16-row group lies in one shard when shards are multiples of 16 rows
       constexpr bool kGroupPull = BM <= 128;
       u32x4 da;
-      if constexpr (EPI == kEpiExperts) {
+      if constexpr (EPI == kEpiLinear) {
+        // (row r of the descriptor that starts at the tile's first row)
+        da = buffer_desc(opA + lo * a.x.a_stride, (uint32_t)((hi - lo - 1) * a.x.a_stride + kbytes));
+      } else if constexpr (EPI == kEpiExperts) {
         const int64_t rows = a.x.slot_token ? a.x.a_rows : hi - lo;
         da = buffer_desc(opA + (a.x.slot_token ? 0 : lo * a.x.a_stride),
                          (uint32_t)((rows - 1) * a.x.a_stride + kbytes));
@@ -1720,7 +1866,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
         return FP8 ? wn * WTN + (j >> 2) * 32 + (j & 3) * 8 + (lane >> 5) * 4
                    : wn * WTN + j * 16 + (lane >> 4) * 4;
       };
-      if constexpr (EPI == kEpiExperts) {
+      if constexpr (EPI == kEpiLinear) {
+        linear_epilogue<BM, BN, FP8, FM, FN, kStageBytes, WTM>(a, acc, stages, wm * wave_rows, FM >> low, lo, hi, n0, qrow,
+                                                               qcol);
+      } else if constexpr (EPI == kEpiExperts) {
         expert_epilogue<FP8, FM, FN>(a, acc, expert, lo, hi, n0, qrow, qcol);
       } else if (EPI == kEpiFfn && ph1) {
         // phase 1: h = silu(acc) as bf16, written through (phase-2 tiles on any XCD read it), then
@@ -2080,7 +2229,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
     else tile_body(std::false_type{});
   }
 
-  if constexpr (EPI == kEpiExperts) return;   // no counters to clear
+  if constexpr (kGrouped) return;   // no counters to clear
 
   // (only a launch that computes the tiles reduces: a copy-only launch leaves `out` alone)
   if (((EPI == kEpiReduceScatter && !a.fuse_local) || EPI == kEpiFfn) && a.n_row_tiles > 0)

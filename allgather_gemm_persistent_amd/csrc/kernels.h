@@ -30,7 +30,7 @@ constexpr int kMaxLists = 16;
 
 constexpr int kXcds = 8;           // accelerator dies of an MI355X, each with its own L2
 
-enum Epilogue { kEpiAllGather = 0, kEpiReduceScatter = 1, kEpiAllReduce = 2, kEpiFfn = 3, kEpiExperts = 4 };
+enum Epilogue { kEpiAllGather = 0, kEpiReduceScatter = 1, kEpiAllReduce = 2, kEpiFfn = 3, kEpiExperts = 4, kEpiLinear = 5 };
 
 // One set of copy jobs of the in-kernel producer: job i*pieces + q of the set moves piece q of the
 // i-th arriving chunk from its peer's block into the symmetric buffer; the job completing a chunk
@@ -59,6 +59,15 @@ struct ExpertArgs {
   int64_t a_rows, a_stride;   // rows of A and the bytes from one to the next
   int n_experts;
   int gated;                  // B = [gate | up], out = silu(A gate) * (A up)
+};
+
+// The epilogue of a product with one (kEpiLinear): out = act(product + bias) + residual.
+struct LinearArgs {
+  const uint16_t* bias;       // bfloat16 per column, or null
+  const void* residual;       // rows of bfloat16 or float, or null
+  void* out;                  // rows of bfloat16 or float
+  int64_t ld_residual, ld_out;   // elements
+  int act, residual_fp32, out_fp32;
 };
 
 struct GemmArgs {
@@ -131,8 +140,10 @@ struct GemmArgs {
   int chunk_rows1, cps1;
   int n_row_tiles1, n_col_tiles1;
   // experts' products (kEpiExperts): `a` rows taken through x, `b` n_experts x K x N, `c` slots x
-  // N (gated: N/2) bfloat16
+  // N (gated: N/2) bfloat16. A product with an epilogue (kEpiLinear): one expert that holds every
+  // slot (no offsets, no slot_token), its result in y
   ExpertArgs x;
+  LinearArgs y;
 };
 
 // Launch the persistent kernel instantiated for (bm, bn, dtype, epilogue) with `grid`

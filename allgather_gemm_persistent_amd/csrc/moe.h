@@ -17,11 +17,16 @@ struct StreamArgs {
   float* ws;            // ksplit > 1: ksplit x slots x N floats
   int64_t ws_bytes;
   uint32_t* counts;     // ksplit > 1: n_experts x strips counters, zero before and after
+  LinearArgs y;         // a product with an epilogue: the epilogue and the result (not c)
 };
 
 hipError_t launch_expert_stream(const StreamArgs& args, int dtype, hipStream_t stream);
 // The tiled kernel: args as kEpiExperts reads them, tiles of bm x bn.
 hipError_t launch_expert_tiles(const GemmArgs& args, int bm, int bn, int dtype, int grid, hipStream_t stream);
+
+// The same for a product with an epilogue (linear.hip): x describes one expert that holds every slot.
+hipError_t launch_linear_stream(const StreamArgs& args, int dtype, hipStream_t stream);
+hipError_t launch_linear_tiles(const GemmArgs& args, int bm, int bn, int dtype, int grid, hipStream_t stream);
 
 // ---- row operators
 struct NormArgs {

@@ -93,7 +93,7 @@ extern "C" int moe_gemm(agg_ctx* ctx, int64_t slots, int n_experts, int64_t n, i
                                       : choose_expert_shape(dtype, slots, n_experts, n, k, gated, units);
   if (shape.stream) {
     StreamArgs s{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(b), static_cast<uint16_t*>(out),
-                 cols, k, x, shape.strips, shape.ksplit, nullptr, 0, nullptr};
+                 cols, k, x, shape.strips, shape.ksplit, nullptr, 0, nullptr, {}};
     if (s.ksplit > 1) {
       s.ws_bytes = int64_t(s.ksplit) * slots * cols * int64_t(sizeof(float));
       if (int rc = ctx_moe_workspace(ctx, stream, size_t(s.ws_bytes), &s.ws, &s.counts)) return rc;

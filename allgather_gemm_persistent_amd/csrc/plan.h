@@ -99,6 +99,6 @@ struct ExpertShape {
   TileShape tile;
 };
 ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated,
-                                int units);
+                                int units, bool even = false);
 
 }  // namespace agg
