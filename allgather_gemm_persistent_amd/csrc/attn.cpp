@@ -136,6 +136,10 @@ extern "C" int agg_check_paged_attn_args(const agg_kv_cache* cache, int64_t rows
   if (out_dtype != AGG_BF16 && out_dtype != AGG_FP32) return fail(AGG_E_ARG, "out has dtype %d, not bf16 or fp32", out_dtype);
   if (rows > kMostRows / 1024) return fail(AGG_E_UNSUPPORTED, "rows beyond 2^20");
   CHECK(check_table(cache, table, seqs, seq_pages, ld_table));
+  // (the tiles of a row are counted in 31 bits)
+  const int64_t room = seq_pages * cache->page_size, splits = (q_heads / cache->kv_heads + 15) / 16;
+  if (((window > 0 && window < room ? window : room) / 32 + 2) * cache->kv_heads * splits >= (int64_t(1) << 31))
+    return fail(AGG_E_UNSUPPORTED, "%lld positions of %d heads are beyond 2^36", (long long)room, q_heads);
   if (rows == 0) return AGG_OK;
   const int64_t cols = int64_t(q_heads) * cache->head_dim;
   CHECK(check_rows(q, ld_q, cols, 2, "q"));

@@ -42,16 +42,22 @@ struct AttnArgs {
   void* out;                  // rows x (q_heads * head_dim), bfloat16 or float
   float* lse;                 // rows x q_heads, or null
   const int32_t* lens;
-  const int32_t* row_seq;     // or null: row r is sequence r
+  const int32_t* row_seq;     // or null: row r is sequence first_row + r
   const int32_t* table;       // seqs x seq_pages
   int64_t seqs, seq_pages, ld_table;
-  int64_t rows, ld_q, ld_out;
+  int64_t rows, first_row, ld_q, ld_out;
   int64_t window;             // 0: none
   float scale2;               // scale * log2(e)
   int q_heads, group;         // heads of queries, and how many share a head of the cache
   int row_tiles;              // 16-row tiles of a head's queries a workgroup takes at once (1, 2, 4)
   int out_fp32;
+  int least;                  // tiles of a unit at least
+  float* ws;                  // four slots of slot_bytes for every workgroup
+  int64_t ws_bytes;
+  int slot_bytes;
+  uint32_t* counts;           // eight for every workgroup, zero before and after
 };
-hipError_t launch_attn(const AttnArgs& a, hipStream_t stream);
+// `grid` workgroups divide the work; rows * kv_heads * (tiles of a row) stays below 2^31.
+hipError_t launch_attn(const AttnArgs& a, int grid, hipStream_t stream);
 
 }  // namespace agg

@@ -11,10 +11,14 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kAttnWaves = 4;
+constexpr int kAttnWaves = 4, kThreads = kAttnWaves * 64;
 constexpr int kTile = 32;                      // tokens a wave takes at once: two runs of 16
 constexpr int kBufferFlags = 0x00020000;       // word 3 of a raw buffer resource
 constexpr uint32_t kOutOfRange = 0x80000000u;  // an offset past every descriptor
+constexpr int kCoherent = 1 | 16;              // an access that bypasses the caches, or writes through them
+constexpr uint32_t kFan = 16;                  // units joined in one step
+constexpr int kChoices = 6;                    // lengths of a unit to choose from
+constexpr uint32_t kUnitCost = 6;              // of a unit, beside its tiles, in tiles
 constexpr float kLn2 = 0.693147181f;
 
 __device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -36,8 +40,16 @@ __device__ inline uint32_t widen8(uint32_t p) {
 
 }  // namespace
 
-// One workgroup per row, head of the cache and 16 * RT of the queries that share it; its four waves take runs
-// of the length and join their results.
+// An item is a row, a head of the cache, and up to 16 * RT of the queries that share it; its length counts in tiles of 32
+// tokens. An item is cut into equal units of at most S tiles, S by the lengths of all rows (choose, below), so long
+// sequences are split over many workgroups and short ones are not split at all; the workgroups take units in
+// turn, a unit's tiles divided among the four waves. An item of one unit is written at once; the units of others go
+// to the workspace (fp32, written through: output, maximum and sum), and the workgroup that finishes the last of them
+// joins them in their order. More than kFan units are joined in two steps, groups of them first, so that no
+// workgroup has many to read (one compute unit reads some 50 GB/s). Who is last depends on timing, what it
+// computes does not.
+//
+// The loads of the next unit's first tile are on their way before the results of a unit are summed and stored.
 //
 // A wave takes 32 tokens at a time through the matrix units, transposed, so that nothing passes between
 // lanes on the way: S^T = K Q^T with the tokens as rows and the (up to 16) queries as columns puts into lane
@@ -47,12 +59,13 @@ __device__ inline uint32_t widen8(uint32_t p) {
 // byte permutes inside the lane: fragment m holds channel m of every lane's chunk.
 //
 // Softmax in one pass: a lane holds the running maximum and sum (in powers of 2) of its query, over its own
-// tokens the sum, over all the maximum. The weights enter the second product as a bf16 and the bf16 of what that
-// leaves, so they carry 16 bits; the matrix units are far from busy (32 tokens of 128 channels are 8 KiB of K
-// and of V, and 24 matrix instructions).
-template <bool FP8, int DP, int RT>
-__global__ void __launch_bounds__(kAttnWaves * 64) attn_kernel(const AttnArgs a) {
+// tokens the sum, over all the maximum. The weights enter the second product in bf16 parts, each the bf16 of what the
+// ones before leave: two, 16 bits, for a bf16 result, three, the whole fp32, for an fp32 one; the matrix units are far
+// from busy (32 tokens of 128 channels are 8 KiB of K and of V, and 24 or 32 matrix instructions).
+template <bool FP8, int DP, int RT, bool OUT32>
+__global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_kernel(const AttnArgs a) {
   constexpr int EL = FP8 ? 1 : 2;
+  constexpr int PARTS = OUT32 ? 3 : 2;         // of the weights
   constexpr int KS = DP / 32;                  // contraction steps of the first product
   constexpr int VE = DP / 16;                  // channels of V a lane holds
   constexpr int KL = DP * EL / 64;             // 16-byte loads of a token's keys by a lane
@@ -60,53 +73,182 @@ __global__ void __launch_bounds__(kAttnWaves * 64) attn_kernel(const AttnArgs a)
   constexpr int PO = DP + 4;                   // padded row of the partial results
   __shared__ __attribute__((aligned(16))) float s_o[kAttnWaves][16][PO];
   __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16];
+  __shared__ uint32_t s_sum[kAttnWaves][kChoices], s_units[kThreads], s_slots[kThreads], s_last;
+  __shared__ int s_seq[kThreads], s_len[kThreads];
 
   const agg_kv_cache& cache = a.cache;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int D = cache.head_dim, pg = cache.page_size;
-  // the item
-  const int splits = (a.group + 16 * RT - 1) / (16 * RT);
-  const int item = blockIdx.x;
-  const int part = item % splits, head = item / splits % cache.kv_heads;
-  const int64_t row = item / splits / cache.kv_heads;
-  const int q0 = part * 16 * RT;               // first query of the head's group
-  const int held = a.group - q0 < 16 * RT ? a.group - q0 : 16 * RT;
-
-  // its tokens [lo, hi)
-  const int seq = __builtin_amdgcn_readfirstlane(a.row_seq ? a.row_seq[row] : (int)row);
+  // ---- the lengths, and with them the units of each row
   const int room = (int)(a.seq_pages * pg);
-  int hi = __builtin_amdgcn_readfirstlane(a.lens[row]);
-  hi = seq < 0 || seq >= a.seqs || hi < 0 ? 0 : hi < room ? hi : room;
-  const int lo = a.window > 0 && hi > a.window ? (int)(hi - a.window) : 0;
-  const int32_t* const table = a.table + (hi > 0 ? seq * a.ld_table : 0);
-
-  // this wave's runs of 32 tokens
-  const int first = lo / kTile, tiles = hi > lo ? (hi + kTile - 1) / kTile - first : 0;
-  const int t_lo = first + tiles * wave / kAttnWaves, t_hi = first + tiles * (wave + 1) / kAttnWaves;
-
-  // Q: column c, steps of 32 channels; lane's 8 of step s as K's lane has them
-  u32x4 qf[RT][KS];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d = FP8 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
-      const int j = r * 16 + c;
-      qf[r][s] = u32x4{};
-      if (j < held && d < D)
-        qf[r][s] = *reinterpret_cast<const u32x4*>(a.q + row * a.ld_q + (int64_t)(head * a.group + q0 + j) * D + d);
+  struct Row {
+    int seq, lo, hi;                           // its tokens [lo, hi)
+    uint32_t tiles;                            // one for an empty row, which has to be written too
+  };
+  auto row_of = [&](int seq, int n) {
+    Row x;
+    x.seq = seq;
+    x.hi = seq < 0 || seq >= a.seqs || n < 0 ? 0 : n < room ? n : room;
+    x.lo = a.window > 0 && x.hi > a.window ? (int)(x.hi - a.window) : 0;
+    x.tiles = x.hi > x.lo ? ((uint32_t)x.hi + kTile - 1) / kTile - (uint32_t)x.lo / kTile : 1;
+    return x;
+  };
+  auto row_at = [&](uint32_t r) { return row_of(a.row_seq ? a.row_seq[r] : (int)(a.first_row + r), a.lens[r]); };
+  // thread t counts rows [t * chunk, + chunk)
+  const uint32_t rows = (uint32_t)a.rows, chunk = (rows + kThreads - 1) / kThreads;
+  const uint32_t splits = (uint32_t)((a.group + 16 * RT - 1) / (16 * RT)), items = splits * (uint32_t)cache.kv_heads;
+  auto each_row = [&](auto f) {
+    for (uint32_t i = 0; i < chunk; ++i) {
+      const uint32_t r = (uint32_t)tid * chunk + i;
+      if (r < rows) f(row_at(r));
     }
-
-  f32x4 o[RT][VE];
-  float m[RT], l[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) o[r][e] = f32x4{};
+  };
+  uint32_t mine = 0;
+  Row only{0, 0, 0, 0};                        // (up to a row a thread: kept)
+  if (chunk == 1) {
+    if ((uint32_t)tid < rows) only = row_at((uint32_t)tid);
+    mine = only.tiles;
+    s_seq[tid] = only.seq;
+    s_len[tid] = only.hi;
+  } else {
+    each_row([&](const Row& x) { mine += x.tiles; });
   }
+  auto sum_of = [&](uint32_t (&v)[kChoices]) {  // over the workgroup
+#pragma unroll
+    for (int k = 0; k < kChoices; ++k) {
+#pragma unroll
+      for (int d = 32; d > 0; d /= 2) v[k] += (uint32_t)__shfl_xor((int)v[k], d);
+      if (lane == 0) s_sum[wave][k] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kChoices; ++k)
+      v[k] = __builtin_amdgcn_readfirstlane(s_sum[0][k] + s_sum[1][k] + s_sum[2][k] + s_sum[3][k]);
+    __syncthreads();
+  };
+  uint32_t n[kChoices] = {mine};
+  sum_of(n);
+  const uint32_t grid = gridDim.x, total = n[0] * items, share = (total + grid - 1) / grid;
+  // ---- choose S: of some multiples of an even share, the one that is expected to end first. A unit costs its tiles and
+  // as much as kUnitCost of them; where every unit has a workgroup of its own the longest one counts, else the mean and half
+  // of the longest
+  auto candidate = [&](int k) {
+    constexpr uint32_t quarters[kChoices] = {2, 4, 5, 6, 8, 16};
+    const uint32_t x = (share * quarters[k] + 3) / 4;
+    return x < (uint32_t)a.least ? (uint32_t)a.least : x;
+  };
+#pragma unroll
+  for (int k = 0; k < kChoices; ++k) n[k] = 0;
+  auto count = [&](const Row& x) {
+#pragma unroll
+    for (int k = 0; k < kChoices; ++k) n[k] += (x.tiles + candidate(k) - 1) / candidate(k);
+  };
+  if (chunk == 1) count(only);
+  else each_row(count);
+  sum_of(n);
+  uint32_t most = 0, best = 0xFFFFFFFFu;
+#pragma unroll
+  for (int k = 0; k < kChoices; ++k) {
+    const uint32_t s = candidate(k), u = n[k] * items;
+    const uint32_t cost = u <= grid ? s + kUnitCost : share + s / 2 + (uint32_t)((uint64_t)u * kUnitCost / grid);
+    if (cost < best) {
+      best = cost;
+      most = s;
+    }
+  }
+  // ---- units, and slots of the workspace, of the rows before each thread's. (An item of more units than one has fewer than
+  // twice its tiles over S, and S is at least half of an even share: slots are fewer than 4 * grid)
+  uint32_t units = 0, slots = 0;
+  auto add = [&](const Row& x) {
+    const uint32_t k = (x.tiles + most - 1) / most;
+    units += k;
+    slots += k > 1 ? k : 0;
+  };
+  if (chunk == 1) add(only);
+  else each_row(add);
+  uint32_t upto = units, slots_upto = slots;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t x = (uint32_t)__shfl_up((int)upto, d), y = (uint32_t)__shfl_up((int)slots_upto, d);
+    if (lane >= d) {
+      upto += x;
+      slots_upto += y;
+    }
+  }
+  if (lane == 63) {
+    s_sum[wave][0] = upto;
+    s_sum[wave][1] = slots_upto;
+  }
+  __syncthreads();
+  uint32_t all = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnWaves; ++w) {
+    if (w < wave) {
+      upto += s_sum[w][0];
+      slots_upto += s_sum[w][1];
+    }
+    all += s_sum[w][0];
+  }
+  s_units[tid] = upto;
+  s_slots[tid] = slots_upto - slots;
+  __syncthreads();
+  const uint32_t all_units = __builtin_amdgcn_readfirstlane(all) * items;
+
+  struct Unit {
+    uint32_t row;
+    int seq, lo, hi;
+    int t_lo, t_hi;                            // this wave's tiles
+    int head, q0, held;                        // the first of its queries in the head's group, and how many
+    uint32_t part, parts;                      // which unit of the item, and of how many
+    uint32_t slot;                             // the item's first place in the workspace
+  };
+  auto locate = [&](uint32_t u) {
+    const uint32_t x = u / items;
+    // the first thread whose rows reach past x
+    int t = 0;
+#pragma unroll
+    for (int step = kThreads / 2; step > 0; step /= 2)
+      if (s_units[t + step - 1] <= x) t += step;
+    t = __builtin_amdgcn_readfirstlane(t);
+    uint32_t r = (uint32_t)t * chunk, before = __builtin_amdgcn_readfirstlane(t ? s_units[t - 1] : 0u);
+    uint32_t slots_before = __builtin_amdgcn_readfirstlane(s_slots[t]);
+    Row at;
+    if (chunk == 1) {
+      at = row_of(s_seq[t], 0);
+      at.hi = s_len[t];
+    } else {
+      for (;; ++r) {
+        at = row_at(r);
+        const uint32_t k = (__builtin_amdgcn_readfirstlane(at.tiles) + most - 1) / most;
+        if (before + k > x) break;
+        before += k;
+        slots_before += k > 1 ? k : 0;
+      }
+    }
+    at.seq = __builtin_amdgcn_readfirstlane(at.seq);
+    at = row_of(at.seq, __builtin_amdgcn_readfirstlane(at.hi));
+    Unit y;
+    y.row = r;
+    y.seq = at.seq;
+    y.lo = at.lo;
+    y.hi = at.hi;
+    y.parts = (at.tiles + most - 1) / most;
+    const uint32_t in = u - before * items, item = in / y.parts;
+    y.part = in - item * y.parts;
+    y.head = (int)(item / splits);
+    y.q0 = (int)(item % splits) * 16 * RT;
+    y.held = a.group - y.q0 < 16 * RT ? a.group - y.q0 : 16 * RT;
+    y.slot = slots_before * items + item * y.parts;
+    // (tiles below 2^25 by parts that are at least 4 tiles long: the products stay inside 64 bits)
+    const uint32_t from = (uint32_t)((uint64_t)at.tiles * y.part / y.parts);
+    const uint32_t len = (uint32_t)((uint64_t)at.tiles * (y.part + 1) / y.parts) - from;
+    const int first = at.lo / kTile + (int)from;
+    y.t_lo = first + (int)(len * (uint32_t)wave / kAttnWaves);
+    y.t_hi = at.hi > at.lo ? first + (int)(len * (uint32_t)(wave + 1) / kAttnWaves) : y.t_lo;
+    return y;
+  };
+  const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(a.ws, 0, (int)a.ws_bytes, kBufferFlags);
 
   // offsets of this lane in a run of 16 tokens
   const uint32_t token_bytes = (uint32_t)(cache.ld_token * EL);
@@ -125,6 +267,9 @@ __global__ void __launch_bounds__(kAttnWaves * 64) attn_kernel(const AttnArgs a)
     voff[i] = d < D ? (uint32_t)(d * EL) : kOutOfRange;
   }
 
+  // ---- the unit in work, or the next one
+  int head = 0, lo = 0, hi = 0;
+  const int32_t* table = a.table;
   // the page of each run of 16 tokens, and the place in it: 64 runs in the lanes at a time
   int pages = -1, inside = 0, block = -1;
   auto look_up = [&](int run) {
@@ -221,11 +366,45 @@ __global__ void __launch_bounds__(kAttnWaves * 64) attn_kernel(const AttnArgs a)
 
   Keys kx;
   Values vx;
-  if (t_lo < t_hi) {
-    load_keys(kx, t_lo);
-    load_values(vx, t_lo);
+  u32x4 qf[RT][KS];
+  auto begin = [&](const Unit& u) {
+    head = u.head;
+    lo = u.lo;
+    hi = u.hi;
+    table = a.table + (hi > 0 ? u.seq * a.ld_table : 0);
+    block = -1;
+    // Q: column c, steps of 32 channels; lane's 8 of step s as K's lane has them
+    const uint16_t* const q = a.q + (int64_t)u.row * a.ld_q + (int64_t)(head * a.group + u.q0) * D;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int d = FP8 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
+        const int j = r * 16 + c;
+        qf[r][s] = u32x4{};
+        if (j < u.held && d < D) qf[r][s] = *reinterpret_cast<const u32x4*>(q + j * D + d);
+      }
+    if (u.t_lo < u.t_hi) {
+      load_keys(kx, u.t_lo);
+      load_values(vx, u.t_lo);
+    }
+  };
+
+  uint32_t number = blockIdx.x;
+  if (number >= all_units) return;
+  Unit now = locate(number);
+  begin(now);
+  for (;;) {
+  f32x4 o[RT][VE];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) o[r][e] = f32x4{};
   }
-  for (int tile = t_lo; tile < t_hi; ++tile) {
+  for (int tile = now.t_lo; tile < now.t_hi; ++tile) {
     // ---- S^T, times the scale and in powers of 2
     f32x4 s[RT][2];
 #pragma unroll
@@ -282,54 +461,80 @@ __global__ void __launch_bounds__(kAttnWaves * 64) attn_kernel(const AttnArgs a)
           if constexpr (FP8) s[r][u][i] = in[u][i] ? s[r][u][i] * vx.scale[u][i] : 0.0f;
         }
     }
-    if (tile + 1 < t_hi) load_keys(kx, tile + 1);
+    if (tile + 1 < now.t_hi) load_keys(kx, tile + 1);
     // ---- O^T
-    u32x4 hi2[RT], lo2[RT];
+    u32x4 w[RT][PARTS];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const float x = s[r][p >> 1][2 * (p & 1)], y = s[r][p >> 1][2 * (p & 1) + 1];
-        hi2[r][p] = pack2(x, y);
-        lo2[r][p] = pack2(x - low_half(hi2[r][p]), y - high_half(hi2[r][p]));
+        float x = s[r][p >> 1][2 * (p & 1)], y = s[r][p >> 1][2 * (p & 1) + 1];
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t) {
+          w[r][t][p] = pack2(x, y);
+          x -= low_half(w[r][t][p]);
+          y -= high_half(w[r][t][p]);
+        }
       }
     // fragments of two channels at a time
-    auto turn = [&](const uint32_t (&w)[8], int e) {
-      u32x4 f0, f1;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        f0[p] = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], 0x05040100u);
-        f1[p] = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], 0x07060302u);
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        o[r][e] = mfma16(f0, hi2[r], o[r][e]);
-        o[r][e] = mfma16(f0, lo2[r], o[r][e]);
-        o[r][e + 1] = mfma16(f1, hi2[r], o[r][e + 1]);
-        o[r][e + 1] = mfma16(f1, lo2[r], o[r][e + 1]);
-      }
-    };
 #pragma unroll
     for (int e = 0; e < VE; e += 2) {
-      uint32_t w[8];
+      uint32_t v[8];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         if constexpr (FP8) {
           const uint32_t x = vx.v[t >> 2][t & 3][e / 4];
-          w[t] = e & 2 ? widen8<true>(x) : widen8<false>(x);
+          v[t] = e & 2 ? widen8<true>(x) : widen8<false>(x);
         } else {
-          w[t] = vx.v[t >> 2][t & 3][e / 2];
+          v[t] = vx.v[t >> 2][t & 3][e / 2];
         }
       }
-      turn(w, e);
+      u32x4 f0, f1;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        f0[p] = __builtin_amdgcn_perm(v[2 * p + 1], v[2 * p], 0x05040100u);
+        f1[p] = __builtin_amdgcn_perm(v[2 * p + 1], v[2 * p], 0x07060302u);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t) {
+          o[r][e] = mfma16(f0, w[r][t], o[r][e]);
+          o[r][e + 1] = mfma16(f1, w[r][t], o[r][e + 1]);
+        }
     }
-    if (tile + 1 < t_hi) load_values(vx, tile + 1);
+    if (tile + 1 < now.t_hi) load_values(vx, tile + 1);
   }
 
   // ---- the waves' results, 16 queries at a time
+  const Unit done = now;
+  number += grid;
+  const bool more = number < all_units;
+  if (more) {
+    now = locate(number);
+    begin(now);
+  }
+  // a result: query j of the item, channels d .. d + 3
+  auto finish = [&](int j, int d, float top, float sum, const f32x4& y) {
+    const float inv = sum > 0.0f ? 1.0f / sum : sum;       // (a NaN stays one)
+    const int qh = done.head * a.group + done.q0 + j;
+    const int64_t to = (int64_t)done.row * a.ld_out + (int64_t)qh * D + d;
+    const f32x4 v = y * inv;
+    if constexpr (OUT32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = v;
+    else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + to) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+    if (a.lse && d == 0) a.lse[(int64_t)done.row * a.q_heads + qh] = sum > 0.0f ? top * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
+  };
+  // a place of the workspace: its queries' outputs, then their maxima and sums, and the same of a group
+  auto put = [&](uint32_t slot, int step, int j, int d, float top, float sum, const f32x4& y) {
+    const uint32_t to = slot * (uint32_t)a.slot_bytes;
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), ws, (int)(to + (uint32_t)(j * D + d) * 4), 0, kCoherent);
+    if (d == 0)
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{top, sum}), ws,
+                                            (int)(to + (uint32_t)(done.held * (D + 2 * step) + 2 * j) * 4), 0, kCoherent);
+  };
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    if (r * 16 >= held) break;
+    if (r * 16 >= done.held) break;
     float sum = l[r];
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
@@ -342,61 +547,142 @@ __global__ void __launch_bounds__(kAttnWaves * 64) attn_kernel(const AttnArgs a)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        s_o[wave][c][e / VC * 16 * VC + (4 * g + i) * VC + e % VC] = o[r][e][i];
+      for (int e = 0; e < VE; e += 4)
+        *reinterpret_cast<f32x4*>(&s_o[wave][c][e / VC * 16 * VC + (4 * g + i) * VC + e % VC]) =
+            f32x4{o[r][e][i], o[r][e + 1][i], o[r][e + 2][i], o[r][e + 3][i]};
     __syncthreads();
-    for (int x = tid; x < 16 * (DP / 8); x += kAttnWaves * 64) {
-      const int j = x / (DP / 8), d = x % (DP / 8) * 8;
-      if (r * 16 + j >= held || d >= D) continue;
+    for (int x = tid; x < 16 * (DP / 4); x += kThreads) {
+      const int j = x / (DP / 4), d = x % (DP / 4) * 4;
+      if (r * 16 + j >= done.held || d >= D) continue;
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, s_m[w][j]);
       const float base = top == -INFINITY ? 0.0f : top;
-      float total = 0.0f, y[8] = {};
+      float all_sum = 0.0f;
+      f32x4 y = f32x4{};
 #pragma unroll
       for (int w = 0; w < kAttnWaves; ++w) {
         const float by = __builtin_amdgcn_exp2f(s_m[w][j] - base);
-        total += by * s_l[w][j];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] += by * s_o[w][j][d + e];
+        all_sum += by * s_l[w][j];
+        y += by * *reinterpret_cast<const f32x4*>(&s_o[w][j][d]);
       }
-      const float inv = total > 0.0f ? 1.0f / total : total;   // (a NaN stays one)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= inv;
-      const int qh = head * a.group + q0 + r * 16 + j;
-      const int64_t to = row * a.ld_out + (int64_t)qh * D + d;
-      if (a.out_fp32) {
-        f32x4* const p = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to);
-        p[0] = f32x4{y[0], y[1], y[2], y[3]};
-        p[1] = f32x4{y[4], y[5], y[6], y[7]};
-      } else {
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to) = narrow(y);
-      }
-      if (a.lse && d == 0) a.lse[row * a.q_heads + qh] = top == -INFINITY ? top : top * kLn2 + logf(total);
+      if (done.parts == 1) finish(r * 16 + j, d, top, all_sum, y);
+      else put(done.slot + done.part, 0, r * 16 + j, d, top, all_sum, y);
     }
+  }
+  if (done.parts > 1) {
+    // ---- the units' results, in groups of `fan` and then the groups'
+    auto arrive = [&](uint32_t counter, uint32_t expected) {
+      // (the stores have completed, so no fence is needed: who reads them bypasses the caches too. The count is left at
+      // zero for the next launch)
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (tid == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(a.counts + counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = before == expected - 1;
+        if (before == expected - 1) __hip_atomic_store(a.counts + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      return __builtin_amdgcn_readfirstlane(s_last) != 0;
+    };
+    // the results in slots first, first + apart, ... (n of them) as one; `give` takes it
+    auto join = [&](uint32_t first, uint32_t apart, uint32_t n, int step, auto give) {
+      const int quads = D / 4;
+      // threads of a quad: as many as there are to spare, up to 8, each every so manyth result
+      uint32_t log2 = 0;
+      while (log2 < 3 && (done.held * quads) << (log2 + 1) <= kThreads) ++log2;
+      const uint32_t sub = (uint32_t)tid & ((1u << log2) - 1), stride = 1u << log2;
+      for (int x = tid >> log2; x < (done.held * quads + (kThreads >> log2) - 1) / (kThreads >> log2) * (kThreads >> log2);
+           x += kThreads >> log2) {
+        const bool in = x < done.held * quads;
+        const int j = in ? x / quads : 0, d = in ? x % quads * 4 : 0;
+        float top = -INFINITY, sum = 0.0f;
+        f32x4 y = f32x4{};
+        constexpr int B = 8;
+        for (uint32_t i0 = sub; i0 < n; i0 += B * stride) {
+          f32x4 v[B];
+          f32x2 ms[B];
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            const uint32_t i = i0 + b * stride;
+            const uint32_t from = i < n ? (first + i * apart) * (uint32_t)a.slot_bytes : kOutOfRange;
+            v[b] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                ws, (int)((from + (uint32_t)(j * D + d) * 4) | (from & kOutOfRange)), 0, kCoherent));
+            ms[b] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                ws, (int)((from + (uint32_t)(done.held * (D + 2 * step) + 2 * j) * 4) | (from & kOutOfRange)), 0, kCoherent));
+            if (i >= n) ms[b][0] = -INFINITY;
+          }
+          float high = top;
+#pragma unroll
+          for (int b = 0; b < B; ++b) high = fmaxf(high, ms[b][0]);
+          const float base = high == -INFINITY ? 0.0f : high;
+          const float keep = __builtin_amdgcn_exp2f(top - base);
+          sum *= keep;
+          y *= keep;
+          top = high;
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            const float by = __builtin_amdgcn_exp2f(ms[b][0] - base);
+            sum += by * ms[b][1];
+            y += by * v[b];
+          }
+        }
+        for (uint32_t s = 1; s < stride; s *= 2) {
+          const float other = __shfl_xor(top, (int)s);
+          const float both = fmaxf(top, other), base = both == -INFINITY ? 0.0f : both;
+          const float keep = __builtin_amdgcn_exp2f(top - base), take = __builtin_amdgcn_exp2f(other - base);
+          top = both;
+          sum = keep * sum + take * __shfl_xor(sum, (int)s);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = keep * y[e] + take * __shfl_xor(y[e], (int)s);
+        }
+        if (in && sub == 0) give(j, d, top, sum, y);
+      }
+    };
+    if (done.parts <= kFan) {
+      if (arrive(done.slot, done.parts)) join(done.slot, 1, done.parts, 0, finish);
+    } else {
+      uint32_t fan = kFan;
+      while (fan * fan < done.parts) fan *= 2;
+      const uint32_t group = done.part / fan, lead = done.slot + group * fan, groups = (done.parts + fan - 1) / fan;
+      const uint32_t n = done.parts - group * fan < fan ? done.parts - group * fan : fan;
+      if (arrive(lead, n)) {
+        // (the thread that reads an element of the leader's output writes it; the maxima and sums, which others
+        // read too, have a second place)
+        join(lead, 1, n, 0, [&](int j, int d, float top, float sum, const f32x4& y) { put(lead, 1, j, d, top, sum, y); });
+        if (arrive(4 * grid + done.slot, groups)) join(done.slot, fan, groups, 1, finish);
+      }
+    }
+  }
+  if (!more) return;
+  __syncthreads();                             // (the next unit writes s_o, s_m, s_l and s_last again)
   }
 }
 
-template <bool FP8, int DP>
-static hipError_t launch_attn_dp(const AttnArgs& a, hipStream_t stream) {
-  const int splits = (a.group + 16 * a.row_tiles - 1) / (16 * a.row_tiles);
-  const dim3 grid((unsigned)(a.rows * a.cache.kv_heads * splits)), block(kAttnWaves * 64);
-  if (a.row_tiles == 1) hipLaunchKernelGGL((attn_kernel<FP8, DP, 1>), grid, block, 0, stream, a);
-  else if (a.row_tiles == 2) hipLaunchKernelGGL((attn_kernel<FP8, DP, 2>), grid, block, 0, stream, a);
-  else if constexpr (DP < 256) hipLaunchKernelGGL((attn_kernel<FP8, DP, 4>), grid, block, 0, stream, a);
-  else return hipErrorInvalidValue;
+template <bool FP8, int DP, int RT>
+static hipError_t launch_attn_rt(const AttnArgs& a, int grid, hipStream_t stream) {
+  if (a.out_fp32) hipLaunchKernelGGL((attn_kernel<FP8, DP, RT, true>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((attn_kernel<FP8, DP, RT, false>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
-template <bool FP8>
-static hipError_t launch_attn_type(const AttnArgs& a, hipStream_t stream) {
-  if (a.cache.head_dim <= 64) return launch_attn_dp<FP8, 64>(a, stream);
-  if (a.cache.head_dim <= 128) return launch_attn_dp<FP8, 128>(a, stream);
-  return launch_attn_dp<FP8, 256>(a, stream);
+template <bool FP8, int DP>
+static hipError_t launch_attn_dp(const AttnArgs& a, int grid, hipStream_t stream) {
+  if (a.row_tiles == 1) return launch_attn_rt<FP8, DP, 1>(a, grid, stream);
+  if (a.row_tiles == 2) return launch_attn_rt<FP8, DP, 2>(a, grid, stream);
+  if constexpr (DP < 256) return launch_attn_rt<FP8, DP, 4>(a, grid, stream);
+  else return hipErrorInvalidValue;
 }
 
-hipError_t launch_attn(const AttnArgs& a, hipStream_t stream) {
-  return a.cache.dtype == AGG_FP8_E4M3 ? launch_attn_type<true>(a, stream) : launch_attn_type<false>(a, stream);
+template <bool FP8>
+static hipError_t launch_attn_type(const AttnArgs& a, int grid, hipStream_t stream) {
+  if (a.cache.head_dim <= 64) return launch_attn_dp<FP8, 64>(a, grid, stream);
+  if (a.cache.head_dim <= 128) return launch_attn_dp<FP8, 128>(a, grid, stream);
+  return launch_attn_dp<FP8, 256>(a, grid, stream);
+}
+
+hipError_t launch_attn(const AttnArgs& a, int grid, hipStream_t stream) {
+  return a.cache.dtype == AGG_FP8_E4M3 ? launch_attn_type<true>(a, grid, stream) : launch_attn_type<false>(a, grid, stream);
 }
 
 }  // namespace agg

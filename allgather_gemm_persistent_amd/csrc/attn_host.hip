@@ -20,6 +20,8 @@ int enter(const agg_ctx* ctx) {
   return AGG_OK;
 }
 
+constexpr int kAttnLeast = 4;   // 32-token tiles: one for each wave
+
 // (a dimension of one element may come with any stride: none is taken)
 agg_kv_cache without_idle_strides(const agg_kv_cache& c) {
   agg_kv_cache r = c;
@@ -77,9 +79,30 @@ extern "C" int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows,
   // what the registers hold
   const int most = cache->head_dim > 128 ? 2 : 4;
   const int tiles = group <= 16 ? 1 : group <= 32 || most == 2 ? 2 : 4;
-  const AttnArgs a{without_idle_strides(*cache), static_cast<const uint16_t*>(q), out, lse, lens, row_seq, table, seqs,
-                   seq_pages, ld_table, rows, ld_q, ld_out, window, scale * 1.442695041f, q_heads, group, tiles,
-                   out_dtype == AGG_FP32};
-  HIP_TRY(launch_attn(a, S(stream)));
+  AttnArgs a{without_idle_strides(*cache), static_cast<const uint16_t*>(q), out, lse, lens, row_seq, table, seqs,
+             seq_pages, ld_table, rows, 0, ld_q, ld_out, window, scale * 1.442695041f, q_heads, group, tiles,
+             out_dtype == AGG_FP32, kAttnLeast, nullptr, 0, 0, nullptr};
+  // the grid: what the compute units hold at once; and the workspace of its units
+  const int units = ctx_units(ctx) < kMoeCounters / 16 ? ctx_units(ctx) : kMoeCounters / 16;
+  const int grid = units * (tiles == 1 && cache->head_dim <= 128 ? 2 : 1);
+  const int queries = group < 16 * tiles ? group : 16 * tiles;
+  a.slot_bytes = (queries * (cache->head_dim + 4) * 4 + 15) / 16 * 16;
+  a.ws_bytes = int64_t(4) * grid * a.slot_bytes;
+  if (int rc = ctx_moe_workspace(ctx, stream, size_t(a.ws_bytes), &a.ws, &a.counts)) return rc;
+  // (a launch counts its tiles in 31 bits)
+  const int64_t splits = (group + 16 * tiles - 1) / (16 * tiles), room = seq_pages * cache->page_size;
+  const int64_t row_most = ((window > 0 && window < room ? window : room) / 32 + 2) * cache->kv_heads * splits;
+  const int64_t at_once = ((int64_t(1) << 31) - 1) / row_most;
+  for (int64_t r = 0; r < rows; r += at_once) {
+    AttnArgs p = a;
+    p.rows = rows - r < at_once ? rows - r : at_once;
+    p.first_row = r;
+    p.q += r * ld_q;
+    p.out = static_cast<char*>(out) + r * ld_out * (a.out_fp32 ? 4 : 2);
+    if (lse) p.lse += r * q_heads;
+    p.lens += r;
+    if (row_seq) p.row_seq += r;
+    HIP_TRY(launch_attn(p, grid, S(stream)));
+  }
   return AGG_OK;
 }

@@ -94,7 +94,8 @@ struct StaticScratch {
 std::mutex g_static_mu;
 StaticScratch g_static[kMaxDevices];
 
-// A workspace of moe_gemm's split K: kMoeCounters counters, then `bytes` for partial sums.
+// A workspace of a split (moe_gemm's and linear's K, paged_attn's length): kMoeCounters counters, then `bytes` for
+// partial results.
 struct MoeWorkspace {
   uint8_t* mem;
   size_t bytes;
@@ -799,9 +800,11 @@ int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws,
   while (w && !(w->stream == s && w->captured == captured && w->capture == capture && w->bytes >= bytes)) w = w->next;
   if (!w) {
     constexpr size_t kCounterBytes = size_t(kMoeCounters) * sizeof(uint32_t);
-    const size_t room = captured ? (bytes + 65535) / 65536 * 65536 : size_t(kMoeWsBytes);
+    // (an eager call's is there for later, larger calls too: powers of two)
+    size_t room = captured ? (bytes + 65535) / 65536 * 65536 : size_t(kMoeWsBytes);
+    while (room < bytes) room *= 2;
     w = new (std::nothrow) MoeWorkspace{nullptr, room, s, captured, capture, ctx->moe_ws};
-    if (!w) return fail(AGG_E_HIP, "moe_gemm: no host memory for a workspace");
+    if (!w) return fail(AGG_E_HIP, "no host memory for a workspace");
     // (an allocation is no work of the capture; the mode says so to the runtime, which otherwise
     // refuses it beside one)
     hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
@@ -815,7 +818,7 @@ int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws,
     }
     if (e != hipSuccess) {
       delete w;
-      return fail(AGG_E_HIP, "moe_gemm's workspace: %s", hipGetErrorString(e));
+      return fail(AGG_E_HIP, "a workspace of %zu bytes: %s", room, hipGetErrorString(e));
     }
     ctx->moe_ws = w;
   }

@@ -83,10 +83,10 @@ int ctx_device(const agg_ctx* ctx);
 // The tile shape agg_ctx_set_tile forces; {0, 0}: none.
 TileShape ctx_forced_tile(const agg_ctx* ctx);
 
-// The workspace of moe_gemm's split K for calls on `stream`, with room for `bytes` (at most kMoeWsBytes)
-// of partial sums, and kMoeCounters counters, one for every strip of every expert, that are zero when a
-// call starts and when it ends. Every stream has one of its own, and every capture on it, so calls that
-// are not ordered do not meet. Returns an AGG_E_* code.
+// The workspace of a split (moe_gemm's and linear's K: at most kMoeWsBytes, a counter for every strip of every
+// expert; paged_attn's length: eight counters for every workgroup) for calls on `stream`, with room for `bytes`
+// of partial results, and kMoeCounters counters that are zero when a call starts and when it ends. Every stream
+// has one of its own, and every capture on it, so calls that are not ordered do not meet. Returns an AGG_E_* code.
 constexpr int64_t kMoeWsBytes = int64_t(8) << 20;
 constexpr int kMoeCounters = 4096;
 int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws, uint32_t** counts);
