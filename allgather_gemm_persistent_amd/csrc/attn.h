@@ -55,7 +55,8 @@ struct AttnArgs {
   float* ws;                  // four slots of slot_bytes for every workgroup
   int64_t ws_bytes;
   int slot_bytes;
-  uint32_t* counts;           // eight for every workgroup, zero before and after
+  uint32_t* counts;           // eight for every workgroup and two, zero before and after
+  uint32_t page_magic, page_shift;   // x / (page_size / 16) = x * page_magic >> page_shift for x below 2^27
 };
 // `grid` workgroups divide the work; rows * kv_heads * (tiles of a row) stays below 2^31.
 hipError_t launch_attn(const AttnArgs& a, int grid, hipStream_t stream);

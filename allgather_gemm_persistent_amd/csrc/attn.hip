@@ -13,12 +13,13 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kAttnWaves = 4, kThreads = kAttnWaves * 64;
 constexpr int kTile = 32;                      // tokens a wave takes at once: two runs of 16
+constexpr int kBlock = 64;                     // tiles whose pages are looked up at once
 constexpr int kBufferFlags = 0x00020000;       // word 3 of a raw buffer resource
 constexpr uint32_t kOutOfRange = 0x80000000u;  // an offset past every descriptor
-constexpr int kCoherent = 1 | 16;              // an access that bypasses the caches, or writes through them
-constexpr uint32_t kFan = 16;                  // units joined in one step
+constexpr int kCoherent = 16;                  // an access that the whole GPU sees: past the L2, or written through it
+constexpr uint32_t kFan = 32;                  // units joined in one step
 constexpr int kChoices = 6;                    // lengths of a unit to choose from
-constexpr uint32_t kUnitCost = 6;              // of a unit, beside its tiles, in tiles
+constexpr float kUnitCost = 12;                // of a unit, beside its tiles, in tiles
 constexpr float kLn2 = 0.693147181f;
 
 __device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -31,6 +32,36 @@ __device__ inline uint32_t pack2(float lo, float hi) {
 }
 __device__ inline float low_half(uint32_t p) { return __builtin_bit_cast(float, p << 16); }
 __device__ inline float high_half(uint32_t p) { return __builtin_bit_cast(float, p & 0xFFFF0000u); }
+
+// Over the wave's lanes, without LDS: the sum of the lanes up to this one, and x of lane 63 of it.
+__device__ inline uint32_t sum_upto(uint32_t x) {
+  auto step = [&](auto ctrl, auto rows) {
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+  };
+  using std::integral_constant;
+  step(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});   // row_shr 1, 2, 4, 8
+  step(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+  step(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+  step(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // lane 15 of the row before, lane 31
+  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
+  return x;
+}
+__device__ inline uint32_t last_lane(uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane((int)x, 63); }
+
+// f over lanes l, l ^ 16, l ^ 32, l ^ 48. The swap exchanges the odd rows of 16 (or the upper 32 lanes) of one copy with the
+// even rows (the lower lanes) of the other, so the two copies then hold what is to be joined. (In asm: given one
+// value twice, the builtin's two results came out as one register. The nops are the wait between a vector write and
+// the swap that reads it.)
+template <typename F>
+__device__ inline float over_rows(float x, F f) {
+  float y = x;
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  x = f(x, y);
+  y = x;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return f(x, y);
+}
 
 // two e4m3 of a word as two bf16 (exact)
 template <bool HIGH>
@@ -73,8 +104,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   constexpr int PO = DP + 4;                   // padded row of the partial results
   __shared__ __attribute__((aligned(16))) float s_o[kAttnWaves][16][PO];
   __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16];
-  __shared__ uint32_t s_sum[kAttnWaves][kChoices], s_units[kThreads], s_slots[kThreads], s_last;
-  __shared__ int s_seq[kThreads], s_len[kThreads];
+  __shared__ uint32_t s_sum[kAttnWaves][kChoices], s_units[kThreads], s_slots[kThreads], s_last, s_next;
 
   const agg_kv_cache& cache = a.cache;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -95,41 +125,42 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
     return x;
   };
   auto row_at = [&](uint32_t r) { return row_of(a.row_seq ? a.row_seq[r] : (int)(a.first_row + r), a.lens[r]); };
-  // thread t counts rows [t * chunk, + chunk)
-  const uint32_t rows = (uint32_t)a.rows, chunk = (rows + kThreads - 1) / kThreads;
+  const uint32_t rows = (uint32_t)a.rows, grid = gridDim.x;
   const uint32_t splits = (uint32_t)((a.group + 16 * RT - 1) / (16 * RT)), items = splits * (uint32_t)cache.kv_heads;
+  // lane t of every wave holds row t; more than 64 rows: thread t counts rows [t * chunk, + chunk)
+  const bool few = rows <= 64;
+  const uint32_t chunk = (rows + kThreads - 1) / kThreads;
+  Row only{0, 0, 0, 0};
+  if (few && (uint32_t)lane < rows) only = row_at((uint32_t)lane);
   auto each_row = [&](auto f) {
-    for (uint32_t i = 0; i < chunk; ++i) {
-      const uint32_t r = (uint32_t)tid * chunk + i;
-      if (r < rows) f(row_at(r));
+    if (few) {
+      if (only.tiles) f(only);
+    } else {
+      for (uint32_t i = 0; i < chunk; ++i) {
+        const uint32_t r = (uint32_t)tid * chunk + i;
+        if (r < rows) f(row_at(r));
+      }
     }
   };
-  uint32_t mine = 0;
-  Row only{0, 0, 0, 0};                        // (up to a row a thread: kept)
-  if (chunk == 1) {
-    if ((uint32_t)tid < rows) only = row_at((uint32_t)tid);
-    mine = only.tiles;
-    s_seq[tid] = only.seq;
-    s_len[tid] = only.hi;
-  } else {
-    each_row([&](const Row& x) { mine += x.tiles; });
-  }
-  auto sum_of = [&](uint32_t (&v)[kChoices]) {  // over the workgroup
+  // sums over the rows
+  auto sum_all = [&](auto& v) {
+    constexpr int N = sizeof(v) / sizeof(v[0]);
 #pragma unroll
-    for (int k = 0; k < kChoices; ++k) {
+    for (int k = 0; k < N; ++k) v[k] = last_lane(sum_upto(v[k]));
+    if (few) return;
+    if (lane == 0)
 #pragma unroll
-      for (int d = 32; d > 0; d /= 2) v[k] += (uint32_t)__shfl_xor((int)v[k], d);
-      if (lane == 0) s_sum[wave][k] = v[k];
-    }
+      for (int k = 0; k < N; ++k) s_sum[wave][k] = v[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kChoices; ++k)
+    for (int k = 0; k < N; ++k)
       v[k] = __builtin_amdgcn_readfirstlane(s_sum[0][k] + s_sum[1][k] + s_sum[2][k] + s_sum[3][k]);
     __syncthreads();
   };
-  uint32_t n[kChoices] = {mine};
-  sum_of(n);
-  const uint32_t grid = gridDim.x, total = n[0] * items, share = (total + grid - 1) / grid;
+  uint32_t all_tiles[1] = {0};
+  each_row([&](const Row& x) { all_tiles[0] += x.tiles; });
+  sum_all(all_tiles);
+  const uint32_t total = all_tiles[0] * items, share = (total + grid - 1) / grid;
   // ---- choose S: of some multiples of an even share, the one that is expected to end first. A unit costs its tiles and
   // as much as kUnitCost of them; where every unit has a workgroup of its own the longest one counts, else the mean and half
   // of the longest
@@ -138,62 +169,58 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
     const uint32_t x = (share * quarters[k] + 3) / 4;
     return x < (uint32_t)a.least ? (uint32_t)a.least : x;
   };
+  // (units of a row: tiles / S, rounded up but for 2^-21 of it, by which the reciprocal is shorter: never more)
+  auto units_of = [&](uint32_t tiles, float inv) { return (uint32_t)ceilf((float)tiles * inv); };
+  uint32_t n[kChoices] = {};
+  float inv[kChoices];
 #pragma unroll
-  for (int k = 0; k < kChoices; ++k) n[k] = 0;
-  auto count = [&](const Row& x) {
+  for (int k = 0; k < kChoices; ++k) inv[k] = (1.0f - 0x1p-21f) / (float)candidate(k);
+  each_row([&](const Row& x) {
 #pragma unroll
-    for (int k = 0; k < kChoices; ++k) n[k] += (x.tiles + candidate(k) - 1) / candidate(k);
-  };
-  if (chunk == 1) count(only);
-  else each_row(count);
-  sum_of(n);
-  uint32_t most = 0, best = 0xFFFFFFFFu;
+    for (int k = 0; k < kChoices; ++k) n[k] += units_of(x.tiles, inv[k]);
+  });
+  sum_all(n);
+  float inv_most = 1.0f;
+  float best = INFINITY;
 #pragma unroll
   for (int k = 0; k < kChoices; ++k) {
-    const uint32_t s = candidate(k), u = n[k] * items;
-    const uint32_t cost = u <= grid ? s + kUnitCost : share + s / 2 + (uint32_t)((uint64_t)u * kUnitCost / grid);
+    const uint32_t u = n[k] * items;
+    const float s = (float)candidate(k);
+    const float cost = u <= grid ? s + kUnitCost : (float)share + 0.5f * s + (float)u / (float)grid * kUnitCost;
     if (cost < best) {
       best = cost;
-      most = s;
+      inv_most = inv[k];
     }
   }
   // ---- units, and slots of the workspace, of the rows before each thread's. (An item of more units than one has fewer than
-  // twice its tiles over S, and S is at least half of an even share: slots are fewer than 4 * grid)
+  // twice its tiles over S, and S is at least half of an even share: slots are no more than 4 * grid)
   uint32_t units = 0, slots = 0;
-  auto add = [&](const Row& x) {
-    const uint32_t k = (x.tiles + most - 1) / most;
+  each_row([&](const Row& x) {
+    const uint32_t k = units_of(x.tiles, inv_most);
     units += k;
     slots += k > 1 ? k : 0;
-  };
-  if (chunk == 1) add(only);
-  else each_row(add);
-  uint32_t upto = units, slots_upto = slots;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint32_t x = (uint32_t)__shfl_up((int)upto, d), y = (uint32_t)__shfl_up((int)slots_upto, d);
-    if (lane >= d) {
-      upto += x;
-      slots_upto += y;
+  });
+  uint32_t upto = sum_upto(units), slots_upto = sum_upto(slots), all_units = last_lane(upto) * items;
+  if (!few) {
+    if (lane == 63) {
+      s_sum[wave][0] = upto;
+      s_sum[wave][1] = slots_upto;
     }
-  }
-  if (lane == 63) {
-    s_sum[wave][0] = upto;
-    s_sum[wave][1] = slots_upto;
-  }
-  __syncthreads();
-  uint32_t all = 0;
+    __syncthreads();
+    uint32_t all = 0;
 #pragma unroll
-  for (int w = 0; w < kAttnWaves; ++w) {
-    if (w < wave) {
-      upto += s_sum[w][0];
-      slots_upto += s_sum[w][1];
+    for (int w = 0; w < kAttnWaves; ++w) {
+      if (w < wave) {
+        upto += s_sum[w][0];
+        slots_upto += s_sum[w][1];
+      }
+      all += s_sum[w][0];
     }
-    all += s_sum[w][0];
+    s_units[tid] = upto;
+    s_slots[tid] = slots_upto;
+    __syncthreads();
+    all_units = __builtin_amdgcn_readfirstlane(all) * items;
   }
-  s_units[tid] = upto;
-  s_slots[tid] = slots_upto - slots;
-  __syncthreads();
-  const uint32_t all_units = __builtin_amdgcn_readfirstlane(all) * items;
 
   struct Unit {
     uint32_t row;
@@ -205,44 +232,44 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   };
   auto locate = [&](uint32_t u) {
     const uint32_t x = u / items;
-    // the first thread whose rows reach past x
-    int t = 0;
-#pragma unroll
-    for (int step = kThreads / 2; step > 0; step /= 2)
-      if (s_units[t + step - 1] <= x) t += step;
-    t = __builtin_amdgcn_readfirstlane(t);
-    uint32_t r = (uint32_t)t * chunk, before = __builtin_amdgcn_readfirstlane(t ? s_units[t - 1] : 0u);
-    uint32_t slots_before = __builtin_amdgcn_readfirstlane(s_slots[t]);
+    uint32_t r, before, slots_before;          // the unit's row, and the units and slots of the rows before it
     Row at;
-    if (chunk == 1) {
-      at = row_of(s_seq[t], 0);
-      at.hi = s_len[t];
+    if (few) {
+      // (rows past the last have the last one's sum, which x is below)
+      r = (uint32_t)__popcll(__ballot(upto <= x));
+      before = (uint32_t)__builtin_amdgcn_readlane((int)(upto - units), (int)r);
+      slots_before = (uint32_t)__builtin_amdgcn_readlane((int)(slots_upto - slots), (int)r);
+      at = row_of(__builtin_amdgcn_readlane(only.seq, (int)r), __builtin_amdgcn_readlane(only.hi, (int)r));
     } else {
-      for (;; ++r) {
+      // the first thread whose rows reach past x: of every fourth, then of four
+      const uint32_t four = (uint32_t)__popcll(__ballot(s_units[4 * lane + 3] <= x)) * 4;
+      const uint32_t t = four + (uint32_t)__popcll(__ballot(lane < 4 && s_units[(four + lane) & (kThreads - 1)] <= x));
+      before = __builtin_amdgcn_readfirstlane(t ? s_units[t - 1] : 0u);
+      slots_before = __builtin_amdgcn_readfirstlane(t ? s_slots[t - 1] : 0u);
+      for (r = t * chunk;; ++r) {
         at = row_at(r);
-        const uint32_t k = (__builtin_amdgcn_readfirstlane(at.tiles) + most - 1) / most;
+        at = row_of(__builtin_amdgcn_readfirstlane(at.seq), __builtin_amdgcn_readfirstlane(at.hi));
+        const uint32_t k = __builtin_amdgcn_readfirstlane(units_of(at.tiles, inv_most));
         if (before + k > x) break;
         before += k;
         slots_before += k > 1 ? k : 0;
       }
     }
-    at.seq = __builtin_amdgcn_readfirstlane(at.seq);
-    at = row_of(at.seq, __builtin_amdgcn_readfirstlane(at.hi));
     Unit y;
     y.row = r;
     y.seq = at.seq;
     y.lo = at.lo;
     y.hi = at.hi;
-    y.parts = (at.tiles + most - 1) / most;
+    y.parts = __builtin_amdgcn_readfirstlane(units_of(at.tiles, inv_most));
     const uint32_t in = u - before * items, item = in / y.parts;
     y.part = in - item * y.parts;
     y.head = (int)(item / splits);
     y.q0 = (int)(item % splits) * 16 * RT;
     y.held = a.group - y.q0 < 16 * RT ? a.group - y.q0 : 16 * RT;
     y.slot = slots_before * items + item * y.parts;
-    // (tiles below 2^25 by parts that are at least 4 tiles long: the products stay inside 64 bits)
-    const uint32_t from = (uint32_t)((uint64_t)at.tiles * y.part / y.parts);
-    const uint32_t len = (uint32_t)((uint64_t)at.tiles * (y.part + 1) / y.parts) - from;
+    // equal parts, the first ones a tile longer
+    const uint32_t base = at.tiles / y.parts, over = at.tiles - base * y.parts;
+    const uint32_t from = base * y.part + (y.part < over ? y.part : over), len = base + (y.part < over ? 1 : 0);
     const int first = at.lo / kTile + (int)from;
     y.t_lo = first + (int)(len * (uint32_t)wave / kAttnWaves);
     y.t_hi = at.hi > at.lo ? first + (int)(len * (uint32_t)(wave + 1) / kAttnWaves) : y.t_lo;
@@ -270,36 +297,43 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   // ---- the unit in work, or the next one
   int head = 0, lo = 0, hi = 0;
   const int32_t* table = a.table;
-  // the page of each run of 16 tokens, and the place in it: 64 runs in the lanes at a time
-  int pages = -1, inside = 0, block = -1;
-  auto look_up = [&](int run) {
-    if (run >> 6 == block) return;
-    block = run >> 6;
-    const uint32_t token = ((uint32_t)block * 64 + (uint32_t)lane) * 16;
-    const uint32_t n = token / (uint32_t)pg;
-    pages = -1;
-    if ((int)token < hi) {
-      const int p = table[n];
-      if (p >= 0 && p < cache.pages) pages = p;
+  // the page of each run of 16 tokens, and the place in it: the 128 runs of kBlock tiles from `block` on, in the lanes
+  int pages[2] = {-1, -1}, inside[2] = {0, 0}, block = 0;
+  auto look_up = [&](int tile) {
+    block = tile;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t own = (uint32_t)tile * 2 + (uint32_t)(h * 64 + lane), token = own * 16;
+      const uint32_t n = (uint32_t)((uint64_t)own * a.page_magic >> a.page_shift);   // own / (page_size / 16)
+      pages[h] = (int)token < hi ? table[n] : -1;
+      inside[h] = (int)(token - n * (uint32_t)pg);
     }
-    inside = (int)(token - n * (uint32_t)pg);
   };
   struct Run {
     int page, inside;
-    int held;                                  // of its 16 tokens, from the first
+    int held;                                  // of its 16 tokens, from the first; 0 past the `end` of the tiles
   };
-  auto run_of = [&](int run) {
-    look_up(run);
-    Run r{__builtin_amdgcn_readlane(pages, run & 63), __builtin_amdgcn_readlane(inside, run & 63), hi - run * 16};
-    r.held = r.page < 0 || r.held < 0 ? 0 : r.held < 16 ? r.held : 16;
-    return r;
+  auto run_of = [&](int tile, int u, int end) {
+    const int at = (tile - block) * 2 + u;
+    const int p0 = __builtin_amdgcn_readlane(pages[0], at & 63), p1 = __builtin_amdgcn_readlane(pages[1], at & 63);
+    const int i0 = __builtin_amdgcn_readlane(inside[0], at & 63), i1 = __builtin_amdgcn_readlane(inside[1], at & 63);
+    const int page = at & 64 ? p1 : p0, left = hi - (tile * 2 + u) * 16;
+    const bool is = page >= 0 && page < cache.pages && tile < end && left > 0;
+    return Run{is ? page : 0, at & 64 ? i1 : i0, is ? (left < 16 ? left : 16) : 0};
   };
+  // (readfirstlane: the compiler counts the bytes in vector registers and then loops over the lanes' descriptors, which are
+  // the same. No tokens: a descriptor of no bytes, whose loads read nothing and give zeros. The loads stand in straight
+  // lines, since behind a branch the compiler waits for all of them where it needs the older half)
   auto descriptor = [&](const void* pool, const Run& r) {
-    const int64_t at = r.held ? (int64_t)r.page * cache.ld_page + (int64_t)r.inside * cache.ld_token +
-                                    (int64_t)head * cache.ld_head : 0;
-    return __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(static_cast<const uint8_t*>(pool)) + at * EL, 0,
-        r.held ? (int)((uint32_t)(r.held - 1) * token_bytes + (uint32_t)(D * EL)) : 0, kBufferFlags);
+    const int64_t at = (int64_t)r.page * cache.ld_page + (int64_t)r.inside * cache.ld_token + (int64_t)head * cache.ld_head;
+    const int bytes = (int)((uint32_t)(r.held - 1) * token_bytes + (uint32_t)(D * EL));
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(static_cast<const uint8_t*>(pool)) + at * EL, 0,
+                                             __builtin_amdgcn_readfirstlane(r.held ? bytes : 0), kBufferFlags);
+  };
+  auto load_scales = [&](const float* scales, const Run& r) {
+    const __amdgpu_buffer_rsrc_t d = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(scales) + ((int64_t)r.page * cache.kv_heads + head) * pg + r.inside, 0, r.held ? 64 : 0, kBufferFlags);
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(d, 16 * g, 0, 0));
   };
 
   struct Keys {
@@ -311,27 +345,22 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
     uint32_t v[2][4][VW];
     f32x4 scale[2];
   };
-  auto load_keys = [&](Keys& x, int tile) {
+  auto load_keys = [&](Keys& x, int tile, int end) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const Run r = run_of(2 * tile + u);
+      const Run r = run_of(tile, u, end);
       x.held[u] = r.held;
       const __amdgpu_buffer_rsrc_t d = descriptor(cache.k, r);
 #pragma unroll
       for (int i = 0; i < KL; ++i)
         x.k[u][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(d, (int)koff[i], 0, 0));
-      if constexpr (FP8) {
-        x.scale[u] = f32x4{};
-        if (r.held)
-          x.scale[u] = *reinterpret_cast<const f32x4*>(
-              cache.k_scale + ((int64_t)r.page * cache.kv_heads + head) * pg + r.inside + 4 * g);
-      }
+      if constexpr (FP8) x.scale[u] = load_scales(cache.k_scale, r);
     }
   };
-  auto load_values = [&](Values& x, int tile) {
+  auto load_values = [&](Values& x, int tile, int end) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const Run r = run_of(2 * tile + u);
+      const Run r = run_of(tile, u, end);
       const __amdgpu_buffer_rsrc_t d = descriptor(cache.v, r);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -355,12 +384,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
           }
         }
       }
-      if constexpr (FP8) {
-        x.scale[u] = f32x4{};
-        if (r.held)
-          x.scale[u] = *reinterpret_cast<const f32x4*>(
-              cache.v_scale + ((int64_t)r.page * cache.kv_heads + head) * pg + r.inside + 4 * g);
-      }
+      if constexpr (FP8) x.scale[u] = load_scales(cache.v_scale, r);
     }
   };
 
@@ -372,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
     lo = u.lo;
     hi = u.hi;
     table = a.table + (hi > 0 ? u.seq * a.ld_table : 0);
-    block = -1;
+    look_up(u.t_lo);                           // (before Q: its wait is a wait for what was asked for earlier too)
     // Q: column c, steps of 32 channels; lane's 8 of step s as K's lane has them
     const uint16_t* const q = a.q + (int64_t)u.row * a.ld_q + (int64_t)(head * a.group + u.q0) * D;
 #pragma unroll
@@ -384,17 +408,21 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
         qf[r][s] = u32x4{};
         if (j < u.held && d < D) qf[r][s] = *reinterpret_cast<const u32x4*>(q + j * D + d);
       }
-    if (u.t_lo < u.t_hi) {
-      load_keys(kx, u.t_lo);
-      load_values(vx, u.t_lo);
-    }
+    load_keys(kx, u.t_lo, u.t_hi);
+    load_values(vx, u.t_lo, u.t_hi);
   };
 
+  // ---- the first unit by the workgroup's number; of further ones, where there are more units than workgroups, the
+  // next that nobody has (asked for while a unit is in work)
   uint32_t number = blockIdx.x;
   if (number >= all_units) return;
+  const bool claims = all_units > grid;
+  uint32_t* const claimed = a.counts + 8 * grid;
   Unit now = locate(number);
   begin(now);
   for (;;) {
+  uint32_t claim = 0;
+  if (claims && tid == 0) claim = grid + __hip_atomic_fetch_add(claimed, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   f32x4 o[RT][VE];
   float m[RT], l[RT];
 #pragma unroll
@@ -404,7 +432,14 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
 #pragma unroll
     for (int e = 0; e < VE; ++e) o[r][e] = f32x4{};
   }
-  for (int tile = now.t_lo; tile < now.t_hi; ++tile) {
+  for (int from = now.t_lo; from < now.t_hi; from += kBlock) {
+  if (from > now.t_lo) {
+    look_up(from);
+    load_keys(kx, from, now.t_hi);
+    load_values(vx, from, now.t_hi);
+  }
+  const int to = now.t_hi - from < kBlock ? now.t_hi : from + kBlock;
+  for (int tile = from; tile < to; ++tile) {
     // ---- S^T, times the scale and in powers of 2
     f32x4 s[RT][2];
 #pragma unroll
@@ -432,8 +467,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
       for (int i = 0; i < 4; ++i)
         in[u][i] = 4 * g + i < kx.held[u] && tile * kTile + u * 16 + 4 * g + i >= lo;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float top = -INFINITY;
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -441,10 +475,19 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
           float x = s[r][u][i] * a.scale2;
           if constexpr (FP8) x *= kx.scale[u][i];
           s[r][u][i] = in[u][i] ? x : -INFINITY;
-          top = fmaxf(top, s[r][u][i]);
         }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
+    // (the scheduling barriers keep the loads where they stand: the compiler otherwise moves them to the loop's end)
+    __builtin_amdgcn_sched_barrier(0);
+    load_keys(kx, tile + 1, to);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[r][u][i]);
+      top = over_rows(top, [](float x, float y) { return fmaxf(x, y); });
       const float now = fmaxf(m[r], top);
       const float base = now == -INFINITY ? 0.0f : now;   // (nothing so far)
       const float shrink = __builtin_amdgcn_exp2f(m[r] - base);
@@ -461,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
           if constexpr (FP8) s[r][u][i] = in[u][i] ? s[r][u][i] * vx.scale[u][i] : 0.0f;
         }
     }
-    if (tile + 1 < now.t_hi) load_keys(kx, tile + 1);
     // ---- O^T
     u32x4 w[RT][PARTS];
 #pragma unroll
@@ -503,13 +545,22 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
           o[r][e + 1] = mfma16(f1, w[r][t], o[r][e + 1]);
         }
     }
-    if (tile + 1 < now.t_hi) load_values(vx, tile + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    load_values(vx, tile + 1, to);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   }
 
   // ---- the waves' results, 16 queries at a time
   const Unit done = now;
-  number += grid;
-  const bool more = number < all_units;
+  bool more = false;
+  __syncthreads();                             // (everyone is past the last unit's s_o, s_m, s_l and s_last)
+  if (claims) {
+    if (tid == 0) s_next = claim;
+    __syncthreads();
+    number = __builtin_amdgcn_readfirstlane(s_next);
+    more = number < all_units;
+  }
   if (more) {
     now = locate(number);
     begin(now);
@@ -535,10 +586,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     if (r * 16 >= done.held) break;
-    float sum = l[r];
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    __syncthreads();
+    const float sum = over_rows(l[r], [](float x, float y) { return x + y; });
+    if (r > 0) __syncthreads();
     if (g == 0) {
       s_m[wave][c] = m[r];
       s_l[wave][c] = sum;
@@ -598,7 +647,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
         const int j = in ? x / quads : 0, d = in ? x % quads * 4 : 0;
         float top = -INFINITY, sum = 0.0f;
         f32x4 y = f32x4{};
-        constexpr int B = 8;
+        auto take = [&](auto batch) {
+        constexpr int B = decltype(batch)::value;
         for (uint32_t i0 = sub; i0 < n; i0 += B * stride) {
           f32x4 v[B];
           f32x2 ms[B];
@@ -627,6 +677,10 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
             y += by * v[b];
           }
         }
+        };
+        // (as many loads in flight as there are registers; few where few are enough)
+        if (n <= 4 * stride) take(std::integral_constant<int, 4>{});
+        else take(std::integral_constant<int, RT == 1 && DP <= 128 ? 16 : 8>{});
         for (uint32_t s = 1; s < stride; s *= 2) {
           const float other = __shfl_xor(top, (int)s);
           const float both = fmaxf(top, other), base = both == -INFINITY ? 0.0f : both;
@@ -654,8 +708,13 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
       }
     }
   }
-  if (!more) return;
-  __syncthreads();                             // (the next unit writes s_o, s_m, s_l and s_last again)
+  if (!more) break;
+  }
+  if (!claims) return;
+  // the last workgroup to end leaves the counters at zero (all claims came before)
+  if (tid == 0 && __hip_atomic_fetch_add(claimed + 1, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == grid - 1) {
+    __hip_atomic_store(claimed, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(claimed + 1, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 

@@ -81,9 +81,16 @@ extern "C" int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows,
   const int tiles = group <= 16 ? 1 : group <= 32 || most == 2 ? 2 : 4;
   AttnArgs a{without_idle_strides(*cache), static_cast<const uint16_t*>(q), out, lse, lens, row_seq, table, seqs,
              seq_pages, ld_table, rows, 0, ld_q, ld_out, window, scale * 1.442695041f, q_heads, group, tiles,
-             out_dtype == AGG_FP32, kAttnLeast, nullptr, 0, 0, nullptr};
+             out_dtype == AGG_FP32, kAttnLeast, nullptr, 0, 0, nullptr, 0, 0};
+  // runs of 16 tokens to pages: with 2^s <= d < 2^(s+1) and magic = ceil(2^(31+s) / d), magic * d is less than d above
+  // 2^(31+s), so x * magic >> (31+s) is x / d while x * 2^(s+1) stays below 2^(31+s)
+  const uint32_t d = uint32_t(cache->page_size) / 16;
+  int s = 0;
+  while (d >> (s + 1)) ++s;
+  a.page_magic = uint32_t(((uint64_t(1) << (31 + s)) + d - 1) / d);
+  a.page_shift = uint32_t(31 + s);
   // the grid: what the compute units hold at once; and the workspace of its units
-  const int units = ctx_units(ctx) < kMoeCounters / 16 ? ctx_units(ctx) : kMoeCounters / 16;
+  const int units = ctx_units(ctx) < kWsCounters / 17 ? ctx_units(ctx) : kWsCounters / 17;
   const int grid = units * (tiles == 1 && cache->head_dim <= 128 ? 2 : 1);
   const int queries = group < 16 * tiles ? group : 16 * tiles;
   a.slot_bytes = (queries * (cache->head_dim + 4) * 4 + 15) / 16 * 16;

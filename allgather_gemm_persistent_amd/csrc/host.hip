@@ -94,7 +94,7 @@ struct StaticScratch {
 std::mutex g_static_mu;
 StaticScratch g_static[kMaxDevices];
 
-// A workspace of a split (moe_gemm's and linear's K, paged_attn's length): kMoeCounters counters, then `bytes` for
+// A workspace of a split (moe_gemm's and linear's K, paged_attn's length): kWsCounters counters, then `bytes` for
 // partial results.
 struct MoeWorkspace {
   uint8_t* mem;
@@ -799,7 +799,7 @@ int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws,
   MoeWorkspace* w = ctx->moe_ws;
   while (w && !(w->stream == s && w->captured == captured && w->capture == capture && w->bytes >= bytes)) w = w->next;
   if (!w) {
-    constexpr size_t kCounterBytes = size_t(kMoeCounters) * sizeof(uint32_t);
+    constexpr size_t kCounterBytes = size_t(kWsCounters) * sizeof(uint32_t);
     // (an eager call's is there for later, larger calls too: powers of two)
     size_t room = captured ? (bytes + 65535) / 65536 * 65536 : size_t(kMoeWsBytes);
     while (room < bytes) room *= 2;
@@ -813,7 +813,7 @@ int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws,
     if (enter == hipSuccess) (void)hipThreadExchangeStreamCaptureMode(&mode);
     // the counters are cleared on the call's own stream: by a graph, at every replay
     if (e == hipSuccess) {
-      e = launch_fill_u32(reinterpret_cast<uint32_t*>(w->mem), kMoeCounters, 0u, s);
+      e = launch_fill_u32(reinterpret_cast<uint32_t*>(w->mem), kWsCounters, 0u, s);
       if (e != hipSuccess) (void)hipFree(w->mem);
     }
     if (e != hipSuccess) {
@@ -823,7 +823,7 @@ int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws,
     ctx->moe_ws = w;
   }
   *counts = reinterpret_cast<uint32_t*>(w->mem);
-  *ws = reinterpret_cast<float*>(w->mem + size_t(kMoeCounters) * sizeof(uint32_t));
+  *ws = reinterpret_cast<float*>(w->mem + size_t(kWsCounters) * sizeof(uint32_t));
   return AGG_OK;
 }
 
@@ -880,7 +880,7 @@ extern "C" int agg_ctx_reset(agg_ctx* ctx, agg_stream stream) {
   HIP_TRY(launch_fill_u32(ctx->scratch, kScrWords, 0u, S(stream)));
   HIP_TRY(launch_fill_u32(ctx->scratch + kScrFailed, 1, 0xFFFFFFFFu, S(stream)));
   for (MoeWorkspace* w = ctx->moe_ws; w; w = w->next)
-    HIP_TRY(launch_fill_u32(reinterpret_cast<uint32_t*>(w->mem), kMoeCounters, 0u, S(stream)));
+    HIP_TRY(launch_fill_u32(reinterpret_cast<uint32_t*>(w->mem), kWsCounters, 0u, S(stream)));
   if (ctx->used_static) {
     // the device's static scratch too (shared by every ctx on the device)
     std::lock_guard<std::mutex> lock(g_static_mu);

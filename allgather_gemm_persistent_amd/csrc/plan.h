@@ -84,11 +84,13 @@ int ctx_device(const agg_ctx* ctx);
 TileShape ctx_forced_tile(const agg_ctx* ctx);
 
 // The workspace of a split (moe_gemm's and linear's K: at most kMoeWsBytes, a counter for every strip of every
-// expert; paged_attn's length: eight counters for every workgroup) for calls on `stream`, with room for `bytes`
-// of partial results, and kMoeCounters counters that are zero when a call starts and when it ends. Every stream
-// has one of its own, and every capture on it, so calls that are not ordered do not meet. Returns an AGG_E_* code.
+// expert, kMoeCounters at most; paged_attn's length: eight counters for every workgroup and two) for calls on
+// `stream`, with room for `bytes` of partial results, and kWsCounters counters that are zero when a call starts and
+// when it ends. Every stream has one of its own, and every capture on it, so calls that are not ordered do not
+// meet. Returns an AGG_E_* code.
 constexpr int64_t kMoeWsBytes = int64_t(8) << 20;
 constexpr int kMoeCounters = 4096;
+constexpr int kWsCounters = 8192;
 int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws, uint32_t** counts);
 
 // How moe_gemm multiplies: stream: strips of the output's columns with K in ksplit parts; otherwise
