@@ -9,9 +9,9 @@ namespace agg {
 // Where the tokens of a call lie in a cache.
 struct PlaceArgs {
   const int32_t* positions;
-  const int32_t* token_seq;   // or null: token t is sequence t
+  const int32_t* token_seq;   // or null: token t is sequence first + t
   const int32_t* table;       // seqs x seq_pages
-  int64_t seqs, seq_pages, ld_table;
+  int64_t seqs, seq_pages, ld_table, first;
 };
 
 struct KvWriteArgs {

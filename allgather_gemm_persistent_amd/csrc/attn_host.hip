@@ -43,7 +43,7 @@ extern "C" int kv_write(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens,
   if (int rc = enter(ctx)) return rc;
   // (no sequence, page or table: no token has a place)
   if (tokens == 0 || seqs == 0 || seq_pages == 0 || cache->pages == 0) return AGG_OK;
-  const KvWriteArgs a{without_idle_strides(*cache), {positions, token_seq, table, seqs, seq_pages, ld_table},
+  const KvWriteArgs a{without_idle_strides(*cache), {positions, token_seq, table, seqs, seq_pages, ld_table, 0},
                       static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                       static_cast<uint16_t*>(q_out), ld_q, ld_q_out, ld_k, ld_v, rope, tokens, rope_rows, q_heads,
                       rope_dim, rope_pairs};
@@ -59,7 +59,7 @@ extern "C" int kv_read(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens, 
     return rc;
   if (int rc = enter(ctx)) return rc;
   if (tokens == 0) return AGG_OK;
-  const KvReadArgs a{without_idle_strides(*cache), {positions, token_seq, table, seqs, seq_pages, ld_table}, k_out, v_out,
+  const KvReadArgs a{without_idle_strides(*cache), {positions, token_seq, table, seqs, seq_pages, ld_table, 0}, k_out, v_out,
                      ld_k, ld_v, tokens, out_dtype == AGG_FP32};
   HIP_TRY(launch_kv_read(a, ctx_units(ctx), S(stream)));
   return AGG_OK;

@@ -1,5 +1,7 @@
 // The paged cache's row operators, bound by memory: the rotation of queries and keys with the write of
 // keys and values (kv_write), and the rows read back (kv_read).
+#include <type_traits>
+
 #include "attn.h"
 #include "convert.h"
 
@@ -14,7 +16,7 @@ struct Place {
 
 __device__ inline Place place_of(const PlaceArgs& a, const agg_kv_cache& c, int64_t t) {
   const int p = a.positions[t];
-  const int s = a.token_seq ? a.token_seq[t] : (int)t;
+  const int s = a.token_seq ? a.token_seq[t] : (int)(a.first + t);
   Place r{-1, 0, p};
   if (p < 0 || s < 0 || s >= a.seqs) return r;
   const uint32_t n = (uint32_t)p / (uint32_t)c.page_size;
@@ -25,6 +27,20 @@ __device__ inline Place place_of(const PlaceArgs& a, const agg_kv_cache& c, int6
   return r;
 }
 
+// the largest over a group of 2^lanes_log2 lanes (1 to 16 of them)
+__device__ inline uint32_t group_max(uint32_t m, int lanes_log2) {
+  auto with = [&](auto ctrl) {
+    const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, decltype(ctrl)::value, 0xF, 0xF, true);
+    m = b > m ? b : m;
+  };
+  using std::integral_constant;
+  if (lanes_log2 > 0) with(integral_constant<int, 0xB1>{});    // lanes 1 0 3 2 of each four
+  if (lanes_log2 > 1) with(integral_constant<int, 0x4E>{});    // lanes 2 3 0 1
+  if (lanes_log2 > 2) with(integral_constant<int, 0x141>{});   // eight lanes mirrored
+  if (lanes_log2 > 3) with(integral_constant<int, 0x140>{});   // sixteen mirrored
+  return m;
+}
+
 // element `d` of head `h` at a place
 __device__ inline int64_t element(const agg_kv_cache& c, const Place& at, int h, int d) {
   return at.page * c.ld_page + at.off * c.ld_token + h * c.ld_head + d;
@@ -32,187 +48,283 @@ __device__ inline int64_t element(const agg_kv_cache& c, const Place& at, int h,
 
 }  // namespace
 
-// A row is one head of one token: a query's, a key's or a value's. It is taken by a group of 2^group_log2
-// lanes of a wave, a chunk of 8 channels each. A channel that turns has its partner in the same
-// chunk (pairs) or in the chunk rope_dim / 16 further (halves), which the lane reads as well: from
-// the cache that its neighbour's read fills. Sums of the rotation and the largest element of a row are fp32;
-// each stored value is rounded once.
+// How a workgroup's threads stand: groups of 2^lanes_log2 lanes, 2^heads_log2 groups to a token, and the other
+// tokens after it. A group takes heads first, first + 2^heads_log2, ... of its token, kAhead at a time with all their loads
+// ahead of the first use.
+struct Deal {
+  int lanes_log2, heads_log2;
+};
+constexpr int kAhead = 4;
+
+// A row is one head of one token: a query's, a key's or a value's. A lane of its group takes two chunks of 8 channels,
+// those that turn together where they do (channel i and i + rope_dim / 2 in chunks rope_dim / 16 apart), so nothing is
+// read twice or passed between lanes, and the angles are read once for all of a token's heads. The
+// rotation and the largest element of a row are fp32; each stored value is rounded once.
+//
+// Bound by memory: 8192 tokens of 64 + 8 + 8 heads of 128 into 8 bits (322 MB) take 60 us, 5.4 TB/s, where a large copy
+// reaches 5.1; a lane with one chunk of one head, its partner's read beside it, took 100. 16 such tokens: 3.6 us, a
+// launch and three round trips to memory (position, page, row).
 template <bool FP8>
-__global__ void __launch_bounds__(256) kv_write_kernel(const KvWriteArgs a, int64_t first, uint32_t rows,
-                                                       int group_log2) {
-  const int lane = threadIdx.x & ((1 << group_log2) - 1);
-  const uint32_t per_block = 256u >> group_log2;
+__global__ void __launch_bounds__(256) kv_write_kernel(const KvWriteArgs a, const Deal deal) {
   const agg_kv_cache& c = a.cache;
-  const uint32_t heads = (uint32_t)(a.q_heads + 2 * c.kv_heads);
-  const int d = lane * 8;
-  const bool in = d < c.head_dim;
-  for (uint32_t r = blockIdx.x * per_block + (threadIdx.x >> group_log2); r < rows; r += gridDim.x * per_block) {
-    const int64_t t = first + r / heads;
-    const int head = (int)(r % heads);
-    const Place at = place_of(a.at, c, t);
-    if (at.page < 0 || (a.rope && at.position >= a.rope_rows)) continue;
-    // 0: a query, 1: a key, 2: a value
-    const int kind = head < a.q_heads ? 0 : head < a.q_heads + c.kv_heads ? 1 : 2;
-    const int h = kind == 0 ? head : kind == 1 ? head - a.q_heads : head - a.q_heads - c.kv_heads;
-    const uint16_t* const src = (kind == 0 ? a.q + t * a.ld_q : kind == 1 ? a.k + t * a.ld_k : a.v + t * a.ld_v) +
-                                (int64_t)h * c.head_dim;
-    float x[8] = {};
-    if (in) widen(*reinterpret_cast<const u32x4*>(src + d), x);
-    if (kind < 2 && d < a.rope_dim) {
-      const float* const cosines = a.rope + (int64_t)at.position * a.rope_dim;
-      const float* const sines = cosines + a.rope_dim / 2;
-      if (a.pairs) {
+  const int D = c.head_dim, lane = threadIdx.x & ((1 << deal.lanes_log2) - 1), group = threadIdx.x >> deal.lanes_log2;
+  const int64_t t = (int64_t)blockIdx.x * (256 >> (deal.lanes_log2 + deal.heads_log2)) + (group >> deal.heads_log2);
+  if (t >= a.tokens) return;
+  const Place at = place_of(a.at, c, t);
+  if (at.page < 0 || (a.rope && at.position >= a.rope_rows)) return;
+  // this lane's chunks
+  const int turning = a.rope_dim / 16;                     // lanes whose channels turn
+  const bool in = lane * 16 < D, halves = lane < turning && !a.pairs;
+  const int d0 = halves ? lane * 8 : lane * 16, d1 = halves ? d0 + a.rope_dim / 2 : d0 + 8;
+  // their angles: halves: 8 of both chunks; pairs: 4 of each
+  float cs[8], sn[8];
+  if (lane < turning) {
+    const float* const p = a.rope + (int64_t)at.position * a.rope_dim + lane * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float cs = cosines[d / 2 + i], sn = sines[d / 2 + i], u = x[2 * i], w = x[2 * i + 1];
-          x[2 * i] = u * cs - w * sn;
-          x[2 * i + 1] = w * cs + u * sn;
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 x = reinterpret_cast<const f32x4*>(p)[i], y = reinterpret_cast<const f32x4*>(p + a.rope_dim / 2)[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        cs[4 * i + e] = x[e];
+        sn[4 * i + e] = y[e];
+      }
+    }
+  }
+  const int heads = a.q_heads + 2 * c.kv_heads, step = 1 << deal.heads_log2;
+  for (int h0 = group & (step - 1); h0 < heads; h0 += kAhead * step) {
+    u32x4 w[kAhead][2];
+    // (past the last head or channel: nothing is read)
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int head = h0 + u * step;
+      const uint16_t* const src = head < a.q_heads              ? a.q + t * a.ld_q + (int64_t)head * D
+                                  : head < a.q_heads + c.kv_heads ? a.k + t * a.ld_k + (int64_t)(head - a.q_heads) * D
+                                                                : a.v + t * a.ld_v + (int64_t)(head - a.q_heads - c.kv_heads) * D;
+      w[u][0] = w[u][1] = u32x4{};
+      if (in && head < heads) {
+        w[u][0] = *reinterpret_cast<const u32x4*>(src + d0);
+        w[u][1] = *reinterpret_cast<const u32x4*>(src + d1);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int head = h0 + u * step;
+      if (head >= heads) break;
+      float x[2][8];
+      widen(w[u][0], x[0]);
+      widen(w[u][1], x[1]);
+      if (lane < turning && head < a.q_heads + c.kv_heads) {
+        if (a.pairs) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float &p = x[i >> 2][2 * (i & 3)], &q = x[i >> 2][2 * (i & 3) + 1];
+            const float v = p * cs[i] - q * sn[i];
+            q = q * cs[i] + p * sn[i];
+            p = v;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float v = x[0][i] * cs[i] - x[1][i] * sn[i];
+            x[1][i] = x[1][i] * cs[i] + x[0][i] * sn[i];
+            x[0][i] = v;
+          }
+        }
+      }
+      if (head < a.q_heads) {
+        uint16_t* const to = a.q_out + t * a.ld_q_out + (int64_t)head * D;
+        if (in) {
+          *reinterpret_cast<u32x4*>(to + d0) = narrow(x[0]);
+          *reinterpret_cast<u32x4*>(to + d1) = narrow(x[1]);
+        }
+        continue;
+      }
+      const bool key = head < a.q_heads + c.kv_heads;
+      const int h = key ? head - a.q_heads : head - a.q_heads - c.kv_heads;
+      void* const pool = key ? c.k : c.v;
+      const int64_t to = element(c, at, h, 0);
+      if constexpr (!FP8) {
+        if (in) {
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(pool) + to + d0) = narrow(x[0]);
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(pool) + to + d1) = narrow(x[1]);
         }
       } else {
-        const int half = a.rope_dim / 2;
-        const bool low = d < half;
-        const int angle = low ? d : d - half;
-        float other[8];
-        widen(*reinterpret_cast<const u32x4*>(src + (low ? d + half : d - half)), other);
+        // the largest element by its bit pattern: a NaN is larger than every number and is kept
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float cs = cosines[angle + i], sn = sines[angle + i];
-          x[i] = low ? x[i] * cs - other[i] * sn : x[i] * cs + other[i] * sn;
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t b = __builtin_bit_cast(uint32_t, x[i >> 3][i & 7]) & 0x7FFFFFFFu;
+          m = b > m ? b : m;
         }
-      }
-    }
-    if (kind == 0) {
-      if (in) *reinterpret_cast<u32x4*>(a.q_out + t * a.ld_q_out + (int64_t)h * c.head_dim + d) = narrow(x);
-      continue;
-    }
-    void* const pool = kind == 1 ? c.k : c.v;
-    const int64_t to = element(c, at, h, d);
-    if constexpr (!FP8) {
-      if (in) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(pool) + to) = narrow(x);
-    } else {
-      // the largest element by its bit pattern: a NaN is larger than every number and is kept
-      uint32_t m = 0;
+        m = group_max(m, deal.lanes_log2);
+        const float top = __builtin_bit_cast(float, m) / 448.0f;
+        const float scale = top > 0.0f ? top : 1.0f;        // a row of zeros, or with a NaN: 1
+        // (one reciprocal a row: it and the division differ by a unit of fp32 at most, far below e4m3's. A
+        // scale so small that the reciprocal overflows divides; a subnormal one can be a third below
+        // max|x| / 448, and the 1 of a row with a NaN has nothing to do with the others: these clamp)
+        const bool usual = top >= kNormal;
+        const float by = 1.0f / scale;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu;
-        m = b > m ? b : m;
+        for (int i = 0; i < 16; ++i) {
+          float& v = x[i >> 3][i & 7];
+          v = scale >= kNormal ? v * by : v / scale;
+          if (!usual) v = clamp_e4m3(v);
+        }
+        if (in) {
+          *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(pool) + to + d0) = narrow_e4m3(x[0]);
+          *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(pool) + to + d1) = narrow_e4m3(x[1]);
+        }
+        if (lane == 0) (key ? c.k_scale : c.v_scale)[((int64_t)at.page * c.kv_heads + h) * c.page_size + at.off] = scale;
       }
-      for (int s = 1 << group_log2 >> 1; s > 0; s >>= 1) {
-        const uint32_t b = (uint32_t)__shfl_xor((int)m, s);
-        m = b > m ? b : m;
-      }
-      const float top = __builtin_bit_cast(float, m) / 448.0f;
-      const float scale = top > 0.0f ? top : 1.0f;          // a row of zeros, or with a NaN: 1
-      // (one reciprocal a row: it and the division differ by a unit of fp32 at most, far below e4m3's. A
-      // scale so small that the reciprocal overflows divides; a subnormal one can be a third below
-      // max|x| / 448, and the 1 of a row with a NaN has nothing to do with the others: these clamp)
-      const bool small = !(scale >= kNormal);
-      const float by = 1.0f / scale;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = small ? x[i] / scale : x[i] * by;
-        if (!(top >= kNormal)) x[i] = clamp_e4m3(x[i]);
-      }
-      if (in) *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(pool) + to) = narrow_e4m3(x);
-      if (lane == 0)
-        (kind == 1 ? c.k_scale : c.v_scale)[((int64_t)at.page * c.kv_heads + h) * c.page_size + at.off] = scale;
     }
   }
 }
 
-// A row is one head of one token, of the keys or of the values; a lane takes a chunk of 8 channels.
+// A row is one head of one token, of the keys or of the values; a lane of its group takes two chunks of 8 channels.
+// Bound by memory: 65536 tokens of 8 heads of 64 bf16 (269 MB) take 55 us, 4.9 TB/s (one chunk a lane: 60), 4951 of 8
+// heads of 128 from 8 bits (31 MB) 8.4.
 template <bool FP8, bool OUT32>
-__global__ void __launch_bounds__(256) kv_read_kernel(const KvReadArgs a, int64_t first, uint32_t rows,
-                                                      int group_log2) {
-  const int lane = threadIdx.x & ((1 << group_log2) - 1);
-  const uint32_t per_block = 256u >> group_log2;
+__global__ void __launch_bounds__(256) kv_read_kernel(const KvReadArgs a, const Deal deal) {
   const agg_kv_cache& c = a.cache;
-  const uint32_t heads = (uint32_t)(2 * c.kv_heads);
-  const int d = lane * 8;
-  if (d >= c.head_dim) return;
-  for (uint32_t r = blockIdx.x * per_block + (threadIdx.x >> group_log2); r < rows; r += gridDim.x * per_block) {
-    const int64_t t = first + r / heads;
-    const int head = (int)(r % heads);
-    const bool key = head < c.kv_heads;
-    const int h = key ? head : head - c.kv_heads;
-    const Place at = place_of(a.at, c, t);
-    float x[8] = {};
-    if (at.page >= 0) {
-      const void* const pool = key ? c.k : c.v;
-      const int64_t from = element(c, at, h, d);
-      if constexpr (FP8) {
-        const u32x2 p = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(pool) + from);
-        const float scale = (key ? c.k_scale : c.v_scale)[((int64_t)at.page * c.kv_heads + h) * c.page_size + at.off];
+  const int D = c.head_dim, lane = threadIdx.x & ((1 << deal.lanes_log2) - 1), group = threadIdx.x >> deal.lanes_log2;
+  const int64_t t = (int64_t)blockIdx.x * (256 >> (deal.lanes_log2 + deal.heads_log2)) + (group >> deal.heads_log2);
+  const int d = lane * 16;
+  if (t >= a.tokens || d >= D) return;
+  const Place at = place_of(a.at, c, t);
+  const int heads = 2 * c.kv_heads, step = 1 << deal.heads_log2;
+  for (int h0 = group & (step - 1); h0 < heads; h0 += kAhead * step) {
+    u32x4 w[kAhead][FP8 ? 1 : 2];
+    float scale[kAhead];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)p[i], false);
-          const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)p[i], true);
-          x[4 * i] = lo[0] * scale;
-          x[4 * i + 1] = lo[1] * scale;
-          x[4 * i + 2] = hi[0] * scale;
-          x[4 * i + 3] = hi[1] * scale;
+    for (int u = 0; u < kAhead; ++u) {
+      const int head = h0 + u * step;
+      const bool key = head < c.kv_heads;
+      const int h = key ? head : head - c.kv_heads;
+      scale[u] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < (FP8 ? 1 : 2); ++i) w[u][i] = u32x4{};
+      if (head < heads && at.page >= 0) {
+        const int64_t from = element(c, at, h, d);
+        const void* const pool = key ? c.k : c.v;
+        if constexpr (FP8) {
+          w[u][0] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(pool) + from);
+          scale[u] = (key ? c.k_scale : c.v_scale)[((int64_t)at.page * c.kv_heads + h) * c.page_size + at.off];
+        } else {
+          w[u][0] = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(pool) + from)[0];
+          w[u][1] = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(pool) + from)[1];
         }
-      } else {
-        widen(*reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(pool) + from), x);
       }
     }
-    const int64_t to = t * (key ? a.ld_k : a.ld_v) + (int64_t)h * c.head_dim + d;
-    void* const out = key ? a.k : a.v;
-    if constexpr (OUT32) {
-      f32x4* const p = reinterpret_cast<f32x4*>(static_cast<float*>(out) + to);
-      p[0] = f32x4{x[0], x[1], x[2], x[3]};
-      p[1] = f32x4{x[4], x[5], x[6], x[7]};
-    } else {
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + to) = narrow(x);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int head = h0 + u * step;
+      if (head >= heads) break;
+      const bool key = head < c.kv_heads;
+      const int h = key ? head : head - c.kv_heads;
+      const int64_t to = t * (key ? a.ld_k : a.ld_v) + (int64_t)h * D + d;
+      void* const out = key ? a.k : a.v;
+      if constexpr (!FP8 && !OUT32) {
+        reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + to)[0] = w[u][0];
+        reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + to)[1] = w[u][1];
+        continue;
+      }
+      float x[2][8];
+      if constexpr (FP8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u][0][i], false);
+          const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u][0][i], true);
+          float* const p = &x[i >> 1][4 * (i & 1)];
+          p[0] = lo[0] * scale[u];
+          p[1] = lo[1] * scale[u];
+          p[2] = hi[0] * scale[u];
+          p[3] = hi[1] * scale[u];
+        }
+      } else {
+        widen(w[u][0], x[0]);
+        widen(w[u][FP8 ? 0 : 1], x[1]);
+      }
+      if constexpr (OUT32) {
+        f32x4* const p = reinterpret_cast<f32x4*>(static_cast<float*>(out) + to);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = f32x4{x[i >> 1][4 * (i & 1)], x[i >> 1][4 * (i & 1) + 1], x[i >> 1][4 * (i & 1) + 2], x[i >> 1][4 * (i & 1) + 3]};
+      } else {
+        reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + to)[0] = narrow(x[0]);
+        reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + to)[1] = narrow(x[1]);
+      }
     }
   }
 }
 
 namespace {
 
-// lanes of a row of `d` channels, as a power of two
-int group_of(int d) {
-  int g = 1;
-  while ((8 << g) < d) ++g;
-  return g;
+// The deal of `heads` rows a token of `d` channels: a group takes several heads where tokens enough are left to fill the
+// GPU (their places and angles are then read less often).
+Deal deal_of(int64_t tokens, int heads, int d, int cus) {
+  Deal r{0, 0};
+  while ((16 << r.lanes_log2) < d) ++r.lanes_log2;
+  const int groups_log2 = 8 - r.lanes_log2;
+  while (r.heads_log2 < groups_log2 && (1 << r.heads_log2) < heads &&
+         ((kAhead << r.heads_log2) < heads || (tokens << (r.lanes_log2 + r.heads_log2)) < int64_t(cus) * 1024))
+    ++r.heads_log2;
+  return r;
 }
 
-// `go(first token, rows, blocks)` for every launch: a launch counts its rows in 32 bits
-template <typename F>
-hipError_t in_launches(int64_t tokens, int64_t heads, int group_log2, int cus, F go) {
-  const int64_t most = (int64_t(1) << 30) / heads;
-  for (int64_t t = 0; t < tokens; t += most) {
-    const int64_t rows = (tokens - t < most ? tokens - t : most) * heads;
-    const int64_t per_block = 256 >> group_log2, blocks = (rows + per_block - 1) / per_block;
-    const int64_t grid = blocks < int64_t(cus) * 64 ? blocks : int64_t(cus) * 64;
-    go(t, (uint32_t)rows, (unsigned)grid);
+unsigned blocks_of(int64_t tokens, const Deal& d) {
+  const int64_t each = 256 >> (d.lanes_log2 + d.heads_log2);
+  return (unsigned)((tokens + each - 1) / each);
+}
+
+// (a launch holds fewer than 2^32 threads)
+constexpr int64_t kMostTokens = int64_t(1) << 23;
+
+PlaceArgs after(const PlaceArgs& a, int64_t t) {
+  PlaceArgs r = a;
+  r.positions += t;
+  if (r.token_seq) r.token_seq += t;
+  r.first += t;
+  return r;
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(const KvWriteArgs& all, int cus, hipStream_t stream) {
+  for (int64_t t = 0; t < all.tokens; t += kMostTokens) {
+    KvWriteArgs a = all;
+    a.tokens = all.tokens - t < kMostTokens ? all.tokens - t : kMostTokens;
+    a.at = after(all.at, t);
+    a.q += t * a.ld_q;
+    a.q_out += t * a.ld_q_out;
+    a.k += t * a.ld_k;
+    a.v += t * a.ld_v;
+    const Deal d = deal_of(a.tokens, a.q_heads + 2 * a.cache.kv_heads, a.cache.head_dim, cus);
+    const dim3 grid(blocks_of(a.tokens, d)), block(256);
+    if (a.cache.dtype == AGG_FP8_E4M3) hipLaunchKernelGGL(kv_write_kernel<true>, grid, block, 0, stream, a, d);
+    else hipLaunchKernelGGL(kv_write_kernel<false>, grid, block, 0, stream, a, d);
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
 }
 
-}  // namespace
-
-hipError_t launch_kv_write(const KvWriteArgs& a, int cus, hipStream_t stream) {
-  const int g = group_of(a.cache.head_dim);
-  return in_launches(a.tokens, a.q_heads + 2 * a.cache.kv_heads, g, cus, [&](int64_t t, uint32_t rows, unsigned grid) {
-    if (a.cache.dtype == AGG_FP8_E4M3) hipLaunchKernelGGL(kv_write_kernel<true>, dim3(grid), dim3(256), 0, stream, a, t, rows, g);
-    else hipLaunchKernelGGL(kv_write_kernel<false>, dim3(grid), dim3(256), 0, stream, a, t, rows, g);
-  });
-}
-
-hipError_t launch_kv_read(const KvReadArgs& a, int cus, hipStream_t stream) {
-  const int g = group_of(a.cache.head_dim);
-  return in_launches(a.tokens, 2 * a.cache.kv_heads, g, cus, [&](int64_t t, uint32_t rows, unsigned grid) {
-    const dim3 gr(grid), bl(256);
+hipError_t launch_kv_read(const KvReadArgs& all, int cus, hipStream_t stream) {
+  for (int64_t t = 0; t < all.tokens; t += kMostTokens) {
+    KvReadArgs a = all;
+    a.tokens = all.tokens - t < kMostTokens ? all.tokens - t : kMostTokens;
+    a.at = after(all.at, t);
+    a.k = static_cast<char*>(all.k) + t * a.ld_k * (a.out_fp32 ? 4 : 2);
+    a.v = static_cast<char*>(all.v) + t * a.ld_v * (a.out_fp32 ? 4 : 2);
+    const Deal d = deal_of(a.tokens, 2 * a.cache.kv_heads, a.cache.head_dim, cus);
+    const dim3 grid(blocks_of(a.tokens, d)), block(256);
     if (a.cache.dtype == AGG_FP8_E4M3) {
-      if (a.out_fp32) hipLaunchKernelGGL((kv_read_kernel<true, true>), gr, bl, 0, stream, a, t, rows, g);
-      else hipLaunchKernelGGL((kv_read_kernel<true, false>), gr, bl, 0, stream, a, t, rows, g);
+      if (a.out_fp32) hipLaunchKernelGGL((kv_read_kernel<true, true>), grid, block, 0, stream, a, d);
+      else hipLaunchKernelGGL((kv_read_kernel<true, false>), grid, block, 0, stream, a, d);
     } else {
-      if (a.out_fp32) hipLaunchKernelGGL((kv_read_kernel<false, true>), gr, bl, 0, stream, a, t, rows, g);
-      else hipLaunchKernelGGL((kv_read_kernel<false, false>), gr, bl, 0, stream, a, t, rows, g);
+      if (a.out_fp32) hipLaunchKernelGGL((kv_read_kernel<false, true>), grid, block, 0, stream, a, d);
+      else hipLaunchKernelGGL((kv_read_kernel<false, false>), grid, block, 0, stream, a, d);
     }
-  });
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace agg

@@ -551,6 +551,28 @@ def test_write_and_read_beyond_a_launch(ctx):
         assert bool((out[4:-20] == 0).all()) and bool((out[:3] == 0).all())
 
 
+def test_write_and_read_more_tokens_than_a_launch(ctx):
+    tokens, d = (1 << 23) + 9, 16
+    p = _Paged([64, 64], 1, d, 16, "fp8", seed=32)
+    pos = torch.full((tokens,), -1, dtype=I32, device="cuda")
+    pos[-20:] = torch.arange(20, dtype=I32, device="cuda")
+    pos[3] = 40
+    seq = torch.ones(tokens, dtype=I32, device="cuda")
+    x = torch.full((tokens, d), 7.0, dtype=BF16, device="cuda")
+    x[-20:] = torch.randint(-7, 8, (20, d), generator=p.g).bfloat16().cuda()
+    x[-20:, 3] = 7.0                                       # (whole numbers below 8 over 7 / 448 = 2^-6: exact in 8 bits)
+    st = torch.cuda.current_stream()
+    B.kv_write(ctx, p.cache, tokens, x, x, pos, p.dev_table, token_seq=seq, stream=st)
+    back = [torch.full((tokens, d), 5.0, dtype=BF16, device="cuda") for _ in range(2)]
+    B.kv_read(ctx, p.cache, tokens, pos, p.dev_table, *back, token_seq=seq, stream=st)
+    for y in back:
+        assert torch.equal(y[-20:], x[-20:]) and torch.equal(y[3], x[3])
+        assert bool((y[4:-20] == 0).all()) and bool((y[:3] == 0).all())
+    # a token is a sequence of its own: those past the table have no place
+    B.kv_read(ctx, p.cache, 2, pos[3:].contiguous(), p.dev_table, *back, stream=st)
+    assert bool((back[0][1] == 0).all())
+
+
 # ------------------------------------------------------------------------------ streams and graphs
 
 def test_attn_repeats_its_bits_on_any_stream(ctx):
