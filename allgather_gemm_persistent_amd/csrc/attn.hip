@@ -20,6 +20,7 @@ constexpr int kCoherent = 16;                  // an access that the whole GPU s
 constexpr uint32_t kFan = 32;                  // units joined in one step
 constexpr int kChoices = 6;                    // lengths of a unit to choose from
 constexpr float kUnitCost = 12;                // of a unit, beside its tiles, in tiles
+constexpr float kJoinCost = 10;                // of units that are joined
 constexpr float kLn2 = 0.693147181f;
 
 __device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -93,10 +94,11 @@ __device__ inline uint32_t widen8(uint32_t p) {
 // tokens the sum, over all the maximum. The weights enter the second product in bf16 parts, each the bf16 of what the
 // ones before leave: two, 16 bits, for a bf16 result, three, the whole fp32, for an fp32 one; the matrix units are far
 // from busy (32 tokens of 128 channels are 8 KiB of K and of V, and 24 or 32 matrix instructions).
-template <bool FP8, int DP, int RT, bool OUT32>
+template <bool FP8, int DP, int RT, bool OUT32, bool NT>
 __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_kernel(const AttnArgs a) {
   constexpr int EL = FP8 ? 1 : 2;
   constexpr int PARTS = OUT32 ? 3 : 2;         // of the weights
+  constexpr int kRead = NT ? 2 : 0;            // cache policy of the keys' and values' loads
   constexpr int KS = DP / 32;                  // contraction steps of the first product
   constexpr int VE = DP / 16;                  // channels of V a lane holds
   constexpr int KL = DP * EL / 64;             // 16-byte loads of a token's keys by a lane
@@ -162,11 +164,12 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   sum_all(all_tiles);
   const uint32_t total = all_tiles[0] * items, share = (total + grid - 1) / grid;
   // ---- choose S: of some multiples of an even share, the one that is expected to end first. A unit costs its tiles and
-  // as much as kUnitCost of them; where every unit has a workgroup of its own the longest one counts, else the mean and half
-  // of the longest
+  // as much as kUnitCost of them, and joining units as much as kJoinCost, or twice that in two steps; where every unit has a
+  // workgroup of its own the longest one counts, else the mean and half of the longest
+  const uint32_t some = share < (uint32_t)a.least ? (uint32_t)a.least : share;
   auto candidate = [&](int k) {
     constexpr uint32_t quarters[kChoices] = {2, 4, 5, 6, 8, 16};
-    const uint32_t x = (share * quarters[k] + 3) / 4;
+    const uint32_t x = (some * quarters[k] + 3) / 4;
     return x < (uint32_t)a.least ? (uint32_t)a.least : x;
   };
   // (units of a row: tiles / S, rounded up but for 2^-21 of it, by which the reciprocal is shorter: never more)
@@ -186,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   for (int k = 0; k < kChoices; ++k) {
     const uint32_t u = n[k] * items;
     const float s = (float)candidate(k);
-    const float cost = u <= grid ? s + kUnitCost : (float)share + 0.5f * s + (float)u / (float)grid * kUnitCost;
+    const float cost = (u <= grid ? s + kUnitCost : (float)share + 0.5f * s + (float)u / (float)grid * kUnitCost) +
+                       (n[k] > rows ? kJoinCost : 0.0f) + (n[k] > kFan * rows ? kJoinCost : 0.0f);
     if (cost < best) {
       best = cost;
       inv_most = inv[k];
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
       const __amdgpu_buffer_rsrc_t d = descriptor(cache.k, r);
 #pragma unroll
       for (int i = 0; i < KL; ++i)
-        x.k[u][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(d, (int)koff[i], 0, 0));
+        x.k[u][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(d, (int)koff[i], 0, kRead));
       if constexpr (FP8) x.scale[u] = load_scales(cache.k_scale, r);
     }
   };
@@ -372,15 +376,15 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
         for (int p = 0; p < VL; ++p) {
           const int off = (int)((voff[p] + base) | skip | (voff[p] & kOutOfRange));
           if constexpr (VW >= 4) {
-            const u32x4 w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(d, off, 0, 0));
+            const u32x4 w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(d, off, 0, kRead));
 #pragma unroll
             for (int e = 0; e < 4; ++e) x.v[u][i][4 * p + e] = w[e];
           } else if constexpr (VW == 2) {
-            const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(d, off, 0, 0));
+            const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(d, off, 0, kRead));
             x.v[u][i][0] = w[0];
             x.v[u][i][1] = w[1];
           } else {
-            x.v[u][i][0] = __builtin_amdgcn_raw_buffer_load_b32(d, off, 0, 0);
+            x.v[u][i][0] = __builtin_amdgcn_raw_buffer_load_b32(d, off, 0, kRead);
           }
         }
       }
@@ -718,11 +722,24 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   }
 }
 
+template <bool FP8, int DP, int RT, bool NT>
+static hipError_t launch_attn_nt(const AttnArgs& a, int grid, hipStream_t stream) {
+  const dim3 g((unsigned)grid), b(kThreads);
+  if (a.out_fp32) hipLaunchKernelGGL((attn_kernel<FP8, DP, RT, true, NT>), g, b, 0, stream, a);
+  else hipLaunchKernelGGL((attn_kernel<FP8, DP, RT, false, NT>), g, b, 0, stream, a);
+  return hipGetLastError();
+}
+
 template <bool FP8, int DP, int RT>
 static hipError_t launch_attn_rt(const AttnArgs& a, int grid, hipStream_t stream) {
-  if (a.out_fp32) hipLaunchKernelGGL((attn_kernel<FP8, DP, RT, true>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((attn_kernel<FP8, DP, RT, false>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
+  // A cache that the last level's 256 MB cannot hold is read once and not kept there (non-temporal: 4 x 131072 tokens of
+  // 8 bits, 1.07 GB, 201 -> 187 us); a smaller one may be there still (three of 90 MB in turn: 29.6 us, and 32.2
+  // non-temporal). More queries than 16 to a head of the cache: what one workgroup reads another may
+  if constexpr (RT == 1) {
+    const double bytes = 2.0 * (double)a.cache.pages * a.cache.page_size * a.cache.kv_heads * a.cache.head_dim * (FP8 ? 1 : 2);
+    if (bytes > 256e6 && a.group <= 16) return launch_attn_nt<FP8, DP, 1, true>(a, grid, stream);
+  }
+  return launch_attn_nt<FP8, DP, RT, false>(a, grid, stream);
 }
 
 template <bool FP8, int DP>
