@@ -848,7 +848,7 @@ def linear(ctx, m: int, n: int, k: int, dtype, a, b, out, *, a_scale=None, b_sca
 
 
 def agg_linear_shape(dtype, m: int, n: int, k: int):
-    """How linear multiplies: ("stream", parts of K) or ("tiles", (bm, bn))."""
+    """How linear multiplies: ("stream" or (bm, bn) of its tiles, parts of K)."""
     parts, bm, bn = _c_int(), _c_int(), _c_int()
     _call("agg_linear_shape", _dtype(dtype), m, n, k, ctypes.byref(parts), ctypes.byref(bm), ctypes.byref(bn))
-    return ("stream", parts.value) if parts.value else ("tiles", (bm.value, bn.value))
+    return (bm.value, bn.value) if bm.value else "stream", parts.value

@@ -1083,10 +1083,13 @@ struct LinearRow {
 // after the K loop) in passes of RP rows, so that a thread then holds 8 columns of a row: whole lines
 // of the residual and of out, and the activations' code once instead of once an accumulator. The
 // quads of an LDS row are exchanged by the row's number, which keeps the 16 rows that a wave writes at
-// once on different banks. Ends with every thread past its LDS reads only after the tile's last barrier.
-template <int BM, int BN, bool FP8, int FM, int FN, int STAGE_BYTES, int ROWS, typename Row, typename Col>
-__device__ inline void linear_epilogue(const GemmArgs& a, const f32x4 (&acc)[FM][FN], uint8_t* stages, int first_row,
-                                       int blocks, int64_t lo, int64_t hi, int64_t n0, Row qrow, Col qcol) {
+// once on different banks. A split K: every part writes its sums to the workspace (through the
+// caches, as the part that reads them, the tile's last, does: no fence) and the last one adds them in
+// part order. `last` is one word of LDS. (The caller's next barrier comes before anyone writes the LDS again.)
+template <int BM, int BN, bool FP8, bool SPLIT, int FM, int FN, int STAGE_BYTES, int ROWS, typename Row, typename Col>
+__device__ inline void linear_epilogue(const GemmArgs& a, const f32x4 (&acc)[FM][FN], uint8_t* stages, int* last,
+                                       int first_row, int blocks, int64_t lo, int64_t hi, int64_t n0, int part, int tile,
+                                       Row qrow, Col qcol) {
   constexpr int RP0 = STAGE_BYTES / (BN * 4) / ROWS * ROWS, RP = RP0 < BM ? RP0 : BM;
   static_assert(RP >= ROWS && RP * BN * 4 <= STAGE_BYTES, "LDS passes");
   constexpr int Q = BN / 4, C = BN / 8, U = 2;
@@ -1094,18 +1097,11 @@ __device__ inline void linear_epilogue(const GemmArgs& a, const f32x4 (&acc)[FM]
   const int tid = threadIdx.x;
   f32x4* const tl = reinterpret_cast<f32x4*>(stages);
   auto place = [&](int r, int q) { return r * Q + (q ^ (r & 7)); };
-  for (int p0 = 0; p0 < BM && lo + p0 < hi; p0 += RP) {
-    __syncthreads();
-    if (first_row >= p0 && first_row < p0 + RP) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        if (i >= blocks) break;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) tl[place(qrow(i) - p0, qcol(j) >> 2)] = acc[i][j];
-      }
-    }
-    __syncthreads();
-    const int rows = hi - lo - p0 < RP ? (int)(hi - lo - p0) : RP;
+  const bool split = SPLIT && a.ksplit > 1;
+  const __amdgpu_buffer_rsrc_t rw =
+      __builtin_amdgcn_make_buffer_rsrc(a.ws, 0, split ? (int)(a.ksplit * a.M * a.N * 4) : 0, kBufferFlags);
+  // rows [p0, p0 + rows) of the tile, 8 columns a thread: value(row of the pass, quad, m, n, v) gives their sums
+  auto finish = [&](int p0, int rows, auto value) {
     for (int e0 = tid; e0 < rows * C; e0 += kThreads * U) {
       LinearRow<8> x[U];
       int64_t m[U], n[U];
@@ -1121,8 +1117,9 @@ __device__ inline void linear_epilogue(const GemmArgs& a, const f32x4 (&acc)[FM]
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (!in[u]) continue;
-        const int e = e0 + u * kThreads, r = e / C, q = e % C * 2;
-        f32x4 v[2] = {tl[place(r, q)], tl[place(r, q + 1)]};
+        const int e = e0 + u * kThreads;
+        f32x4 v[2];
+        value(e / C, e % C * 2, m[u], n[u], v);
         if constexpr (FP8) {
           const float rs = a.x.a_scale[m[u]];
           const f32x4* const bs = reinterpret_cast<const f32x4*>(a.x.b_scale + n[u]);
@@ -1132,6 +1129,63 @@ __device__ inline void linear_epilogue(const GemmArgs& a, const f32x4 (&acc)[FM]
         x[u].store(a.y, m[u], n[u], v);
       }
     }
+  };
+  for (int p0 = 0; p0 < BM && lo + p0 < hi; p0 += RP) {
+    __syncthreads();
+    if (first_row >= p0 && first_row < p0 + RP) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if (i >= blocks) break;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) tl[place(qrow(i) - p0, qcol(j) >> 2)] = acc[i][j];
+      }
+    }
+    __syncthreads();
+    const int rows = hi - lo - p0 < RP ? (int)(hi - lo - p0) : RP;
+    if (SPLIT && split) {
+      for (int e = tid; e < rows * Q; e += kThreads) {
+        const int64_t m = lo + p0 + e / Q, n = n0 + e % Q * 4;
+        if (n < a.N)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, tl[place(e / Q, e % Q)]), rw,
+                                                 (int)(((part * a.M + m) * a.N + n) * 4), 0, kStoreSystemCoherent);
+      }
+    } else {
+      finish(p0, rows, [&](int r, int q, int64_t, int64_t, f32x4 (&v)[2]) {
+        v[0] = tl[place(r, q)];
+        v[1] = tl[place(r, q + 1)];
+      });
+    }
+  }
+  if constexpr (SPLIT) {
+    if (!split) return;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    uint32_t* const count = a.scratch + tile;
+    if (tid == 0) {
+      const bool all = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.ksplit - 1;
+      *last = all;
+      if (all) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // (for the next launch)
+    }
+    __syncthreads();
+    if (!__builtin_amdgcn_readfirstlane(*last)) return;
+    finish(0, (int)(hi - lo), [&](int, int, int64_t m, int64_t n, f32x4 (&v)[2]) {
+      v[0] = v[1] = f32x4{};
+      for (int p0 = 0; p0 < a.ksplit; p0 += 4) {
+        f32x4 x[4][2];                          // (past the last part the offset is out of range: zeros)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t at = p0 + p < a.ksplit ? (uint32_t)((((p0 + p) * a.M + m) * a.N + n) * 4) : kOutOfRange;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            x[p][h] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(at + 16 * h), 0, kStoreSystemCoherent));
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          v[0] += x[p][0];
+          v[1] += x[p][1];
+        }
+      }
+    });
   }
 }
 
@@ -1279,7 +1333,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
     // single-operation kernel
     auto tile_body = [&](auto ph1_) {
       const int vcol = __builtin_amdgcn_readfirstlane(s_tile[1]);
-      const int ksplit = kGrouped ? 1 : a.ksplit;
+      const int ksplit = EPI == kEpiExperts || (EPI == kEpiLinear && !kSplitTiles) ? 1 : a.ksplit;
       const int col_tile = vcol / ksplit, part = vcol - col_tile * ksplit;
       const int expert = EPI == kEpiExperts ? __builtin_amdgcn_readfirstlane(s_tile[2]) : 0;
       // FFN chain: phase 1 (AllGather+GEMM into h) or phase 2 (GEMM+ReduceScatter of h); the
@@ -1867,8 +1921,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const GemmArgs a) {
                    : wn * WTN + j * 16 + (lane >> 4) * 4;
       };
       if constexpr (EPI == kEpiLinear) {
-        linear_epilogue<BM, BN, FP8, FM, FN, kStageBytes, WTM>(a, acc, stages, wm * wave_rows, FM >> low, lo, hi, n0, qrow,
-                                                               qcol);
+        linear_epilogue<BM, BN, FP8, kSplitTiles, FM, FN, kStageBytes, WTM>(
+            a, acc, stages, &s_ok, wm * wave_rows, FM >> low, lo, hi, n0, part,
+            row_tile * (a.n_col_tiles / ksplit) + col_tile, qrow, qcol);
       } else if constexpr (EPI == kEpiExperts) {
         expert_epilogue<FP8, FM, FN>(a, acc, expert, lo, hi, n0, qrow, qcol);
       } else if (EPI == kEpiFfn && ph1) {

@@ -827,6 +827,7 @@ int ctx_moe_workspace(agg_ctx* ctx, agg_stream stream, size_t bytes, float** ws,
   return AGG_OK;
 }
 
+int ctx_forced_split(const agg_ctx* ctx) { return ctx->force_split; }
 TileShape ctx_forced_tile(const agg_ctx* ctx) { return TileShape{ctx->force_bm, ctx->force_bn}; }
 
 }  // namespace agg

@@ -141,7 +141,7 @@ struct GemmArgs {
   int n_row_tiles1, n_col_tiles1;
   // experts' products (kEpiExperts): `a` rows taken through x, `b` n_experts x K x N, `c` slots x
   // N (gated: N/2) bfloat16. A product with an epilogue (kEpiLinear): one expert that holds every
-  // slot (no offsets, no slot_token), its result in y
+  // slot (no offsets, no slot_token), its result in y; a split K counts its parts in scratch[tile]
   ExpertArgs x;
   LinearArgs y;
 };

@@ -27,8 +27,10 @@ extern "C" int linear(agg_ctx* ctx, int64_t m, int64_t n, int64_t k, int dtype, 
                      residual_dtype == AGG_FP32, out_dtype == AGG_FP32};
   const int units = ctx_units(ctx);
   const TileShape forced = ctx_forced_tile(ctx);
-  const ExpertShape shape = forced.bm ? ExpertShape{false, 0, 0, forced}
-                                      : choose_expert_shape(dtype, m, 1, n, k, 0, units, true);
+  const int parts = ctx_forced_split(ctx);
+  LinearShape shape = forced.bm ? split_linear(dtype, m, n, k, forced, parts ? parts : 1)
+                                : choose_linear_shape(dtype, m, n, k, units);
+  if (!forced.bm && !shape.stream && parts) shape = split_linear(dtype, m, n, k, shape.tile, parts);
   if (shape.stream) {
     StreamArgs t{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(b), nullptr, n, k, x, shape.strips,
                  shape.ksplit, nullptr, 0, nullptr, y};
@@ -45,9 +47,13 @@ extern "C" int linear(agg_ctx* ctx, int64_t m, int64_t n, int64_t k, int dtype, 
   g.N = n;
   g.K = k;
   g.M = m;
-  g.n_col_tiles = int((n + shape.tile.bn - 1) / shape.tile.bn);
-  g.ksplit = 1;
-  g.kps = int((k * eb + 63) / 64);
+  g.n_col_tiles = int((n + shape.tile.bn - 1) / shape.tile.bn) * shape.ksplit;
+  g.ksplit = shape.ksplit;
+  g.kps = shape.kps;
+  if (g.ksplit > 1) {
+    if (int rc = ctx_moe_workspace(ctx, stream, size_t(g.ksplit) * size_t(m) * size_t(n) * sizeof(float), &g.ws, &g.scratch))
+      return rc;
+  }
   g.n_lists = g.list_cols = 1;
   g.scale = 1.0f;
   g.x = x;

@@ -31,15 +31,14 @@ double ceil_div(double a, double b) { return std::ceil(a / b); }
 //   128 x 128         202   207   217   226   377   615
 //   64 x 64           297   309   325   520   710  1277
 // and at 30 of 1000 x 1032, 16 rows: streaming 26, 64 x 64 19, 256 x 256 22.
-ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated, int units,
-                                bool even) {
+ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated, int units) {
   ExpertShape r{false, 0, 1, {64, 64}};
   const bool fp8 = dtype == AGG_FP8_E4M3;
   const int64_t cols = gated ? 2 * n : n;
   // rows an expert holds if the slots are spread evenly over the experts that can hold any; they scatter
-  // around that unless they are known (`even`)
+  // around that
   const int64_t busy = std::max<int64_t>(1, std::min<int64_t>(n_experts, slots));
-  const double rows = double(slots) / double(busy), spread = even ? 0.0 : std::sqrt(rows);
+  const double rows = double(slots) / double(busy), spread = std::sqrt(rows);
   const double k2 = double(k) * (fp8 ? 0.5 : 1.0);             // K in units of two bytes
   const double bytes = double(busy) * double(k) * double(cols) * (fp8 ? 1.0 : 2.0);
   const double u = units;
@@ -54,7 +53,7 @@ ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t
     parts = std::min<int64_t>({units / groups, (k + 511) / 512, 16});
     parts = std::max<int64_t>(1, std::min(parts, kMoeWsBytes / std::max<int64_t>(1, slots * cols * 4)));
   }
-  const double passes = ceil_div(even ? rows : 2 * rows + 2 * spread, 32);   // (the fullest of unevenly liked experts)
+  const double passes = ceil_div(2 * rows + 2 * spread, 32);   // (the fullest of unevenly liked experts)
   const double stream = passes * std::max(bytes / 6.2e6 + 3, ceil_div(double(groups * parts), u) *
                                                                  (5.7 + double(k) * (gated ? 2 : 1) / (160.0 * double(parts))));
 

@@ -100,7 +100,21 @@ struct ExpertShape {
   int strips, ksplit;
   TileShape tile;
 };
+// How linear multiplies: the same, tiles with K in ksplit parts of kps slices (1: no split; the partial sums take at
+// most kLinearWsBytes).
+struct LinearShape {
+  bool stream;
+  int strips, ksplit, kps;
+  TileShape tile;
+};
+constexpr int64_t kLinearWsBytes = int64_t(32) << 20;
+LinearShape choose_linear_shape(int dtype, int64_t m, int64_t n, int64_t k, int units);
+// Tiles of `tile` with K in at most `parts` parts of whole slice pairs.
+LinearShape split_linear(int dtype, int64_t m, int64_t n, int64_t k, TileShape tile, int parts);
+// The parts of K that agg_ctx_set_split asks for; 0: the library's choice.
+int ctx_forced_split(const agg_ctx* ctx);
+
 ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated,
-                                int units, bool even = false);
+                                int units);
 
 }  // namespace agg

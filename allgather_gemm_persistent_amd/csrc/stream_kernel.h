@@ -278,11 +278,22 @@ __global__ void __launch_bounds__(kStreamWaves * 64) expert_stream_kernel(const 
     const int n = strip * SC + e % (SC / 4) * 4;
     if (n >= NO) continue;
     f32x4 v = f32x4{}, up = f32x4{};
-    for (int p = 0; p < ksplit; ++p) {
-      const int64_t at = ((int64_t)p * a.x.slots + s) * N + n;
-      v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(dw, (int)(at * 4), 0, kStoreSystemCoherent));
-      if constexpr (GATED)
-        up += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(dw, (int)((at + NO) * 4), 0, kStoreSystemCoherent));
+    // (four parts' loads ahead of their use; past the last part the offset is out of range: zeros)
+    for (int p0 = 0; p0 < ksplit; p0 += 4) {
+      f32x4 x[4], y[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t at = p0 + p < ksplit ? (uint32_t)((((int64_t)(p0 + p) * a.x.slots + s) * N + n) * 4) : kOutOfRange;
+        x[p] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(dw, (int)at, 0, kStoreSystemCoherent));
+        if constexpr (GATED)
+          y[p] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               dw, (int)(p0 + p < ksplit ? at + (uint32_t)NO * 4 : kOutOfRange), 0, kStoreSystemCoherent));
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        v += x[p];
+        if constexpr (GATED) up += y[p];
+      }
     }
     finish(s, n, v, up);
   }

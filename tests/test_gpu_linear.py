@@ -148,6 +148,55 @@ def test_more_tiles_than_workgroups(ctx, tile, dtype):
         B.agg_ctx_set_tile(ctx)
 
 
+@pytest.mark.parametrize("tile", [(128, 128), (128, 64), (64, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("parts", [2, 3, 5, 16])
+@pytest.mark.parametrize("m,n,k", [(1, 16, 128), (65, 208, 1040), (200, 336, 4096)])
+def test_split_tiles(ctx, tile, dtype, parts, m, n, k):
+    """K of tiles in parts (as many as it has slice pairs at most), called again and on another stream: the same bits."""
+    p = _Product(m, n, k, dtype, residual="bf16", out="fp32", act="silu", extra=16)
+    B.agg_ctx_set_tile(ctx, *tile)
+    B.agg_ctx_set_split(ctx, parts)
+    try:
+        first = p.run(ctx)
+        p.check(first)
+        side = torch.cuda.Stream()
+        for s in (None, side, side, None):
+            again = torch.zeros_like(first)
+            torch.cuda.synchronize()
+            p.run(ctx, out=again, stream=s)
+            torch.cuda.synchronize()
+            assert torch.equal(again[:m, :n], first[:m, :n])
+    finally:
+        B.agg_ctx_set_tile(ctx)
+        B.agg_ctx_set_split(ctx)
+
+
+def test_split_tiles_in_replayed_graphs(ctx):
+    """Two captures of a call whose tiles' K is split, replayed between eager calls of other rows."""
+    ps = [_Product(100, 512, 8192, "bf16", seed=i) for i in range(3)]
+    how, parts = B.agg_linear_shape("bf16", 100, 512, 8192)
+    assert how != "stream" and parts > 1
+    graphs = []
+    for p in ps[:2]:
+        y = torch.zeros(100, 512, dtype=BF16, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            p.run(ctx, out=y, stream=torch.cuda.current_stream())
+        graphs.append((p, g, y))
+    for i in range(6):
+        p, g, y = graphs[i % 2]
+        p.a.copy_(p.a.roll(1, 0))
+        want = p.run(ctx)[:100].clone()
+        ps[2].check(ps[2].run(ctx))
+        y.fill_(5)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 @pytest.mark.parametrize("m", [1, 32, 40])
 def test_split_k(ctx, dtype, m):

@@ -61,12 +61,14 @@ def test_kernel_choice():
     for dtype in ("bf16", "fp8"):
         assert B.agg_linear_shape(dtype, 1, 8192, 8192)[0] == "stream"
         assert B.agg_linear_shape(dtype, 16, 1024, 8192)[1] > 1
-        assert B.agg_linear_shape(dtype, 8192, 8192, 8192) == ("tiles", (256, 256))
+        assert B.agg_linear_shape(dtype, 8192, 8192, 8192) == ((256, 256), 1)
         for m in (0, 1, 33, 500, 1 << 30):
             for n in (0, 16, 1008, 10240):
                 for k in (16, 1008, 8192):
-                    how, what = B.agg_linear_shape(dtype, m, n, k)
-                    assert (1 <= what <= 16) if how == "stream" else what in [(256, 256), (256, 224), (128, 128), (128, 64), (64, 64)]
+                    how, parts = B.agg_linear_shape(dtype, m, n, k)
+                    assert 1 <= parts <= 16 and how in ["stream", (256, 256), (256, 224), (128, 128), (128, 64), (64, 64)]
+                    assert parts == 1 or how in ["stream", (128, 128), (128, 64), (64, 64)]
+                    assert parts * 32 <= max(k, 32)
     for bad in ((0, 1, -1, 8), (0, 1, 8, 4), (3, 1, 8, 8), (0, 1, 1 << 20, 1 << 11)):
         with pytest.raises(B.AggError):
             B.agg_linear_shape(*bad)
