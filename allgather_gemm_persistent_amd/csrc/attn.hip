@@ -732,12 +732,16 @@ static hipError_t launch_attn_nt(const AttnArgs& a, int grid, hipStream_t stream
 
 template <bool FP8, int DP, int RT>
 static hipError_t launch_attn_rt(const AttnArgs& a, int grid, hipStream_t stream) {
-  // A cache that the last level's 256 MB cannot hold is read once and not kept there (non-temporal: 4 x 131072 tokens of
-  // 8 bits, 1.07 GB, 201 -> 187 us); a smaller one may be there still (three of 90 MB in turn: 29.6 us, and 32.2
-  // non-temporal). More queries than 16 to a head of the cache: what one workgroup reads another may
+  // A cache that the last level's 256 MB cannot hold is read once and not kept there (non-temporal), if its lines of 128
+  // bytes are one head's each and neighbours: 4 x 131072 tokens of 8 bits, heads first, 201 -> 186 us; 32 x 8000 of 16
+  // heads of 64 bf16, heads first, 180 -> 161; 256 wide 171 -> 163. Where a line is asked for in parts at different
+  // times it costs: 80 wide 347 -> 420, tokens first 8 bits of 128 118 -> 124, bf16 of 128 189 and 188. More queries than
+  // 16 to a head of the cache: what one workgroup reads another may
   if constexpr (RT == 1) {
-    const double bytes = 2.0 * (double)a.cache.pages * a.cache.page_size * a.cache.kv_heads * a.cache.head_dim * (FP8 ? 1 : 2);
-    if (bytes > 256e6 && a.group <= 16) return launch_attn_nt<FP8, DP, 1, true>(a, grid, stream);
+    const int row = a.cache.head_dim * (FP8 ? 1 : 2);
+    const double bytes = 2.0 * (double)a.cache.pages * a.cache.page_size * a.cache.kv_heads * row;
+    if (bytes > 256e6 && a.group <= 16 && row % 128 == 0 && (a.cache.ld_token == a.cache.head_dim || row >= 512))
+      return launch_attn_nt<FP8, DP, 1, true>(a, grid, stream);
   }
   return launch_attn_nt<FP8, DP, RT, false>(a, grid, stream);
 }
