@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64) expert_stream_kernel(const 
       LinearRow<4> x;
       x.load(a.y, s, n);
       f32x4 w[1] = {v};
-      x.store(a.y, s, n, w);
+      with_activation(a.y.act, [&](auto act) { x.template store<decltype(act)::value>(a.y, s, n, w); });
       return;
     }
     if constexpr (FP8) {
