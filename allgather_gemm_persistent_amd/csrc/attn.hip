@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
         at = row_at(r);
         at = row_of(__builtin_amdgcn_readfirstlane(at.seq), __builtin_amdgcn_readfirstlane(at.hi));
         const uint32_t k = __builtin_amdgcn_readfirstlane(units_of(at.tiles, inv_most));
-        if (before + k > x) break;
+        if (before + k > x || r + 1 >= rows) break;
         before += k;
         slots_before += k > 1 ? k : 0;
       }

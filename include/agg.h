@@ -231,7 +231,7 @@ int agg_ctx_set_reserved_cus(agg_ctx* ctx, int n);
  */
 int agg_ctx_set_tile(agg_ctx* ctx, int bm, int bn);
 
-/* Split-K of later AllGather+GEMM calls. With few output tiles (fewer than half the CUs) and a
+/* Split-K of later AllGather+GEMM and `linear` calls. With few output tiles (fewer than half the CUs) and a
  * long K, the library cuts each tile's K range into parts computed by different workgroups;
  * every part writes an fp32 partial into a ctx-owned buffer (ksplit x M x N floats, allocated
  * and grown by the ctx) and the parts are summed in part order (by the last part to finish, or,
@@ -659,10 +659,13 @@ int moe_combine(agg_ctx* ctx, int64_t tokens, int top_k, int64_t n, int64_t slot
  * page: its positions cannot be written, read as zeros, and are left out of the attention. Sequences
  * may share pages (a common prefix).
  *
- * Every call launches one kernel on `stream` and is capturable. Of the ctx they use its device and,
- * in paged_attn, a workspace of the stream or capture (as moe_gemm's: nothing else is allocated, calls on several
- * streams and graphs do not meet, two replays of one capture must not run at once). Device arrays are
- * 16-byte aligned, the int32 and fp32 ones 4-byte aligned. No floating-point atomics.
+ * Every call launches one kernel on `stream` (kv_write and kv_read one for each 2^23 tokens, paged_attn one for
+ * each 2^31 / (heads of the cache times positions of a table's row over 32) rows) and is capturable. Of the ctx they
+ * use its device and, in paged_attn, a workspace of the stream or capture, as moe_gemm does (4 results of a head's queries
+ * for every workgroup: 9 MiB for 8 heads of 128, up to 70 for 64): nothing else is allocated, calls on several streams and
+ * graphs do not meet, two replays of one capture must not run at once. Rows (q, k, v, the outputs, the cache and its
+ * scales) are 16-byte aligned, positions, lengths, sequences and tables 4-byte. What a call reads must not change while it
+ * runs. No floating-point atomics.
  * Passage: none (the pages give no attention; the formulas are the plain definitions stated here).
  */
 

@@ -232,6 +232,61 @@ def test_attn_many_rows(ctx):
     _check(p, ctx, 4)
 
 
+@pytest.mark.parametrize("rows", [63, 64, 65, 255, 256, 257, 513])
+def test_attn_row_counts(ctx, rows):
+    """Row counts around those at which the work is divided in other ways; a few long rows among them."""
+    g = _gen(rows)
+    lengths = [int(x) for x in torch.randint(0, 20, (rows,), generator=g)]
+    for i in (0, rows // 2, rows - 1):
+        lengths[i] = 1500
+    p = _Paged(lengths, 1, 64, 16, "bf16", seed=rows)
+    _check(p, ctx, 2)
+
+
+def test_attn_more_rows_than_a_launch(ctx):
+    """A table so wide that its rows go in several launches, sequences by the rows' numbers."""
+    p = _Paged([20] * 4 + [5000], 1, 16, 4096, "bf16", seed=6)
+    rows, width = 600, 65536
+    table = torch.full((rows, width), -1, dtype=I32, device="cuda")
+    seqs = [i % 4 for i in range(rows)]
+    seqs[400] = 4
+    table[:, :2] = p.dev_table[torch.tensor(seqs)]
+    lens = torch.tensor([1 + i % 20 for i in range(rows)], dtype=I32)
+    lens[400] = 4999
+    q = torch.randn(rows, 32, generator=p.g).bfloat16()
+    y, lse = torch.full((rows, 32), 7.0, device="cuda"), torch.full((rows, 2), 7.0, device="cuda")
+    B.paged_attn(ctx, p.cache, rows, q.cuda(), lens.cuda(), table, y, scale=0.25, lse=lse, stream=torch.cuda.current_stream())
+    for r in range(rows):
+        n = int(lens[r])
+        want, want_lse, err, err_lse = _attention(q[r].double().reshape(2, 16), p.rows("k", seqs[r], n), p.rows("v", seqs[r], n), 0.25)
+        _within(y[r].reshape(2, 16), want, err + EPS32 * want.abs(), f"row {r}")
+        _within(lse[r], want_lse, err_lse, f"lse {r}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("rows,n", [(1, 300), (1, 3000), (1, 40000), (30, 900), (200, 300)])
+def test_attn_called_again_and_again(ctx, dtype, rows, n):
+    """Calls behind each other on one stream, of other lengths each time, leave the workspace's counters as they found
+    them: the first call's result comes back to the bit."""
+    p = _Paged([max(1, n - 7 * i) for i in range(rows)], 2, 64, 16, dtype, seed=rows)
+    q = torch.randn(rows, 8 * 64, generator=p.g).bfloat16().cuda()
+    st = torch.cuda.current_stream()
+    y = [torch.zeros(rows, 8 * 64, device="cuda") for _ in range(8)]
+    for i, out in enumerate(y):
+        lens = torch.tensor([max(0, x - (37 * i if 0 < i < 7 else 0)) for x in p.lengths], dtype=I32, device="cuda")
+        B.paged_attn(ctx, p.cache, rows, q, lens, p.dev_table, out, scale=0.125, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], y[7]) and not torch.equal(y[0], y[3])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("heads_first,dim", [(True, 128), (False, 128), (True, 64), (False, 256)])
+def test_attn_of_a_large_cache(ctx, dtype, heads_first, dim):
+    """A pool beyond the size from which its lines are read past the last level, most of it free."""
+    p = _Paged([700, 1, 0, 333], 2, dim, 64, dtype, heads_first, seed=dim, spare=(600000 if dtype == "bf16" else 1200000) // dim)
+    _check(p, ctx, 8, out="fp32")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 def test_attn_rows_of_one_sequence(ctx, dtype):
     """Several new tokens of a sequence, each up to its own place."""
