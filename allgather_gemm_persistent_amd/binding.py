@@ -608,7 +608,7 @@ def _rows(x, rows, cols, what, dtype=None):
     read once.)"""
     if x is None:
         return None, 0
-    shape, strides = x.shape, x.stride()
+    shape, strides = x.size(), x.stride()
     if len(shape) != 2 or shape[1] != cols or shape[0] < rows:
         raise AggError(AGG_E_ARG, what, f"has shape {tuple(shape)}, the call takes {rows} x {cols}")
     if dtype is not None and x.dtype is not dtype:
@@ -759,9 +759,10 @@ class KvCache:
 
 def _table(table):
     """(pointer, sequences, pages of each, elements from one row to the next) of a table of pages."""
-    if table.dtype is not torch.int32 or table.dim() != 2:
-        raise AggError(AGG_E_ARG, "table", f"is {table.dtype} of {table.dim()} dimensions, not int32 of two")
-    seqs, pages = table.shape
+    size = table.size()
+    if table.dtype is not torch.int32 or len(size) != 2:
+        raise AggError(AGG_E_ARG, "table", f"is {table.dtype} of {len(size)} dimensions, not int32 of two")
+    seqs, pages = size
     ld, step = table.stride()
     if step != 1 and pages > 1:
         raise AggError(AGG_E_ARG, "table", "must have contiguous rows")
@@ -786,16 +787,17 @@ def kv_write(ctx, cache, tokens: int, k, v, positions, table, *, token_seq=None,
     pv, lv = _rows(v, tokens, cols, "v", bf16)
     heads, pq, lq, po, lo = 0, None, 0, None, 0
     if q is not None:
-        heads = q.shape[-1] // cache.head_dim
+        heads = q.size(-1) // cache.head_dim
         pq, lq = _rows(q, tokens, heads * cache.head_dim, "q", bf16)
         if q_out is None:
             raise AggError(AGG_E_ARG, "q_out", "is needed with q")
         po, lo = _rows(q_out, tokens, heads * cache.head_dim, "q_out", bf16)
     rows, dim = 0, 0
     if rope is not None:
-        if rope.dim() != 2:
-            raise AggError(AGG_E_ARG, "rope", f"has {rope.dim()} dimensions, not two")
-        rows, dim = rope.shape
+        size = rope.size()
+        if len(size) != 2:
+            raise AggError(AGG_E_ARG, "rope", f"has {len(size)} dimensions, not two")
+        rows, dim = size
     pt, seqs, pages, lt = _table(table)
     _call("kv_write", ctx, cache.ref, tokens, heads, pq, lq, po, lo, pk, lk, pv, lv,
           _flat(rope, rows * dim, "rope", torch.float32), rows, dim, int(rope_pairs),
@@ -817,7 +819,7 @@ def paged_attn(ctx, cache, rows: int, q, lens, table, out, *, scale: float, row_
                stream=None) -> None:
     """out = softmax(scale * q K^T) V over the first lens[r] tokens of each row's sequence (the last `window` of
     them, if it is not 0), bfloat16 or float32; lse = the logarithms of the sums."""
-    cols = q.shape[-1]
+    cols = q.size(-1)
     heads = cols // cache.head_dim
     if heads * cache.head_dim != cols:
         raise AggError(AGG_E_ARG, "q", f"has {cols} columns, not whole heads of {cache.head_dim}")

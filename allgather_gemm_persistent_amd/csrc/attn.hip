@@ -34,10 +34,11 @@ __device__ inline uint32_t pack2(float lo, float hi) {
 __device__ inline float low_half(uint32_t p) { return __builtin_bit_cast(float, p << 16); }
 __device__ inline float high_half(uint32_t p) { return __builtin_bit_cast(float, p & 0xFFFF0000u); }
 
-// Over the wave's lanes, without LDS: the sum of the lanes up to this one, and x of lane 63 of it.
-__device__ inline uint32_t sum_upto(uint32_t x) {
+// Over the wave's lanes, without LDS: f (of whole numbers, 0 for none) of the lanes up to this one.
+template <typename F>
+__device__ inline uint32_t lanes_upto(uint32_t x, F f) {
   auto step = [&](auto ctrl, auto rows) {
-    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+    x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
   };
   using std::integral_constant;
   step(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});   // row_shr 1, 2, 4, 8
@@ -47,6 +48,12 @@ __device__ inline uint32_t sum_upto(uint32_t x) {
   step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // lane 15 of the row before, lane 31
   step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
   return x;
+}
+__device__ inline uint32_t sum_upto(uint32_t x) {
+  return lanes_upto(x, [](uint32_t a, uint32_t b) { return a + b; });
+}
+__device__ inline uint32_t most_upto(uint32_t x) {
+  return lanes_upto(x, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 __device__ inline uint32_t last_lane(uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane((int)x, 63); }
 
@@ -174,30 +181,39 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   };
   // (units of a row: tiles / S, rounded up but for 2^-21 of it, by which the reciprocal is shorter: never more)
   auto units_of = [&](uint32_t tiles, float inv) { return (uint32_t)ceilf((float)tiles * inv); };
-  uint32_t n[kChoices] = {};
-  float inv[kChoices];
-#pragma unroll
-  for (int k = 0; k < kChoices; ++k) inv[k] = (1.0f - 0x1p-21f) / (float)candidate(k);
-  each_row([&](const Row& x) {
-#pragma unroll
-    for (int k = 0; k < kChoices; ++k) n[k] += units_of(x.tiles, inv[k]);
-  });
-  sum_all(n);
+  auto inverse = [](uint32_t s) { return (1.0f - 0x1p-21f) / (float)s; };
   float inv_most = 1.0f;
-  float best = INFINITY;
+  if (few && total <= grid) {
+    // a workgroup for every tile: latency counts. Rows that four waves finish in two turns are not split, others at most
+    // into as many units as are joined in one step
+    const uint32_t longest = last_lane(most_upto(only.tiles)), s = (longest + kFan - 1) / kFan;
+    inv_most = inverse(longest <= 8 ? longest : s < (uint32_t)a.least ? (uint32_t)a.least : s);
+  } else {
+    uint32_t n[kChoices] = {};
+    float inv[kChoices];
 #pragma unroll
-  for (int k = 0; k < kChoices; ++k) {
-    const uint32_t u = n[k] * items;
-    const float s = (float)candidate(k);
-    const float cost = (u <= grid ? s + kUnitCost : (float)share + 0.5f * s + (float)u / (float)grid * kUnitCost) +
-                       (n[k] > rows ? kJoinCost : 0.0f) + (n[k] > kFan * rows ? kJoinCost : 0.0f);
-    if (cost < best) {
-      best = cost;
-      inv_most = inv[k];
+    for (int k = 0; k < kChoices; ++k) inv[k] = inverse(candidate(k));
+    each_row([&](const Row& x) {
+#pragma unroll
+      for (int k = 0; k < kChoices; ++k) n[k] += units_of(x.tiles, inv[k]);
+    });
+    sum_all(n);
+    float best = INFINITY;
+#pragma unroll
+    for (int k = 0; k < kChoices; ++k) {
+      const uint32_t u = n[k] * items;
+      const float s = (float)candidate(k);
+      const float cost = (u <= grid ? s + kUnitCost : (float)share + 0.5f * s + (float)u / (float)grid * kUnitCost) +
+                         (n[k] > rows ? kJoinCost : 0.0f) + (n[k] > kFan * rows ? kJoinCost : 0.0f);
+      if (cost < best) {
+        best = cost;
+        inv_most = inv[k];
+      }
     }
   }
   // ---- units, and slots of the workspace, of the rows before each thread's. (An item of more units than one has fewer than
-  // twice its tiles over S, and S is at least half of an even share: slots are no more than 4 * grid)
+  // twice its tiles over S, and S is at least half of an even share: slots are no more than 4 * grid. An even share of one
+  // tile: S is 4 or more, or nothing is split)
   uint32_t units = 0, slots = 0;
   each_row([&](const Row& x) {
     const uint32_t k = units_of(x.tiles, inv_most);
