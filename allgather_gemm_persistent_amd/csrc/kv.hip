@@ -159,16 +159,21 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const KvWriteArgs a, cons
         m = group_max(m, deal.lanes_log2);
         const float top = __builtin_bit_cast(float, m) / 448.0f;
         const float scale = top > 0.0f ? top : 1.0f;        // a row of zeros, or with a NaN: 1
-        // (one reciprocal a row: it and the division differ by a unit of fp32 at most, far below e4m3's. A
-        // scale so small that the reciprocal overflows divides; a subnormal one can be a third below
-        // max|x| / 448, and the 1 of a row with a NaN has nothing to do with the others: these clamp)
-        const bool usual = top >= kNormal;
-        const float by = 1.0f / scale;
+        // One reciprocal a row, and a step that brings each quotient to what the division gives (a product with the
+        // reciprocal alone is a unit off now and then, and puts more elements on the other side of a tie). A
+        // subnormal scale can be a third below max|x| / 448, an infinite one has no reciprocal, and the 1 of a row
+        // with a NaN has nothing to do with the others: these divide and clamp
+        if (top >= kNormal && top < __builtin_inff()) {
+          const float by = 1.0f / scale;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float& v = x[i >> 3][i & 7];
-          v = scale >= kNormal ? v * by : v / scale;
-          if (!usual) v = clamp_e4m3(v);
+          for (int i = 0; i < 16; ++i) {
+            float& v = x[i >> 3][i & 7];
+            const float q = v * by;
+            v = __builtin_fmaf(__builtin_fmaf(-q, scale, v), by, q);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i >> 3][i & 7] = clamp_e4m3(x[i >> 3][i & 7] / scale);
         }
         if (in) {
           *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(pool) + to + d0) = narrow_e4m3(x[0]);
