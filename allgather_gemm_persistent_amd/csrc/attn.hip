@@ -80,9 +80,9 @@ __device__ inline uint32_t widen8(uint32_t p) {
 }  // namespace
 
 // An item is a row, a head of the cache, and up to 16 * RT of the queries that share it; its length counts in tiles of 32
-// tokens. An item is cut into equal units of at most S tiles, S by the lengths of all rows (choose, below), so long
-// sequences are split over many workgroups and short ones are not split at all; the workgroups take units in
-// turn, a unit's tiles divided among the four waves. An item of one unit is written at once; the units of others go
+// tokens. An item is cut into equal units of at most S tiles, S by the lengths of all rows (choose, below; lengths are read
+// on the device, so a captured call follows them), so long sequences are split over many workgroups and short ones are
+// not split at all; the workgroups take units in turn, a unit's tiles divided among the four waves. An item of one unit is written at once; the units of others go
 // to the workspace (fp32, written through: output, maximum and sum), and the workgroup that finishes the last of them
 // joins them in their order. More than kFan units are joined in two steps, groups of them first, so that no
 // workgroup has many to read (one compute unit reads some 50 GB/s). Who is last depends on timing, what it
@@ -101,6 +101,15 @@ __device__ inline uint32_t widen8(uint32_t p) {
 // tokens the sum, over all the maximum. The weights enter the second product in bf16 parts, each the bf16 of what the
 // ones before leave: two, 16 bits, for a bf16 result, three, the whole fp32, for an fp32 one; the matrix units are far
 // from busy (32 tokens of 128 channels are 8 KiB of K and of V, and 24 or 32 matrix instructions).
+//
+// Bound by reading K and V once. A kernel that only reads reaches 6.9 TB/s on the whole GPU, a copy 5.1:
+//   4 rows of 131072 tokens, 8 heads of 128 in 8 bits (1.1 GB)             184 us    6.0 TB/s    matrix units 0.11 busy
+//   61 rows up to 4000 in a window of 1000, 20 heads of 80 (212 MB)     44 - 50 us    4.2 - 4.8 TB/s
+//   16 rows up to 8192, 64 heads on 8 of 128 (90 MB)                    25 - 28 us    3.2 - 3.6 TB/s
+//   1 row of 500 tokens, 8 heads on 1                                     8.8 us    latency
+// (one workgroup a row and head took 2108, 45, 105 and 12 us.) In the third of them planning takes 2.5 us, reading 15, and
+// the joins, where one compute unit reads up to 26 results, 5. A short call is a chain of trips to memory: lengths, table,
+// K, the results' way through the workspace, the counter, the results again.
 template <bool FP8, int DP, int RT, bool OUT32, bool NT>
 __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_kernel(const AttnArgs a) {
   constexpr int EL = FP8 ? 1 : 2;
@@ -185,7 +194,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   float inv_most = 1.0f;
   if (few && total <= grid) {
     // a workgroup for every tile: latency counts. Rows that four waves finish in two turns are not split, others at most
-    // into as many units as are joined in one step
+    // into as many units as are joined in one step (against the choice below: one row of 500 tokens 9.8 -> 8.8 us, of 2000
+    // 13.6 -> 12.5, 16 rows of 800 11.7 -> 10.6)
     const uint32_t longest = last_lane(most_upto(only.tiles)), s = (longest + kFan - 1) / kFan;
     inv_most = inverse(longest <= 8 ? longest : s < (uint32_t)a.least ? (uint32_t)a.least : s);
   } else {
