@@ -732,8 +732,8 @@ int kv_read(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens, const int32
  *   out, out_dtype   AGG_BF16 or AGG_FP32 rows of q_heads * head_dim
  *   lse              fp32 [rows, q_heads] or NULL: with it, parts of a sequence that lie on several
  *                    ranks can be joined
- * Sums, maxima and the weights' products are fp32 (the weights enter the matrix units as two bf16
- * parts each, 16 bits of fraction). The length is split over workgroups and the parts are joined in
+ * Sums and maxima are fp32; the weights enter the matrix units as two bf16 parts each, 16 bits of them, for a
+ * bf16 out, and as three, all of fp32, for an fp32 one. The length is split over workgroups and the parts are joined in
  * their order, so a result does not depend on timing; it may depend, in its last bits, on the other
  * rows' lengths, by which the work is divided.
  */

@@ -243,6 +243,17 @@ def test_attn_row_counts(ctx, rows):
     _check(p, ctx, 2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("lengths,heads,dim", [([256] * 8, 8, 64), ([256] * 7 + [257], 8, 64), ([16384], 1, 64), ([16385], 1, 64),
+                                               ([4096, 1], 4, 64), ([4064, 0], 4, 64), ([1025, 3], 1, 128), ([256, 31, 0], 2, 128),
+                                               ([257, 31, 0], 2, 128), ([8192], 1, 256), ([8193], 1, 256), ([0] * 64, 2, 64)])
+def test_attn_few_tiles(ctx, dtype, lengths, heads, dim):
+    """As many tiles of 32 tokens as there are workgroups (two a compute unit up to 128 channels, one beyond), one more, and
+    rows around those that are not split."""
+    p = _Paged(lengths, heads, dim, 64, dtype, seed=sum(lengths))
+    _check(p, ctx, 2 * heads)
+
+
 def test_attn_more_rows_than_a_launch(ctx):
     """A table so wide that its rows go in several launches, sequences by the rows' numbers."""
     p = _Paged([20] * 4 + [5000], 1, 16, 4096, "bf16", seed=6)
