@@ -593,6 +593,22 @@ def test_write_rows_that_are_not_numbers(ctx):
     assert bool((p.v[page].float()[:4] == 0).all()) and bool((p.v_scale[page][:, :4] == 1).all())
 
 
+def test_write_rows_as_the_division_has_them(ctx):
+    """In 8 bits the elements are the nearest e4m3 of x / scale, the scale of max|x| / 448, both fp32 divisions: to the bit (a
+    product with the reciprocal puts some of half a million on the other side of a tie)."""
+    p = _Paged([512], 8, 128, 16, "fp8", seed=33)
+    x = (torch.randn(512, 8, 128, generator=p.g) * torch.logspace(-30, 30, 512)[:, None, None]).bfloat16()
+    rows = x.reshape(512, -1).cuda()
+    B.kv_write(ctx, p.cache, 512, rows, rows, torch.arange(512, dtype=I32, device="cuda"), p.dev_table,
+               token_seq=torch.zeros(512, dtype=I32, device="cuda"), stream=torch.cuda.current_stream())
+    at = p.table[0].long().cuda()
+    want_scale = x.float().abs().amax(-1) / torch.tensor(448.0)
+    want = (x.float() / want_scale[..., None]).to(FP8)
+    for pool, scale in ((p.k, p.k_scale), (p.v, p.v_scale)):
+        assert torch.equal(scale[at].cpu().transpose(1, 2).reshape(512, 8), want_scale)
+        assert torch.equal(pool[at].view(torch.uint8).cpu().reshape(512, 8, 128), want.view(torch.uint8))
+
+
 def test_write_and_read_beyond_a_launch(ctx):
     """More rows than one launch counts: tokens of 1024 heads."""
     tokens, h, d = (1 << 19) + 9, 1024, 16
