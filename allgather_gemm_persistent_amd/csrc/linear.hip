@@ -8,10 +8,12 @@
 //   128 x 8192 x 8192 fp8, 128 x 64 tiles, K in two      25.6 us    2.7 TB/s (34 where nothing of the weight is cached)
 //   4096 x 8192 x 8192 bf16, 256 x 256 tiles             406 us     1354 TFLOP/s
 //   777 x 1000 x 1032 bf16, GELU, 64 x 64 tiles          10.8 us    latency: 17 slices of K in turn
-// Between some 32 and 256 rows neither bound is near: a tile 64 fp8 columns wide asks for B in pieces of 64 bytes, and a
-// compute unit gets some 150 pieces a microsecond, whatever is in flight (a ring of five slice pairs instead of four:
-// 34.2 -> 34.7 us); wider tiles need K in more parts, whose sums pass through memory (128 x 128, four parts: 33.9; 64 x
-// 64, whole: 40.4).
+// Between some 32 and 256 rows neither bound is near. Rows of B that are a multiple of 1024 bytes apart cost most (32 rows,
+// fp8, 128 x 64 tiles, nothing of the weight cached: 8192 columns 27.2 us, 8128 21.9, 6144, on fewer compute units, 27.2;
+// one part of K 41 and 30), whichever XCD takes which columns, whatever A's stride or the loads' cache policy, and more in
+// flight does not help (a ring of five slice pairs instead of four: 34.2 -> 34.7 us at 128 rows). B's loads non-temporal
+// gain 2 to 8% there, but lose 20% where the last level holds the weight. Wider tiles need K in more parts, whose
+// sums pass through memory (128 rows: 128 x 128, four parts: 33.9; 64 x 64, whole: 40.4).
 #include "stream_kernel.h"
 
 namespace agg {
