@@ -1026,11 +1026,16 @@ __device__ inline float activated(float x) {
   if constexpr (ACT == AGG_ACT_GELU_TANH)
     return x * __builtin_amdgcn_rcpf(1.0f + __expf(-1.59576912f * (x + 0.044715f * x * x * x)));
   if constexpr (ACT == AGG_ACT_GELU) {
-    // x (1 + erf(x / sqrt 2)) / 2 by erfc(z) = t (a1 + .. + a5 t^4) e^-z^2, t = 1 / (1 + p z), z >= 0: Abramowitz and
-    // Stegun, formula 7.1.26, within 1.5e-7
-    const float z = 0.707106781f * fabsf(x), t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * z);
-    const float c = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f)))) *
-                    __expf(-z * z);
+    // x Phi(x) = x c / 2 below zero and x (2 - c) / 2 above, c = erfc(|x| / sqrt 2) = t Q(t) e^(-x^2 / 2) with
+    // t = 1 / (1 + 0.4 |x| / sqrt 2). Q is fitted to the least relative error over all x (1.6e-7), so the small values
+    // below zero keep their digits: within (31 + 1.5 x^2) 2^-24 of themselves. (A formula of five terms within 1.5e-7 of 1
+    // is 5e-5 of the value off at -3 and 2e-2 at -10, and saves 4 us of the 100 of 4096 x 8192 x 1024)
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.282842726f * fabsf(x));
+    float q = 0.0502589568f;
+    for (const float a : {-0.182889894f, 0.169068456f, -0.00559473317f, 0.141426176f, 0.16854313f, 0.207842574f, 0.225669608f,
+                          0.225675866f})
+      q = q * t + a;
+    const float c = t * q * __builtin_amdgcn_exp2f(x * x * -0.721347520f);
     return 0.5f * x * (x < 0.0f ? c : 2.0f - c);
   }
   return x;

@@ -746,7 +746,9 @@ int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows, int q_head
 /* ---- Products with an epilogue --------------------------------------------------------------- */
 
 /* Activations of `linear`: x, max(x, 0), x / (1 + e^-x), x Phi(x) (Phi the normal distribution's),
- * and x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2. */
+ * and x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2. In fp32, within these parts of their value, small
+ * values too: SiLU (6 + 1.5 |x|) 2^-24, GELU (31 + 1.5 x^2) 2^-24, with tanh (6 + 16 |x| + 0.7 |x|^3) 2^-24;
+ * what is below |x| 2^-126 may be zero. */
 enum { AGG_ACT_NONE = 0, AGG_ACT_RELU = 1, AGG_ACT_SILU = 2, AGG_ACT_GELU = 3, AGG_ACT_GELU_TANH = 4 };
 
 /* out = act(A B + bias) + residual, the projections of a layer: one launch.

@@ -286,3 +286,36 @@ def test_streams_and_replayed_graphs(ctx, dtype):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want), i
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("m,dtype", [(5, "bf16"), (300, "bf16"), (5, "fp8"), (300, "fp8")])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_activations_keep_their_small_values(ctx, act, m, dtype, out):
+    """A product of zeros, so that the bias is the activation's argument to the bit, from -10 to 10: each value within
+    some units of itself, the tails' too. The steps' errors in units of 2^-24 of the result, each rounding half a unit in
+    the last place (1), v_exp and v_rcp a whole one (2); an exponent's relative error counts as often as the exponent is large:
+      SiLU       the exponent's constant and product 1.5 |x|, then v_exp 2, the sum 1, v_rcp 2, the product 1
+      GELU       the exponent x^2 / 2: the square, its constant and the product 3 x^2 / 2; t: 5 steps, which Q t passes on 2.9
+                 times; Q: 1.6e-7, 2.6, and its sums, of terms 1.4 times it in all, 8; v_exp 2, three products 3
+      GELU tanh  the exponent 2 u of eight roundings; then as SiLU
+    A reciprocal below 2^-126, which may come out as zero, adds |x| 2^-126."""
+    n, k = 2048, 16
+    x = torch.cat([torch.linspace(-10, 10, n - 64), torch.logspace(-30, 0, 32), -torch.logspace(-30, 0, 32)]).bfloat16()
+    z = x.double()
+    u2 = 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    want, units = {"silu": (z / (1 + torch.exp(-z)), 6 + 1.5 * z.abs()),
+                   "gelu": (0.5 * z * torch.special.erfc(-z / math.sqrt(2)), 31 + 1.5 * z * z),
+                   "gelu_tanh": (z / (1 + torch.exp(-u2)), 6 + 9.5 * u2.abs())}[act]
+    err = want.abs() * units * 2.0 ** -24 + z.abs() * 2.0 ** -126
+    bound = err + (HALF_BF16 * (want.abs() + err) if out == "bf16" else 0)
+    el, to = (FP8, BF16)[dtype == "bf16"], {"bf16": BF16, "fp32": F32}[out]
+    ones = (torch.ones(m, device="cuda"), torch.ones(n, device="cuda")) if dtype == "fp8" else (None, None)
+    y = torch.empty(m, n, dtype=to, device="cuda")
+    B.linear(ctx, m, n, k, dtype, torch.zeros(m, k, device="cuda").to(el), torch.zeros(k, n, device="cuda").to(el), y,
+             a_scale=ones[0], b_scale=ones[1], bias=x.cuda(), act=act, stream=torch.cuda.current_stream())
+    got = y.double().cpu()
+    bad = ~((got - want).abs() <= bound)
+    assert not bad.any(), (f"{int(bad.sum())} of {bad.numel()}; worst error over bound "
+                           f"{float(((got - want).abs() / bound).nan_to_num(0).max()):.3g} at x = "
+                           f"{float(z[((got - want).abs() / bound).nan_to_num(0).amax(0).argmax()])}")
