@@ -30,12 +30,14 @@ class AttnLayer:
     norm: bf16[hidden]; w_qkv: hidden x (q_heads + 2 kv_heads) head_dim (queries, keys, values side by side); w_out:
     q_heads head_dim x hidden, both bf16, or float8_e4m3fn with qkv_scale and out_scale (fp32, per column). bias: bf16 per
     column of w_qkv, or None. rope: fp32, positions x rope_dim (cosines, then sines), or None. The cache: `pages` pages of
-    page_size tokens, made here ("bf16" or "fp8"). `tokens` is the most a call takes.
+    page_size tokens, made here ("bf16" or "fp8"). `tokens` is the most a call takes. ctx: the caller's, which outlives the
+    layer (layers that share one share its workspaces: one of paged_attn's for a stream or a graph, whatever the number
+    of layers), or None: one of the layer's own.
     """
 
     def __init__(self, tokens, q_heads, kv_heads, head_dim, norm, w_qkv, w_out, pages, page_size=64, cache="bf16",
                  qkv_scale=None, out_scale=None, bias=None, rope=None, rope_pairs=False, window=0, scale=None, eps=1e-6,
-                 device="cuda"):
+                 device="cuda", ctx=None):
         self.device = B.cuda_device(device)
         to = lambda t: None if t is None else t.to(self.device).contiguous()  # noqa: E731
         self.norm, self.w_qkv, self.w_out, self.bias = to(norm), to(w_qkv), to(w_out), to(bias)
@@ -61,7 +63,8 @@ class AttnLayer:
         pool = lambda: new(pages, page_size, kv_heads, head_dim, dtype=fp8 if cache == "fp8" else bf16)  # noqa: E731
         scales = lambda: new(pages, kv_heads, page_size, dtype=f32) if cache == "fp8" else None  # noqa: E731
         self.cache = B.KvCache(pool(), pool(), scales(), scales())
-        self.ctx = B.agg_ctx_create(self.device.index)
+        self.owns_ctx = ctx is None
+        self.ctx = B.agg_ctx_create(self.device.index) if ctx is None else ctx
 
     def run(self, x, positions, lens, table, seq=None, residual=None, stream=None):
         """x: tokens x hidden, bf16 or fp32 (what gemm_ar or gemm_rs left); residual: bf16 or None, then overwritten
@@ -92,9 +95,9 @@ class AttnLayer:
         return self.out[:t]
 
     def close(self):
-        if self.ctx is not None:
+        if self.ctx is not None and self.owns_ctx:
             B.agg_ctx_destroy(self.ctx)
-            self.ctx = None
+        self.ctx = None
 
 
 def rotations(positions, dim, base=10000.0):

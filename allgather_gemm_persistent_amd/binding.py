@@ -122,6 +122,7 @@ _SIGNATURES = {
     "agg_check_kv_read_args": [_vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64],
     "agg_check_paged_attn_args": [_vp, _c_i64, _c_int, _vp, _c_i64, _c_f32, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64,
                                   _c_int, _vp, _c_i64],
+    "agg_paged_attn_workspace": [_vp, _c_i64, _c_int, _c_i64, _c_i64, ctypes.POINTER(_c_i64)],
     "agg_check_norm_args": [_c_i64, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_f32,
                             _c_int, _vp, _c_i64, _vp, _c_f32],
     "agg_check_route_args": [_c_i64, _c_int, _c_int, _c_int, _vp, _c_i64, _c_int, _c_int, _c_int, _c_f32,
@@ -829,6 +830,13 @@ def paged_attn(ctx, cache, rows: int, q, lens, table, out, *, scale: float, row_
     _call("paged_attn", ctx, cache.ref, rows, heads, pq, lq, scale, _flat(lens, rows, "lens", torch.int32),
           _token_seq(row_seq, rows, seqs, "row_seq"), pt, seqs, pages, lt, window, _tensor_dtype(out, "out"), po, lo,
           _flat(lse, rows * heads, "lse", torch.float32), _stream(stream))
+
+
+def agg_paged_attn_workspace(cache, rows: int, q_heads: int, seq_pages: int, window: int = 0) -> int:
+    """Bytes of the workspace that paged_attn takes for a call."""
+    n = _c_i64()
+    _call("agg_paged_attn_workspace", cache.ref, rows, q_heads, seq_pages, window, ctypes.byref(n))
+    return n.value
 
 
 # ------------------------------------------------------------------------------ products with an epilogue

@@ -1,7 +1,33 @@
 // The attention operators' host side that needs no GPU: argument checks.
+#include <algorithm>
 #include <cmath>
 
 #include "plan.h"
+
+namespace agg {
+
+AttnShape choose_attn_shape(const agg_kv_cache& cache, int64_t rows, int q_heads, int64_t seq_pages, int64_t window,
+                            int units) {
+  const int group = q_heads / cache.kv_heads, dim = cache.head_dim;
+  // as many of a head's queries at once as there are (a head's keys and values are read again for more), up to
+  // what the registers hold
+  const int most = dim > 128 ? 2 : 4;
+  AttnShape s;
+  s.row_tiles = group <= 16 ? 1 : group <= 32 || most == 2 ? 2 : 4;
+  // the grid: what the compute units hold at once
+  s.grid = std::min(units, kWsCounters / 17) * (s.row_tiles == 1 && dim <= 128 ? 2 : 1);
+  const int queries = std::min(group, 16 * s.row_tiles);
+  s.slot_bytes = (queries * (dim + 4) * 4 + 15) / 16 * 16;
+  const int64_t splits = (group + 16 * s.row_tiles - 1) / (16 * s.row_tiles), room = seq_pages * cache.page_size;
+  s.row_most = ((window > 0 && window < room ? window : room) / 32 + 2) * cache.kv_heads * splits;
+  // Results wait in the workspace where a row is split: at most four for every workgroup, and fewer than half as many
+  // as there are tiles, since a part of a split row has four tiles or more but for the last
+  const int64_t slots = std::min<int64_t>(4 * s.grid, std::max<int64_t>(1, rows * s.row_most / 2));
+  s.ws_bytes = slots * s.slot_bytes;
+  return s;
+}
+
+}  // namespace agg
 
 using namespace agg;
 
@@ -65,15 +91,36 @@ int check_cache(const agg_kv_cache* c) {
   return AGG_OK;
 }
 
+// (positions are 32-bit)
+int check_table_size(const agg_kv_cache* c, int64_t seq_pages) {
+  if (seq_pages > kMostRows || seq_pages * c->page_size > kMostRows)
+    return fail(AGG_E_UNSUPPORTED, "a table's row of %lld pages is beyond 2^30 positions", (long long)seq_pages);
+  return AGG_OK;
+}
+
 int check_table(const agg_kv_cache* c, const int32_t* table, int64_t seqs, int64_t seq_pages, int64_t ld_table) {
   if (seqs < 0 || seq_pages < 0) return fail(AGG_E_ARG, "negative size");
-  // (positions are 32-bit)
-  if (seqs > kMostRows || seq_pages > kMostRows || seq_pages * c->page_size > kMostRows)
-    return fail(AGG_E_UNSUPPORTED, "%lld sequences of %lld pages are beyond 2^30 sequences or positions", (long long)seqs, (long long)seq_pages);
+  if (seqs > kMostRows) return fail(AGG_E_UNSUPPORTED, "%lld sequences are beyond 2^30", (long long)seqs);
+  CHECK(check_table_size(c, seq_pages));
   if (seqs == 0 || seq_pages == 0) return AGG_OK;
   if (seqs > 1 && ld_table < seq_pages) return fail(AGG_E_ARG, "ld_table %lld is below the %lld pages", (long long)ld_table, (long long)seq_pages);
   if (ld_table > kMostStride) return fail(AGG_E_UNSUPPORTED, "ld_table is beyond 2^31");
   return need(table, "table", 4);
+}
+
+// what paged_attn divides its work by
+int check_attn_sizes(const agg_kv_cache* c, int64_t rows, int q_heads, int64_t seq_pages, int64_t window) {
+  if (rows < 0 || window < 0 || seq_pages < 0) return fail(AGG_E_ARG, "negative size");
+  CHECK(check_cache(c));
+  if (q_heads < 1 || q_heads > AGG_MAX_HEADS || q_heads % c->kv_heads)
+    return fail(AGG_E_ARG, "%d heads of queries: a multiple of the cache's %d up to %d is wanted", q_heads, c->kv_heads, AGG_MAX_HEADS);
+  if (rows > kMostRows / 1024) return fail(AGG_E_UNSUPPORTED, "rows beyond 2^20");
+  CHECK(check_table_size(c, seq_pages));
+  // (the tiles of a row are counted in 31 bits)
+  const int64_t room = seq_pages * c->page_size, splits = (q_heads / c->kv_heads + 15) / 16;
+  if (((window > 0 && window < room ? window : room) / 32 + 2) * c->kv_heads * splits >= (int64_t(1) << 31))
+    return fail(AGG_E_UNSUPPORTED, "%lld positions of %d heads are beyond 2^36", (long long)room, q_heads);
+  return AGG_OK;
 }
 
 }  // namespace
@@ -128,21 +175,22 @@ extern "C" int agg_check_paged_attn_args(const agg_kv_cache* cache, int64_t rows
                                          int64_t seqs, int64_t seq_pages, int64_t ld_table, int64_t window,
                                          int out_dtype, const void* out, int64_t ld_out) {
   clear_error();
-  if (rows < 0 || window < 0) return fail(AGG_E_ARG, "negative size");
-  CHECK(check_cache(cache));
-  if (q_heads < 1 || q_heads > AGG_MAX_HEADS || q_heads % cache->kv_heads)
-    return fail(AGG_E_ARG, "%d heads of queries: a multiple of the cache's %d up to %d is wanted", q_heads, cache->kv_heads, AGG_MAX_HEADS);
+  CHECK(check_attn_sizes(cache, rows, q_heads, seq_pages, window));
   if (!std::isfinite(scale) || !std::isfinite(scale * 1.442695041f)) return fail(AGG_E_ARG, "scale is not finite");
   if (out_dtype != AGG_BF16 && out_dtype != AGG_FP32) return fail(AGG_E_ARG, "out has dtype %d, not bf16 or fp32", out_dtype);
-  if (rows > kMostRows / 1024) return fail(AGG_E_UNSUPPORTED, "rows beyond 2^20");
   CHECK(check_table(cache, table, seqs, seq_pages, ld_table));
-  // (the tiles of a row are counted in 31 bits)
-  const int64_t room = seq_pages * cache->page_size, splits = (q_heads / cache->kv_heads + 15) / 16;
-  if (((window > 0 && window < room ? window : room) / 32 + 2) * cache->kv_heads * splits >= (int64_t(1) << 31))
-    return fail(AGG_E_UNSUPPORTED, "%lld positions of %d heads are beyond 2^36", (long long)room, q_heads);
   if (rows == 0) return AGG_OK;
   const int64_t cols = int64_t(q_heads) * cache->head_dim;
   CHECK(check_rows(q, ld_q, cols, 2, "q"));
   CHECK(check_rows(out, ld_out, cols, out_dtype == AGG_FP32 ? 4 : 2, "out"));
   return need(lens, "lens", 4);
+}
+
+extern "C" int agg_paged_attn_workspace(const agg_kv_cache* cache, int64_t rows, int q_heads, int64_t seq_pages,
+                                        int64_t window, int64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(AGG_E_ARG, "agg_paged_attn_workspace: NULL output");
+  CHECK(check_attn_sizes(cache, rows, q_heads, seq_pages, window));
+  *bytes = rows == 0 ? 0 : choose_attn_shape(*cache, rows, q_heads, seq_pages, window, 256).ws_bytes;
+  return AGG_OK;
 }

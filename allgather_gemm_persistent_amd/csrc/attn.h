@@ -52,7 +52,7 @@ struct AttnArgs {
   int row_tiles;              // 16-row tiles of a head's queries a workgroup takes at once (1, 2, 4)
   int out_fp32;
   int least;                  // tiles of a unit at least
-  float* ws;                  // four slots of slot_bytes for every workgroup
+  float* ws;                  // slots of slot_bytes for the parts of the rows that are split
   int64_t ws_bytes;
   int slot_bytes;
   uint32_t* counts;           // eight for every workgroup and two, zero before and after

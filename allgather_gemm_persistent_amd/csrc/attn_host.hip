@@ -74,14 +74,10 @@ extern "C" int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows,
     return rc;
   if (int rc = enter(ctx)) return rc;
   if (rows == 0) return AGG_OK;
-  const int group = q_heads / cache->kv_heads;
-  // as many of a head's queries at once as there are (a head's keys and values are read again for more), up to
-  // what the registers hold
-  const int most = cache->head_dim > 128 ? 2 : 4;
-  const int tiles = group <= 16 ? 1 : group <= 32 || most == 2 ? 2 : 4;
+  const AttnShape shape = choose_attn_shape(*cache, rows, q_heads, seq_pages, window, ctx_units(ctx));
   AttnArgs a{without_idle_strides(*cache), static_cast<const uint16_t*>(q), out, lse, lens, row_seq, table, seqs,
-             seq_pages, ld_table, rows, 0, ld_q, ld_out, window, scale * 1.442695041f, q_heads, group, tiles,
-             out_dtype == AGG_FP32, kAttnLeast, nullptr, 0, 0, nullptr, 0, 0};
+             seq_pages, ld_table, rows, 0, ld_q, ld_out, window, scale * 1.442695041f, q_heads, q_heads / cache->kv_heads,
+             shape.row_tiles, out_dtype == AGG_FP32, kAttnLeast, nullptr, shape.ws_bytes, shape.slot_bytes, nullptr, 0, 0};
   // runs of 16 tokens to pages: with 2^s <= d < 2^(s+1) and magic = ceil(2^(31+s) / d), magic * d is less than d above
   // 2^(31+s), so x * magic >> (31+s) is x / d while x * 2^(s+1) stays below 2^(31+s)
   const uint32_t d = uint32_t(cache->page_size) / 16;
@@ -89,17 +85,9 @@ extern "C" int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows,
   while (d >> (s + 1)) ++s;
   a.page_magic = uint32_t(((uint64_t(1) << (31 + s)) + d - 1) / d);
   a.page_shift = uint32_t(31 + s);
-  // the grid: what the compute units hold at once; and the workspace of its units
-  const int units = ctx_units(ctx) < kWsCounters / 17 ? ctx_units(ctx) : kWsCounters / 17;
-  const int grid = units * (tiles == 1 && cache->head_dim <= 128 ? 2 : 1);
-  const int queries = group < 16 * tiles ? group : 16 * tiles;
-  a.slot_bytes = (queries * (cache->head_dim + 4) * 4 + 15) / 16 * 16;
-  a.ws_bytes = int64_t(4) * grid * a.slot_bytes;
   if (int rc = ctx_moe_workspace(ctx, stream, size_t(a.ws_bytes), &a.ws, &a.counts)) return rc;
   // (a launch counts its tiles in 31 bits)
-  const int64_t splits = (group + 16 * tiles - 1) / (16 * tiles), room = seq_pages * cache->page_size;
-  const int64_t row_most = ((window > 0 && window < room ? window : room) / 32 + 2) * cache->kv_heads * splits;
-  const int64_t at_once = ((int64_t(1) << 31) - 1) / row_most;
+  const int64_t at_once = ((int64_t(1) << 31) - 1) / shape.row_most;
   for (int64_t r = 0; r < rows; r += at_once) {
     AttnArgs p = a;
     p.rows = rows - r < at_once ? rows - r : at_once;
@@ -109,7 +97,7 @@ extern "C" int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows,
     if (lse) p.lse += r * q_heads;
     p.lens += r;
     if (row_seq) p.row_seq += r;
-    HIP_TRY(launch_attn(p, grid, S(stream)));
+    HIP_TRY(launch_attn(p, shape.grid, S(stream)));
   }
   return AGG_OK;
 }

@@ -114,6 +114,16 @@ LinearShape split_linear(int dtype, int64_t m, int64_t n, int64_t k, TileShape t
 // The parts of K that agg_ctx_set_split asks for; 0: the library's choice.
 int ctx_forced_split(const agg_ctx* ctx);
 
+// How paged_attn divides a call on `units` compute units: a head's queries in 16-row tiles, row_tiles of them at once;
+// the workgroups; the tiles of 32 tokens that a row can have at most, over its heads; and the workspace, slots of
+// slot_bytes.
+struct AttnShape {
+  int row_tiles, grid, slot_bytes;
+  int64_t row_most, ws_bytes;
+};
+AttnShape choose_attn_shape(const agg_kv_cache& cache, int64_t rows, int q_heads, int64_t seq_pages, int64_t window,
+                            int units);
+
 ExpertShape choose_expert_shape(int dtype, int64_t slots, int n_experts, int64_t n, int64_t k, int gated,
                                 int units);
 

@@ -661,9 +661,10 @@ int moe_combine(agg_ctx* ctx, int64_t tokens, int top_k, int64_t n, int64_t slot
  *
  * Every call launches one kernel on `stream` (kv_write and kv_read one for each 2^23 tokens, paged_attn one for
  * each 2^31 / (heads of the cache times positions of a table's row over 32) rows) and is capturable. Of the ctx they
- * use its device and, in paged_attn, a workspace of the stream or capture, as moe_gemm does (4 results of a head's queries
- * for every workgroup: 9 MiB for 8 heads of 128, up to 70 for 64): nothing else is allocated, calls on several streams and
- * graphs do not meet, two replays of one capture must not run at once. Rows (q, k, v, the outputs, the cache and its
+ * use its device and, in paged_attn, a workspace of the stream or capture, as moe_gemm does: agg_paged_attn_workspace bytes in
+ * a capture (8.3 MiB at most for 8 queries a head of 128, 33 for 64, little for a few short rows), eagerly the next power of two
+ * from 8 MiB. Every capture's stays until the ctx is destroyed; calls of one ctx share it. Nothing else is allocated, calls
+ * on several streams and graphs do not meet, two replays of one capture must not run at once. Rows (q, k, v, the outputs, the cache and its
  * scales) are 16-byte aligned, positions, lengths, sequences and tables 4-byte. What a call reads must not change while it
  * runs. No floating-point atomics.
  * Passage: none (the pages give no attention; the formulas are the plain definitions stated here).
@@ -902,6 +903,13 @@ int agg_check_linear_args(int64_t m, int64_t n, int64_t k, int dtype, const void
  * without work still name a kernel.
  */
 int agg_linear_shape(int dtype, int64_t m, int64_t n, int64_t k, int* ksplit, int* bm, int* bn);
+
+/* Bytes of the workspace that paged_attn takes for a call on a whole MI355X, beside 32 KiB of counters: at most four results
+ * of a head's queries for every workgroup, and fewer where the rows, which a table's row and the window bound, have fewer parts.
+ * Sizes that paged_attn refuses are refused.
+ */
+int agg_paged_attn_workspace(const agg_kv_cache* cache, int64_t rows, int q_heads, int64_t seq_pages, int64_t window,
+                             int64_t* bytes);
 
 /* How moe_gemm multiplies a call on a whole MI355X: *ksplit > 0: the weights streamed through
  * registers, K in that many parts (then *bm = *bn = 0); *ksplit 0: tiles of *bm x *bn. Sizes that

@@ -178,3 +178,64 @@ def test_binding_refuses_what_the_call_would_read_wrongly():
     _refused(lambda: B.paged_attn(None, cache, 0, q[:, :100], pos, table[:, :0], q, scale=1.0))    # no whole heads
     _refused(lambda: B.paged_attn(None, cache, 0, q.float(), pos, table[:, :0], q, scale=1.0))
     _refused(lambda: B.paged_attn(None, cache, 3, q[:0], pos, table[:2, :0], q, scale=1.0, row_seq=None))
+
+
+# ------------------------------------------------------------------------------ paged_attn's workspace
+
+def _workspace(lib, rows, q_heads, seq_pages, window=0, **kw):
+    n = ctypes.c_int64(-1)
+    c = _cache(**kw)
+    assert lib.agg_paged_attn_workspace(_ref(c), rows, q_heads, seq_pages, window, ctypes.byref(n)) == B.AGG_OK, B.last_error()
+    return n.value
+
+
+@pytest.mark.parametrize("rows,q_heads,kv_heads,dim,seq_pages,window,most", [
+    # (rows * heads * (positions / 32 + 2) / 2 results of a head's queries, dim + 4 floats a query)
+    (0, 8, 1, 128, 100, 0, 0), (1, 8, 1, 128, 1, 0, 1 * 4224), (1, 8, 1, 128, 32, 0, 9 * 4224),
+    (16, 64, 8, 128, 4, 0, 256 * 4224), (16, 64, 8, 128, 1 << 20, 64, 256 * 4224), (64, 1, 1, 64, 2, 0, 96 * 272),
+    (1 << 20, 1024, 16, 128, 1 << 15, 0, 4 * 256 * 64 * 528)])                                     # four a workgroup
+def test_the_workspace_is_no_more_than_the_rows_can_need(lib, rows, q_heads, kv_heads, dim, seq_pages, window, most):
+    """Every capture keeps one as long as its ctx lives."""
+    kw = dict(kv_heads=kv_heads, head_dim=dim, ld_head=dim, ld_token=dim * kv_heads, ld_page=16 * dim * kv_heads)
+    assert _workspace(lib, rows, q_heads, seq_pages, window, **kw) <= most
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(8, 1, 128), (64, 8, 128), (20, 20, 80), (33, 1, 64), (130, 2, 256)])
+def test_the_workspace_holds_every_plan(lib, q_heads, kv_heads, dim):
+    """The kernel cuts a row of t tiles into ceil(t / s) parts, s one of some multiples of an even share of all tiles and four
+    at least, or, where there is a workgroup for every tile, a 32nd of the longest row and four at least; a row of one
+    part takes no place. Whatever the lengths, the places of all parts are inside the workspace."""
+    import random
+    rng = random.Random(q_heads + dim)
+    group = q_heads // kv_heads
+    tiles16 = 1 if group <= 16 else 2 if group <= 32 or dim > 128 else 4
+    grid = 256 * (2 if tiles16 == 1 and dim <= 128 else 1)
+    items = -(-group // (16 * tiles16)) * kv_heads
+    slot = min(group, 16 * tiles16) * (dim + 4) * 4
+    kw = dict(kv_heads=kv_heads, head_dim=dim, ld_head=dim, ld_token=dim * kv_heads, ld_page=16 * dim * kv_heads)
+    for _ in range(400):
+        rows, room = int(2 ** rng.uniform(0, 9)), 16 * int(2 ** rng.uniform(0, 13))
+        window = rng.choice([0, 0, int(2 ** rng.uniform(0, 14))])
+        lens = [rng.choice([room, rng.randint(0, room), int(2 ** rng.uniform(0, 17)) % (room + 1)]) for _ in range(rows)]
+        tiles = []
+        for n in lens:
+            lo = max(0, n - window) if window else 0
+            tiles.append(-(-n // 32) - lo // 32 if n > lo else 1)
+        total = sum(tiles) * items
+        some = max(4, -(-total // grid))
+        sizes = {max(4, -(-some * q // 4)) for q in (2, 4, 5, 6, 8, 16)}
+        if rows <= 64 and total <= grid:
+            sizes = {max(tiles)} if max(tiles) <= 8 else {max(4, -(-max(tiles) // 32))}
+        held = _workspace(lib, rows, q_heads, room // 16, window, **kw) // slot
+        for s in sizes:
+            parts = [-(-t // s) for t in tiles]
+            assert sum(p for p in parts if p > 1) * items <= held, (rows, room, window, s)
+
+
+def test_the_workspace_of_refused_sizes(lib):
+    n = ctypes.c_int64()
+    c = _cache()
+    for args in ((_ref(c), -1, 2, 4, 0), (_ref(c), 1, 3, 4, 0), (_ref(c), 1, 2, -4, 0), (_ref(c), 1, 2, 4, -1), (None, 1, 2, 4, 0),
+                 (_ref(c), (1 << 20) + 1, 2, 4, 0), (_ref(c), 1, 2, 1 << 62, 0)):
+        assert lib.agg_paged_attn_workspace(*args, ctypes.byref(n)) != B.AGG_OK and B.last_error()
+    assert lib.agg_paged_attn_workspace(_ref(c), 1, 2, 4, 0, None) == B.AGG_E_ARG

@@ -183,3 +183,54 @@ def test_layers_on_streams_at_once(gpu):
     finally:
         for z in layers:
             z.close()
+
+
+def test_layers_that_share_a_ctx(gpu):
+    """Layers of several sizes on one ctx, eager, in two graphs replayed in turn, and after one of them is closed: what
+    they give on their own."""
+    ctx = B.agg_ctx_create(0)
+    sizes = [(8, 2, 64), (12, 1, 128), (4, 4, 64)]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    make = lambda i, **kw: attn_layer.random_layer(4, 256, *sizes[i], 4 * 60, positions=960, seed=i, page_size=16, **kw)  # noqa: E731
+    shared, own = [make(i, ctx=ctx) for i in range(3)], [make(i) for i in range(3)]
+    table = torch.arange(240, **i32).reshape(4, 60)
+    x = torch.randn(4, 256, device="cuda")
+    lens, pos = torch.zeros(4, **i32), torch.zeros(4, **i32)
+
+    def set_lens(*n):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        pos.copy_(lens - 1)
+
+    try:
+        for a, b in zip(shared, own):
+            for c in ("k", "v"):
+                getattr(a.cache, c).normal_()
+                getattr(b.cache, c).copy_(getattr(a.cache, c))
+        set_lens(1, 960, 17, 300)
+        run = lambda layers: [z.run(x, pos, lens, table).clone() for z in layers]  # noqa: E731
+        for a, b in zip(run(shared), run(own)):
+            assert torch.equal(a, b)
+        graphs, outs = [], []
+        for part in (shared, shared[1:]):
+            torch.cuda.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                outs.append([z.run(x, pos, lens, table) for z in part])
+        for i, n in enumerate([(5, 700, 18, 301), (6, 701, 19, 960), (7, 2, 20, 303), (960, 960, 959, 958)]):
+            set_lens(*n)
+            x.normal_()
+            want = run(own)
+            torch.cuda.synchronize()
+            graphs[i % 2].replay()
+            torch.cuda.synchronize()
+            for a, b in zip(outs[i % 2], want[i % 2:]):
+                assert torch.equal(a, b), i
+            if i % 2:                                     # (the first layer's cache did not get the row: it runs alone)
+                assert torch.equal(shared[0].run(x, pos, lens, table), want[0])
+        shared[0].close()
+        assert shared[0].ctx is None
+        assert torch.equal(shared[1].run(x, pos, lens, table), own[1].run(x, pos, lens, table))
+    finally:
+        for z in shared + own:
+            z.close()
+        B.agg_ctx_destroy(ctx)
