@@ -20,6 +20,11 @@ int enter(const agg_ctx* ctx) {
   return AGG_OK;
 }
 
+// an array of words that may be missing
+int check_words(const void* p, const char* what) {
+  return reinterpret_cast<uintptr_t>(p) & 3 ? fail(AGG_E_ARG, "%s is not 4-byte aligned", what) : AGG_OK;
+}
+
 constexpr int kAttnLeast = 4;   // 32-token tiles: one for each wave
 
 // (a dimension of one element may come with any stride: none is taken)
@@ -40,6 +45,7 @@ extern "C" int kv_write(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens,
   if (int rc = agg_check_kv_write_args(cache, tokens, q_heads, q, ld_q, q_out, ld_q_out, k, ld_k, v, ld_v, rope, rope_rows,
                                        rope_dim, rope_pairs, positions, table, seqs, seq_pages, ld_table))
     return rc;
+  if (int rc = tokens > 0 ? check_words(token_seq, "token_seq") : AGG_OK) return rc;
   if (int rc = enter(ctx)) return rc;
   // (no sequence, page or table: no token has a place)
   if (tokens == 0 || seqs == 0 || seq_pages == 0 || cache->pages == 0) return AGG_OK;
@@ -57,6 +63,7 @@ extern "C" int kv_read(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens, 
   if (int rc = agg_check_kv_read_args(cache, tokens, positions, table, seqs, seq_pages, ld_table, out_dtype, k_out, ld_k,
                                       v_out, ld_v))
     return rc;
+  if (int rc = tokens > 0 ? check_words(token_seq, "token_seq") : AGG_OK) return rc;
   if (int rc = enter(ctx)) return rc;
   if (tokens == 0) return AGG_OK;
   const KvReadArgs a{without_idle_strides(*cache), {positions, token_seq, table, seqs, seq_pages, ld_table, 0}, k_out, v_out,
@@ -72,6 +79,10 @@ extern "C" int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows,
   if (int rc = agg_check_paged_attn_args(cache, rows, q_heads, q, ld_q, scale, lens, table, seqs, seq_pages, ld_table,
                                          window, out_dtype, out, ld_out))
     return rc;
+  if (rows > 0) {
+    if (int rc = check_words(row_seq, "row_seq")) return rc;
+    if (int rc = check_words(lse, "lse")) return rc;
+  }
   if (int rc = enter(ctx)) return rc;
   if (rows == 0) return AGG_OK;
   const AttnShape shape = choose_attn_shape(*cache, rows, q_heads, seq_pages, window, ctx_units(ctx));

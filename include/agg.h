@@ -665,7 +665,7 @@ int moe_combine(agg_ctx* ctx, int64_t tokens, int top_k, int64_t n, int64_t slot
  * a capture (8.3 MiB at most for 8 queries a head of 128, 33 for 64, little for a few short rows), eagerly the next power of two
  * from 8 MiB. Every capture's stays until the ctx is destroyed; calls of one ctx share it. Nothing else is allocated, calls
  * on several streams and graphs do not meet, two replays of one capture must not run at once. Rows (q, k, v, the outputs, the cache and its
- * scales) are 16-byte aligned, positions, lengths, sequences and tables 4-byte. What a call reads must not change while it
+ * scales) are 16-byte aligned, positions, lengths, sequences, tables and lse 4-byte. What a call reads must not change while it
  * runs. No floating-point atomics.
  * Passage: none (the pages give no attention; the formulas are the plain definitions stated here).
  */

@@ -239,3 +239,20 @@ def test_the_workspace_of_refused_sizes(lib):
                  (_ref(c), (1 << 20) + 1, 2, 4, 0), (_ref(c), 1, 2, 1 << 62, 0)):
         assert lib.agg_paged_attn_workspace(*args, ctypes.byref(n)) != B.AGG_OK and B.last_error()
     assert lib.agg_paged_attn_workspace(_ref(c), 1, 2, 4, 0, None) == B.AGG_E_ARG
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_optional_arrays_that_are_not_aligned_are_refused(lib, off):
+    """The sequences of the tokens or rows, and the logarithms of the sums: words of four bytes, as every array here."""
+    c, rows = _cache(), (FAKE, 128)
+    for what, call in (
+            ("token_seq", lambda p, n: lib.kv_write(None, _ref(c), n, 0, None, 0, None, 0, *rows, *rows, None, 0, 0, 0, FAKE, p,
+                                                    FAKE, 4, 8, 8, None)),
+            ("token_seq", lambda p, n: lib.kv_read(None, _ref(c), n, FAKE, p, FAKE, 4, 8, 8, B.AGG_BF16, *rows, *rows, None)),
+            ("row_seq", lambda p, n: lib.paged_attn(None, _ref(c), n, 2, *rows, 0.1, FAKE, p, FAKE, 4, 8, 8, 0, B.AGG_BF16, *rows,
+                                                    None, None)),
+            ("lse", lambda p, n: lib.paged_attn(None, _ref(c), n, 2, *rows, 0.1, FAKE, None, FAKE, 4, 8, 8, 0, B.AGG_BF16, *rows,
+                                                p, None))):
+        assert call(FAKE + off, 4) == B.AGG_E_ARG and what in B.last_error(), what
+        assert call(FAKE + 4, 4) == B.AGG_E_ARG and "ctx" in B.last_error(), what          # (only the ctx is missing)
+        assert call(FAKE + off, 0) == B.AGG_E_ARG and "ctx" in B.last_error(), what        # (no tokens: not looked at)
