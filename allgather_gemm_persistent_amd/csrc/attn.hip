@@ -114,7 +114,6 @@ template <bool FP8, int DP, int RT, bool OUT32, bool NT>
 __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_kernel(const AttnArgs a) {
   constexpr int EL = FP8 ? 1 : 2;
   constexpr int PARTS = OUT32 ? 3 : 2;         // of the weights
-  constexpr int kRead = NT ? 2 : 0;            // cache policy of the keys' and values' loads
   constexpr int KS = DP / 32;                  // contraction steps of the first product
   constexpr int VE = DP / 16;                  // channels of V a lane holds
   constexpr int KL = DP * EL / 64;             // 16-byte loads of a token's keys by a lane
@@ -307,6 +306,9 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
   };
   const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(a.ws, 0, (int)a.ws_bytes, kBufferFlags);
 
+  // everything from here on, with the cache policy of the keys' and values' loads
+  auto attend = [&](auto policy) {
+  constexpr int kRead = decltype(policy)::value;
   // offsets of this lane in a run of 16 tokens
   const uint32_t token_bytes = (uint32_t)(cache.ld_token * EL);
   uint32_t koff[KL];
@@ -746,6 +748,18 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && DP <= 128 ? 2 : 1) attn_k
     __hip_atomic_store(claimed, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_store(claimed + 1, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  };
+
+  // Non-temporal where the call reads more than the last level's 256 MB can hold, each token once: not more tokens than the
+  // pool has, which rows that share pages would (measured at the launch, below)
+  if constexpr (NT) {
+    const float token = 2.0f * (float)(cache.kv_heads * D * EL), held = (float)cache.pages * (float)pg;
+    if ((float)all_tiles[0] * (kTile * token) > 256e6f && (float)(all_tiles[0] - rows) * kTile <= held) {
+      attend(std::integral_constant<int, 2>{});
+      return;
+    }
+  }
+  attend(std::integral_constant<int, 0>{});
 }
 
 template <bool FP8, int DP, int RT, bool NT>
@@ -758,15 +772,18 @@ static hipError_t launch_attn_nt(const AttnArgs& a, int grid, hipStream_t stream
 
 template <bool FP8, int DP, int RT>
 static hipError_t launch_attn_rt(const AttnArgs& a, int grid, hipStream_t stream) {
-  // A cache that the last level's 256 MB cannot hold is read once and not kept there (non-temporal), if its lines of 128
-  // bytes are one head's each and neighbours: 4 x 131072 tokens of 8 bits, heads first, 201 -> 186 us; 32 x 8000 of 16
-  // heads of 64 bf16, heads first, 180 -> 161; 256 wide 171 -> 163. Where a line is asked for in parts at different
-  // times it costs: 80 wide 347 -> 420, tokens first 8 bits of 128 118 -> 124, bf16 of 128 189 and 188. More queries than
-  // 16 to a head of the cache: what one workgroup reads another may
+  // Non-temporal reads keep a cache that the last level's 256 MB cannot hold out of it. They pay where the lines of 128 bytes
+  // are one head's each and neighbours, and every line is read once: 4 x 131072 tokens of 8 bits, heads first, 203 -> 189 us;
+  // 32 x 8000 bf16 185 -> 170; 32 x 8000 of 16 heads of 64 bf16 180 -> 161; 256 wide 171 -> 163. Where a line is asked
+  // for in parts at different times they cost: 80 wide 347 -> 420, tokens first 8 bits of 128 118 -> 124, bf16 of 128 189 and
+  // 188. So they do where rows share pages (64 x 8000, 7200 shared, 151 -> 194; 32 x 32000, all but 160 shared, 285 -> 440), and
+  // a little where a call reads little of a large pool (16 x 2000 bf16 27.5 -> 29.1): the kernel, which knows the lengths,
+  // leaves them out there. Rows that share pages of a pool that could hold them apart are not told (32 x 16000 in 8 bits, 15200
+  // shared, 120 -> 130). More queries than 16 to a head of the cache: what one workgroup reads another may
   if constexpr (RT == 1) {
     const int row = a.cache.head_dim * (FP8 ? 1 : 2);
     const double bytes = 2.0 * (double)a.cache.pages * a.cache.page_size * a.cache.kv_heads * row;
-    if (bytes > 256e6 && a.group <= 16 && row % 128 == 0 && (a.cache.ld_token == a.cache.head_dim || row >= 512))
+    if (bytes > 256e6 && row % 128 == 0 && (a.cache.ld_token == a.cache.head_dim || row >= 512))
       return launch_attn_nt<FP8, DP, 1, true>(a, grid, stream);
   }
   return launch_attn_nt<FP8, DP, RT, false>(a, grid, stream);

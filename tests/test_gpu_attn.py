@@ -724,3 +724,15 @@ def test_decode_steps_in_replayed_graphs(ctx, dtype):
         torch.cuda.synchronize()
         assert torch.equal(bufs[name][1], want), i
         assert bool(want.isfinite().all()) and float(want.abs().max()) > 0
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("fp8", 128), ("bf16", 64)])
+def test_attn_of_all_of_a_large_cache(ctx, dtype, dim):
+    """A pool beyond the last level's size read whole, its sequences read by two rows each, and only one of them: the kernel
+    tells them apart by the lengths, and reads them with other cache policies."""
+    heads = 2
+    n = int(270e6 / (2 * heads * dim * (2 if dtype == "bf16" else 1))) // 6
+    p = _Paged([n] * 5 + [n + 21], heads, dim, 64, dtype, heads_first=True, seed=dim)
+    _check(p, ctx, 8)
+    _check(p, ctx, 8, lens=[n] * 10, row_seq=[0, 1, 2, 3, 4] * 2)
+    _check(p, ctx, 8, lens=[n + 20, 100], row_seq=[5, 1])
