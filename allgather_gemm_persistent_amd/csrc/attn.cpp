@@ -6,6 +6,11 @@
 
 namespace agg {
 
+// compute units that paged_attn counts on: up to 512 workgroups, so that a row's parts (two a workgroup at most) are joined
+// in two steps of 32, and the counters (eight a workgroup and two) suffice
+constexpr int kAttnUnits = 256;
+static_assert(16 * kAttnUnits + 2 <= kWsCounters, "paged_attn's counters");
+
 AttnShape choose_attn_shape(const agg_kv_cache& cache, int64_t rows, int q_heads, int64_t seq_pages, int64_t window,
                             int units) {
   const int group = q_heads / cache.kv_heads, dim = cache.head_dim;
@@ -15,7 +20,7 @@ AttnShape choose_attn_shape(const agg_kv_cache& cache, int64_t rows, int q_heads
   AttnShape s;
   s.row_tiles = group <= 16 ? 1 : group <= 32 || most == 2 ? 2 : 4;
   // the grid: what the compute units hold at once
-  s.grid = std::min(units, kWsCounters / 17) * (s.row_tiles == 1 && dim <= 128 ? 2 : 1);
+  s.grid = std::min(units, kAttnUnits) * (s.row_tiles == 1 && dim <= 128 ? 2 : 1);
   const int queries = std::min(group, 16 * s.row_tiles);
   s.slot_bytes = (queries * (dim + 4) * 4 + 15) / 16 * 16;
   const int64_t splits = (group + 16 * s.row_tiles - 1) / (16 * s.row_tiles), room = seq_pages * cache.page_size;

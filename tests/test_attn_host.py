@@ -230,6 +230,7 @@ def test_the_workspace_holds_every_plan(lib, q_heads, kv_heads, dim):
         for s in sizes:
             parts = [-(-t // s) for t in tiles]
             assert sum(p for p in parts if p > 1) * items <= held, (rows, room, window, s)
+            assert max(parts) <= 32 * 32, (rows, room, window, s)      # (what two steps join)
 
 
 def test_the_workspace_of_refused_sizes(lib):
