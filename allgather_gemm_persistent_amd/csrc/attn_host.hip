@@ -26,6 +26,7 @@ int check_words(const void* p, const char* what) {
 }
 
 constexpr int kAttnLeast = 4;   // 32-token tiles: one for each wave
+constexpr int64_t kAttnRows = 2048;   // of a launch
 
 // (a dimension of one element may come with any stride: none is taken)
 agg_kv_cache without_idle_strides(const agg_kv_cache& c) {
@@ -97,8 +98,10 @@ extern "C" int paged_attn(agg_ctx* ctx, const agg_kv_cache* cache, int64_t rows,
   a.page_magic = uint32_t(((uint64_t(1) << (31 + s)) + d - 1) / d);
   a.page_shift = uint32_t(31 + s);
   if (int rc = ctx_moe_workspace(ctx, stream, size_t(a.ws_bytes), &a.ws, &a.counts)) return rc;
-  // (a launch counts its tiles in 31 bits)
-  const int64_t at_once = ((int64_t(1) << 31) - 1) / shape.row_most;
+  // (a launch counts its tiles in 31 bits; and a workgroup finds a unit's row by walking up to a 256th of the launch's rows, so
+  // that time would grow with the square of them: 64 heads on 8, rows of 16 tokens, in one launch 241 us for 2048, 1668 for 8192,
+  // 17245 for 32768; in launches of 2048 982 and 3914)
+  const int64_t most = ((int64_t(1) << 31) - 1) / shape.row_most, at_once = most < kAttnRows ? most : kAttnRows;
   for (int64_t r = 0; r < rows; r += at_once) {
     AttnArgs p = a;
     p.rows = rows - r < at_once ? rows - r : at_once;

@@ -659,8 +659,8 @@ int moe_combine(agg_ctx* ctx, int64_t tokens, int top_k, int64_t n, int64_t slot
  * page: its positions cannot be written, read as zeros, and are left out of the attention. Sequences
  * may share pages (a common prefix).
  *
- * Every call launches one kernel on `stream` (kv_write and kv_read one for each 2^23 tokens, paged_attn one for
- * each 2^31 / (heads of the cache times positions of a table's row over 32) rows) and is capturable. Of the ctx they
+ * Every call launches one kernel on `stream` (kv_write and kv_read one for each 2^23 tokens, paged_attn one for each 2048 rows,
+ * or 2^31 / (heads of the cache times positions of a table's row over 32) if that is fewer) and is capturable. Of the ctx they
  * use its device and, in paged_attn, a workspace of the stream or capture, as moe_gemm does: agg_paged_attn_workspace bytes in
  * a capture (8.3 MiB at most for 8 queries a head of 128, 33 for 64, little for a few short rows), eagerly the next power of two
  * from 8 MiB. Every capture's stays until the ctx is destroyed; calls of one ctx share it. Nothing else is allocated, calls

@@ -736,3 +736,15 @@ def test_attn_of_all_of_a_large_cache(ctx, dtype, dim):
     _check(p, ctx, 8)
     _check(p, ctx, 8, lens=[n] * 10, row_seq=[0, 1, 2, 3, 4] * 2)
     _check(p, ctx, 8, lens=[n + 20, 100], row_seq=[5, 1])
+
+
+@pytest.mark.parametrize("rows", [2047, 2048, 2049, 5000])
+@pytest.mark.parametrize("named", [False, True])
+def test_attn_rows_around_a_launch(ctx, rows, named):
+    """More rows than a launch takes: every row's own length and sequence, by its number or by name, one of them long."""
+    g = _gen(rows)
+    lengths = [int(x) for x in torch.randint(0, 24, (rows,), generator=g)]
+    lengths[rows - 2] = 3000
+    p = _Paged(lengths, 1, 16, 16, "bf16", seed=rows)
+    order = torch.randperm(rows, generator=g).tolist() if named else list(range(rows))
+    _check(p, ctx, 2, lens=[lengths[s] for s in order], row_seq=order if named else None, out="fp32")
