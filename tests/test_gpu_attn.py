@@ -748,3 +748,44 @@ def test_attn_rows_around_a_launch(ctx, rows, named):
     p = _Paged(lengths, 1, 16, 16, "bf16", seed=rows)
     order = torch.randperm(rows, generator=g).tolist() if named else list(range(rows))
     _check(p, ctx, 2, lens=[lengths[s] for s in order], row_seq=order if named else None, out="fp32")
+
+
+def _in_parts(w, parts):
+    """w as the sum of so many bfloat16 numbers, each the nearest to what the ones before leave."""
+    total = torch.zeros_like(w)
+    for _ in range(parts):
+        total = total + (w - total).bfloat16().double()
+    return total
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("group,dim", [(1, 64), (8, 128), (24, 128), (48, 64), (16, 256), (32, 256)])
+def test_attn_fp32_results_have_the_whole_weights(ctx, dtype, group, dim):
+    """Two tokens, the second with weight w = e^x, -2 <= x < 0, and the values 0 and 1: out = w / (1 + w). The products are
+    exact, and the steps' errors, in units of 2^-24 of the result (half a unit of a float): the score's scale and two
+    products 3 |x| <= 6, v_exp 2, the weight's three parts 1, their sum in the matrix unit 6, 1 + w and the division and the
+    product with it 3. In two parts a weight is up to 2^-17 of itself off, 128 units, which is seen."""
+    rows, heads = 64, group
+    p = _Paged([2] * rows, 1, dim, 16, dtype, seed=group)
+    for x, second in ((p.k, -1.0), (p.v, 1.0)):
+        x.copy_(torch.zeros(x.shape).to(x.dtype))
+        at = p.table[:, 0].long().cuda()
+        if x is p.k:
+            x[at, 1, 0, 0] = second
+        else:
+            x[at, 1, 0] = torch.ones(dim, device="cuda").to(x.dtype)
+    if dtype == "fp8":
+        p.k_scale.fill_(1)
+        p.v_scale.fill_(1)
+    q = torch.zeros(rows, heads, dim)
+    q[..., 0] = 0.01 + 1.98 * torch.rand(rows, heads, generator=p.g)
+    q = q.bfloat16()
+    y = torch.zeros(rows, heads * dim, device="cuda")
+    B.paged_attn(ctx, p.cache, rows, q.reshape(rows, -1).cuda(), torch.full((rows,), 2, dtype=I32, device="cuda"), p.dev_table, y,
+                 scale=1.0, stream=torch.cuda.current_stream())
+    w = torch.exp(-q[..., 0].double())
+    want = w / (1 + w)
+    bound = want * 18 * 2.0 ** -24
+    two = _in_parts(w, 2) / (1 + w)
+    assert bool(((two - want).abs() > bound).any()), "weights in two parts would pass"
+    _within(y.reshape(rows, heads, dim), want[..., None].expand(rows, heads, dim), bound[..., None], "weights")

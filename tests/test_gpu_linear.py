@@ -319,3 +319,45 @@ def test_activations_keep_their_small_values(ctx, act, m, dtype, out):
     assert not bad.any(), (f"{int(bad.sum())} of {bad.numel()}; worst error over bound "
                            f"{float(((got - want).abs() / bound).nan_to_num(0).max()):.3g} at x = "
                            f"{float(z[((got - want).abs() / bound).nan_to_num(0).amax(0).argmax()])}")
+
+
+def _exact_product(m, n, k, dtype, seed):
+    """Operands of which every product and sum is a multiple of 1/4 below 2^17, so fp32 (and the fp8 instruction, which cuts
+    products to 2^-13 of the largest of eight: 4) holds them exactly; none is zero, so that none can be lost unseen."""
+    g = torch.Generator().manual_seed(seed)
+    values = torch.tensor([0.5, 1.0, 2.0, -0.5, -1.0, -2.0])
+    pick = lambda *s: values[torch.randint(0, 6, s, generator=g)]  # noqa: E731
+    a, b = pick(m, k), pick(k, n)
+    want = (a.cuda().double() @ b.cuda().double()).cpu()
+    if dtype == "bf16":
+        return a.bfloat16().cuda(), b.bfloat16().cuda(), None, None, want
+    sa, sb = (2.0 ** torch.randint(-3, 4, (x,), generator=g) for x in (m, n))
+    return a.to(FP8).cuda(), b.to(FP8).cuda(), sa.cuda(), sb.cuda(), want * sa.double()[:, None] * sb.double()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("m,n,k", [(1, 256, 4096), (3, 128, 1040), (16, 2048, 2048), (32, 1024, 8192), (33, 384, 1008), (64, 2048, 8192),
+                                   (100, 1040, 1008), (128, 512, 8192), (257, 1008, 4096), (300, 1808, 1040), (1024, 1024, 2048),
+                                   (2100, 2064, 1040)])
+def test_no_product_is_lost(ctx, dtype, m, n, k):
+    a, b, sa, sb, want = _exact_product(m, n, k, dtype, m + n + k)
+    y = torch.empty(m, n, device="cuda")
+    B.linear(ctx, m, n, k, dtype, a, b, y, a_scale=sa, b_scale=sb, stream=torch.cuda.current_stream())
+    assert torch.equal(y.double().cpu(), want)
+
+
+@pytest.mark.parametrize("tile", [(256, 256), (256, 224), (128, 128), (128, 64), (64, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("parts", [1, 3, 16])
+def test_no_product_is_lost_in_a_tile(ctx, dtype, tile, parts):
+    m, n, k = 321, 528, 2064
+    a, b, sa, sb, want = _exact_product(m, n, k, dtype, parts)
+    y = torch.empty(m, n, device="cuda")
+    B.agg_ctx_set_tile(ctx, *tile)
+    B.agg_ctx_set_split(ctx, parts)
+    try:
+        B.linear(ctx, m, n, k, dtype, a, b, y, a_scale=sa, b_scale=sb, stream=torch.cuda.current_stream())
+        assert torch.equal(y.double().cpu(), want)
+    finally:
+        B.agg_ctx_set_tile(ctx)
+        B.agg_ctx_set_split(ctx)
