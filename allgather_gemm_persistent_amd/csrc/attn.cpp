@@ -14,8 +14,10 @@ static_assert(16 * kAttnUnits + 2 <= kWsCounters, "paged_attn's counters");
 AttnShape choose_attn_shape(const agg_kv_cache& cache, int64_t rows, int q_heads, int64_t seq_pages, int64_t window,
                             int units) {
   const int group = q_heads / cache.kv_heads, dim = cache.head_dim;
-  // as many of a head's queries at once as there are (a head's keys and values are read again for more), up to
-  // what the registers hold
+  // as many of a head's queries at once as there are (a head's keys and values are read again for more), up to what the
+  // registers nearly hold: 33 to 64 of 128 channels in bf16 spill 27 to 38 registers, 17 and more of 256 channels 73. Half as
+  // many at once and a second reading spill none and cost where reading counts: 32 rows of 8000 tokens on 2 heads 65 -> 85 us
+  // (48 queries of 128), 128 -> 179 (24 of 256); they gain where joins do: 4 rows of 2000 on one head 42 -> 18, 47 -> 31
   const int most = dim > 128 ? 2 : 4;
   AttnShape s;
   s.row_tiles = group <= 16 ? 1 : group <= 32 || most == 2 ? 2 : 4;

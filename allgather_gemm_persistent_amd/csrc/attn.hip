@@ -103,9 +103,9 @@ __device__ inline uint32_t widen8(uint32_t p) {
 // from busy (32 tokens of 128 channels are 8 KiB of K and of V, and 24 or 32 matrix instructions).
 //
 // Bound by reading K and V once. A kernel that only reads reaches 6.9 TB/s on the whole GPU, a copy 5.1:
-//   4 rows of 131072 tokens, 8 heads of 128 in 8 bits (1.1 GB)             184 us    6.0 TB/s    matrix units 0.11 busy
-//   61 rows up to 4000 in a window of 1000, 20 heads of 80 (212 MB)     44 - 50 us    4.2 - 4.8 TB/s
-//   16 rows up to 8192, 64 heads on 8 of 128 (90 MB)                    25 - 28 us    3.2 - 3.6 TB/s
+//   4 rows of 131072 tokens, 8 heads of 128 in 8 bits (1.1 GB)             183 - 187 us    5.9 - 6.1 TB/s    matrix units 0.11 busy
+//   61 rows up to 4000 in a window of 1000, 20 heads of 80 (212 MB)     44 - 52 us    4.1 - 4.8 TB/s
+//   16 rows up to 8192, 64 heads on 8 of 128 (90 MB)                    25 - 30 us    3.0 - 3.6 TB/s
 //   1 row of 500 tokens, 8 heads on 1                                     8.8 us    latency
 // (one workgroup a row and head took 2108, 45, 105 and 12 us.) In the third of them planning takes 2.5 us, reading 15, and
 // the joins, where one compute unit reads up to 26 results, 5. A short call is a chain of trips to memory: lengths, table,

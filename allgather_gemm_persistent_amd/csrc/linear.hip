@@ -6,7 +6,7 @@
 // rows x columns x K, with a bf16 residual or a bias:
 //   16 x 10240 x 8192 bf16, streamed                     31.9 us    5.3 TB/s
 //   128 x 8192 x 8192 fp8, 128 x 64 tiles, K in two      25.6 us    2.7 TB/s (34 where nothing of the weight is cached)
-//   4096 x 8192 x 8192 bf16, 256 x 256 tiles             406 us     1354 TFLOP/s
+//   4096 x 8192 x 8192 bf16, 256 x 256 tiles             406 - 414 us    1328 - 1354 TFLOP/s
 //   777 x 1000 x 1032 bf16, GELU, 64 x 64 tiles          10.8 us    latency: 17 slices of K in turn
 // Between some 32 and 256 rows neither bound is near. Rows of B that are a multiple of 1024 bytes apart cost most (32 rows,
 // fp8, 128 x 64 tiles, nothing of the weight cached: 8192 columns 27.2 us, 8128 21.9, 6144, on fewer compute units, 27.2;

@@ -733,6 +733,7 @@ int kv_read(agg_ctx* ctx, const agg_kv_cache* cache, int64_t tokens, const int32
  *   out, out_dtype   AGG_BF16 or AGG_FP32 rows of q_heads * head_dim
  *   lse              fp32 [rows, q_heads] or NULL: with it, parts of a sequence that lie on several
  *                    ranks can be joined
+ * Values in places that count are finite: an infinite one gives a NaN in its channel.
  * Sums and maxima are fp32; the weights enter the matrix units as two bf16 parts each, 16 bits of them, for a
  * bf16 out, and as three, all of fp32, for an fp32 one. The length is split over workgroups and the parts are joined in
  * their order, so a result does not depend on timing; it may depend, in its last bits, on the other
@@ -766,7 +767,7 @@ enum { AGG_ACT_NONE = 0, AGG_ACT_RELU = 1, AGG_ACT_SILU = 2, AGG_ACT_GELU = 3, A
  * tiles or columns K is split over workgroups, whose sums meet in the ctx's workspace of the stream or capture
  * (see moe_gemm) and are added in part order; nothing depends on timing.
  * The fp8 matrix instructions add 8 products at a time after cutting each to multiples of 2^-13 of the
- * largest of them.
+ * largest of them (an fp32 out of 8192 random terms is 1.2e-5 of the norm off, of fp32 sums 6e-8).
  * Limits: k * elem, n * elem and n * 2 bytes multiples of 16, row strides of whole 16 bytes, A's 256
  * rows and B below 2 GiB.
  * Passage: section "The first move was to expose the overlap" (the GEMM that consumes what a collective
